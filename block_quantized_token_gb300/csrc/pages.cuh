@@ -1,0 +1,78 @@
+// The paged 4-bit K/V cache: where a row's codes and scales lie in the pool, and
+// the quantiser's steps.  A page of one KV head is page_rows / 16 tiles of 16
+// rows, one tile 18 * HD contiguous bytes (a multiple of 128: 2304 or 1152), so
+// that one bulk copy brings all that 16 rows need.
+//   K codes [16 rows][HD / 2 bytes]: word t * (HD / 32) + b of a row holds dims
+//     32 b + 8 t .. + 7, dim 2 i + e of those at bits 4 i + 16 e: a mask yields the
+//     fp16 pair (2 i, 2 i + 1), and lane t of a tensor-core quad finds its 8 dims of
+//     every block in HD / 32 consecutive words.
+//   V codes [HD / 64 q][8 g][4 t][4 u] words: dims 64 q + 16 u + g (low nibbles) and
+//     that + 8 (high nibbles) of rows 2 t + e + 8 i in byte i + 2 e: a mask yields the
+//     pair of rows (2 t, 2 t + 1) of one dim.  A byte belongs to one row, so rows
+//     written at the same time by different threads share none.
+//   K scales [16][HD / 32]; V scales [4 t][HD / 32][2 i][2 e].
+// Scales have 8 significant bits (rounded to bf16 first): d (c - 8) then has at
+// most 8 + 3 = 11, so every value is an fp16 number and enters the tensor cores
+// unrounded; (16 + c) d - 24 d is exact in one fp16 FMA because 24 d has at most
+// 8 + 2 bits and |d| <= 2720 keeps it finite.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace er {
+
+constexpr float PG_DMAX = 2720.f;
+
+__host__ __device__ constexpr int pg_tile_bytes(int hd) { return 18 * hd; }
+__host__ __device__ constexpr int pg_off_ks(int hd) { return 8 * hd; }
+__host__ __device__ constexpr int pg_off_v(int hd) { return 9 * hd; }
+__host__ __device__ constexpr int pg_off_vs(int hd) { return 17 * hd; }
+
+// byte of a tile that holds dims d and (V) d + 8 / (K) the code of dim d of row r; nibble: its bits
+__host__ __device__ inline int pg_k_word(int r, int w, int hd) { return r * (hd / 2) + 4 * w; }  // word w of row r
+__host__ __device__ inline int pg_v_byte(int r, int j, int hd) {  // byte of dims 16 (j / 8) + j % 8 and + 8, j < hd / 2
+    const int q = j >> 5, u = (j >> 3) & 3, g = j & 7, t = (r & 7) >> 1, e = r & 1, i = r >> 3;
+    (void)hd;
+    return ((((q * 8 + g) * 4 + t) * 4) + u) * 4 + i + 2 * e;
+}
+__host__ __device__ inline int pg_vs_half(int r, int b, int hd) {  // index of the V scale of (row r, block b)
+    return ((((r & 7) >> 1) * (hd / 32) + b) * 2 + (r >> 3)) * 2 + (r & 1);
+}
+
+// a slot's tile of KV head h
+ER_DEV uint8_t *pg_tile(uint8_t *pool, int page_rows, int KV, int hd, int slot, int h) {
+    const int page = slot / page_rows, in = slot - page * page_rows;
+    return pool + (((size_t)page * KV + h) * (page_rows >> 4) + (in >> 4)) * pg_tile_bytes(hd);
+}
+
+// fp16(bf16(-m / 8)) within +-PG_DMAX; NaN stays
+ER_DEV float pg_scale(float m) {
+    const float d = __bfloat162float(__float2bfloat16_rn(m * -0.125f));
+    if (isnan(d)) return d;
+    return __half2float(__float2half_rn(fminf(fmaxf(d, -PG_DMAX), PG_DMAX)));
+}
+ER_DEV int pg_code(float x, float d) {
+    if (!(d != 0.f) || isnan(d)) return 8;
+    return (int)fminf(fmaxf(roundf(x / d) + 8.f, 0.f), 15.f);
+}
+
+// one value of a row of `type` (ER_F32, ER_F16, ER_BF16) by its index
+template <class T>
+ER_DEV float pg_ld(const T *p);
+template <>
+ER_DEV float pg_ld<float>(const float *p) { return *p; }
+template <>
+ER_DEV float pg_ld<__half>(const __half *p) { return __half2float(*p); }
+template <>
+ER_DEV float pg_ld<__nv_bfloat16>(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+template <class T>
+ER_DEV T pg_cvt(float v);
+template <>
+ER_DEV float pg_cvt<float>(float v) { return v; }
+template <>
+ER_DEV __half pg_cvt<__half>(float v) { return __float2half_rn(v); }
+template <>
+ER_DEV __nv_bfloat16 pg_cvt<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+}  // namespace er

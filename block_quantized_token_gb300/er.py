@@ -16,8 +16,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liber.so")
 
 ER_OK, ER_EINVAL, ER_ENOMEM, ER_ECUDA, ER_EUNSUPPORTED, ER_EDEVICE = range(6)
-ER_F32, ER_F16, ER_Q4_0, ER_Q8_0 = 0, 1, 2, 8
-DTYPES = {"f32": ER_F32, "f16": ER_F16, "q4_0": ER_Q4_0, "q8_0": ER_Q8_0}
+ER_F32, ER_F16, ER_Q4_0, ER_Q8_0, ER_BF16 = 0, 1, 2, 8, 30
+DTYPES = {"f32": ER_F32, "f16": ER_F16, "q4_0": ER_Q4_0, "q8_0": ER_Q8_0, "bf16": ER_BF16}
+ER_ROPE_PAIRS, ER_ROPE_HALVES = 0, 1
 ER_SCHEDULE_AUTO, ER_SCHEDULE_PERSISTENT, ER_SCHEDULE_KERNELS = 0, 1, 2
 ER_WIDE_AUTO, ER_WIDE_MMA_SYNC, ER_WIDE_TCGEN05 = 0, 1, 2
 (ER_STAGE_EMBED, ER_STAGE_QKV, ER_STAGE_ATTN, ER_STAGE_WO, ER_STAGE_GATEUP, ER_STAGE_DOWN,
@@ -45,6 +46,31 @@ class er_layer_weights(ctypes.Structure):
 class er_weights(ctypes.Structure):
     _fields_ = [("tok_embd", ctypes.c_void_p), ("output_norm", ctypes.c_void_p), ("output", ctypes.c_void_p),
                 ("layers", ctypes.POINTER(er_layer_weights))]
+
+
+def _struct(**fields):
+    """Field list of a C struct from type -> names, in order."""
+    return [(n, getattr(ctypes, t.rstrip("_"))) for t, names in fields.items() for n in names.split()]
+
+
+class er_pages_config(ctypes.Structure):
+    _fields_ = _struct(c_int32="n_layers n_pages page_rows n_kv_heads head_dim kv_type")
+
+
+class er_pages_plan_args(ctypes.Structure):
+    _fields_ = _struct(c_int32="n_seqs max_tokens table_stride",
+                       c_void_p="lens new_ free free_count tables lens_out free_count_out q_start positions slots seqs")
+
+
+class er_pages_append_args(ctypes.Structure):
+    _fields_ = _struct(c_int32="n_tokens n_heads type rope_style rope_positions", c_void_p="q k v q_out",
+                       c_int64="q_stride k_stride v_stride q_out_stride",
+                       c_void_p_="q_gain k_gain rope positions slots", c_float="eps")
+
+
+class er_pages_attention_args(ctypes.Structure):
+    _fields_ = _struct(c_int32="n_seqs n_tokens n_heads type table_stride window", c_void_p="q out lse",
+                       c_int64="q_stride out_stride", c_void_p_="q_start lens tables", c_float="scale")
 
 
 def _load() -> ctypes.CDLL:
@@ -85,6 +111,16 @@ def _load() -> ctypes.CDLL:
         "er_set_wait_limit_ns": (I32, [ctypes.c_uint64]),
         "er_debug_fail_allocation": (I32, [ctypes.c_int64]),
         "er_debug_live_allocations": (ctypes.c_int64, []),
+        "er_pages_pool_bytes": (ctypes.c_size_t, [P(er_pages_config)]),
+        "er_pages_create": (I32, [P(er_pages_config), VP, P(VP)]),
+        "er_pages_destroy": (None, [VP]),
+        "er_pages_plan": (I32, [VP, P(er_pages_plan_args), VP]),
+        "er_pages_release": (I32, [VP, I32, VP, VP, VP, I32, VP, VP, VP]),
+        "er_rope_table": (I32, [I32, ctypes.c_double, I32, VP, VP]),
+        "er_pages_append": (I32, [VP, I32, P(er_pages_append_args), VP]),
+        "er_pages_read": (I32, [VP, I32, I32, VP, I32, VP, VP, VP]),
+        "er_pages_attention": (I32, [VP, I32, P(er_pages_attention_args), VP]),
+        "er_pages_error": (I32, [VP, P(I32)]),
         "er_gguf_open": (I32, [ctypes.c_char_p, P(VP)]),
         "er_gguf_close": (None, [VP]),
         "er_gguf_tensor_count": (ctypes.c_int64, [VP]),
@@ -112,7 +148,9 @@ EXPORTED = ("er_model_create", "er_model_destroy", "er_model_device_bytes", "er_
             "er_kv_launches_per_step", "er_kv_cached_graphs", "er_kv_inject_wait_shortfall", "er_set_wait_limit_ns",
             "er_debug_fail_allocation", "er_debug_live_allocations", "er_gguf_open", "er_gguf_close",
             "er_gguf_tensor_count", "er_gguf_tensor_info", "er_gguf_find", "er_gguf_config",
-            "er_model_create_from_gguf", "er_kv_create_typed", "er_kv_type", "er_kv_read_blocks", "er_prefill", "er_status_str",
+            "er_model_create_from_gguf", "er_kv_create_typed", "er_kv_type", "er_kv_read_blocks", "er_prefill", "er_pages_pool_bytes",
+            "er_pages_create", "er_pages_destroy", "er_pages_plan", "er_pages_release", "er_rope_table",
+            "er_pages_append", "er_pages_read", "er_pages_attention", "er_pages_error", "er_status_str",
             "er_last_error")
 
 
@@ -287,6 +325,56 @@ def er_debug_fail_allocation(n: int) -> None:
 
 def er_debug_live_allocations() -> int:
     return int(_lib.er_debug_live_allocations())
+
+
+def er_pages_pool_bytes(cfg: er_pages_config) -> int:
+    return int(_lib.er_pages_pool_bytes(ctypes.byref(cfg)))
+
+
+def er_pages_create(cfg: er_pages_config, pool: int | None) -> int:
+    out = ctypes.c_void_p()
+    _check(_lib.er_pages_create(ctypes.byref(cfg), pool, ctypes.byref(out)), "er_pages_create")
+    return out.value
+
+
+def er_pages_destroy(pages: int) -> None:
+    _lib.er_pages_destroy(pages)
+
+
+def er_pages_plan(pages: int, args: er_pages_plan_args, stream: int = 0) -> None:
+    _check(_lib.er_pages_plan(pages, args, stream), "er_pages_plan")
+
+
+def er_pages_release(pages: int, n_seqs: int, done: int, lens: int, tables: int, table_stride: int, free: int,
+                     free_count: int, stream: int = 0) -> None:
+    _check(_lib.er_pages_release(pages, n_seqs, done, lens, tables, table_stride, free, free_count, stream),
+           "er_pages_release")
+
+
+def er_rope_table(head_dim: int, base: float, n_positions: int, out: int, stream: int = 0) -> None:
+    _check(_lib.er_rope_table(head_dim, base, n_positions, out, stream), "er_rope_table")
+
+
+def er_pages_append(pages: int, layer: int, args: er_pages_append_args, stream: int = 0) -> None:
+    _check(_lib.er_pages_append(pages, layer, args, stream), "er_pages_append")
+
+
+def er_pages_read(pages: int, layer: int, n: int, slots: int | None, type: int, k_out: int | None, v_out: int | None,
+                  stream: int = 0) -> None:
+    _check(_lib.er_pages_read(pages, layer, n, slots, type, k_out, v_out, stream), "er_pages_read")
+
+
+def er_pages_attention(pages: int, layer: int, args: er_pages_attention_args, stream: int = 0) -> None:
+    _check(_lib.er_pages_attention(pages, layer, args, stream), "er_pages_attention")
+
+
+def er_pages_error(pages: int) -> tuple[int, int]:
+    """Returns (status, code) without raising on ER_EDEVICE."""
+    code = ctypes.c_int32()
+    st = _lib.er_pages_error(pages, ctypes.byref(code))
+    if st not in (ER_OK, ER_EDEVICE):
+        _check(st, "er_pages_error")
+    return st, code.value
 
 
 def er_gguf_open(path: str) -> int:

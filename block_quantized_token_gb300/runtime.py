@@ -159,3 +159,173 @@ class DecodeState:
 
     def __del__(self):
         self.close()
+
+
+_ROW_TYPES = {torch.float32: er.ER_F32, torch.float16: er.ER_F16, torch.bfloat16: er.ER_BF16}
+_ROPE_STYLES = {"pairs": er.ER_ROPE_PAIRS, "halves": er.ER_ROPE_HALVES}
+
+
+def rope_table(head_dim: int, base: float, n_positions: int, device: str = "cuda") -> torch.Tensor:
+    """(cos, sin) of p * base^(-2 i / head_dim), fp32 [n_positions, head_dim / 2, 2], made on the device."""
+    out = torch.empty((n_positions, head_dim // 2, 2), dtype=torch.float32, device=device)
+    er.er_rope_table(head_dim, base, n_positions, out.data_ptr(), torch.cuda.current_stream(out.device).cuda_stream)
+    return out
+
+
+class PagedCache:
+    """Owns an er_pages handle and, unless given, its pool: a paged 4-bit K/V cache (er_pages_* in er.h).
+
+    Row tensors are [tokens, heads, head_dim] with dense heads and any stride between tokens; int tensors are dense
+    int32; all on the cache's device.
+    """
+
+    def __init__(self, n_layers: int, n_pages: int, page_rows: int, n_kv_heads: int, head_dim: int,
+                 pool: torch.Tensor | None = None, device: str = "cuda"):
+        self.n_kv_heads, self.head_dim = n_kv_heads, head_dim
+        self.cfg = er.er_pages_config(n_layers, n_pages, page_rows, n_kv_heads, head_dim, er.ER_Q4_0)
+        need = er.er_pages_pool_bytes(self.cfg)
+        if not need:
+            er.er_pages_create(self.cfg, None)  # raises with the reason
+        if pool is None:
+            pool = torch.empty(need, dtype=torch.uint8, device=device)
+        if not pool.is_cuda or not pool.is_contiguous() or pool.numel() * pool.element_size() != need:
+            raise ValueError(f"pool must be a dense CUDA tensor of {need} bytes")
+        self.pool, self.device = pool, pool.device
+        with torch.cuda.device(self.device):
+            self.handle = er.er_pages_create(self.cfg, pool.data_ptr())
+
+    def _stream(self, stream: int | None) -> int:
+        return torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
+
+    def _ints(self, n: int, *tensors: torch.Tensor) -> None:
+        for t in tensors:
+            if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n or t.device != self.device:
+                raise ValueError(f"a dense int32 tensor of {n} values on {self.device} is needed")
+
+    def _rows(self, x: torch.Tensor, n: int, heads: int | None, dtype: torch.dtype | None) -> int:
+        """Checks row tensors [n, heads, head_dim]; returns the stride between tokens."""
+        if x.dim() != 3 or x.shape[2] != self.head_dim or (heads is not None and x.shape[1] != heads):
+            raise ValueError(f"rows must be [tokens, heads, {self.head_dim}]")
+        st = x.stride()
+        if x.shape[0] < n or x.device != self.device or (dtype is not None and x.dtype != dtype) or st[2] != 1 or \
+                (x.shape[1] > 1 and st[1] != self.head_dim):
+            raise ValueError(f"rows must be {n} dense heads' rows of one type on {self.device}")
+        if x.dtype not in _ROW_TYPES:
+            raise ValueError("rows must be float32, float16 or bfloat16")
+        return st[0] if x.shape[0] > 1 else x.shape[1] * self.head_dim
+
+    def _table(self, tables: torch.Tensor, n_seqs: int) -> int:
+        self._ints(0, tables)
+        if tables.dim() != 2 or tables.shape[0] < n_seqs:
+            raise ValueError("tables must be [sequences, pages]")
+        return tables.shape[1]
+
+    def plan(self, lens: torch.Tensor, new: torch.Tensor, tables: torch.Tensor, free: torch.Tensor,
+             free_count: torch.Tensor, lens_out: torch.Tensor, free_count_out: torch.Tensor, q_start: torch.Tensor,
+             positions: torch.Tensor, slots: torch.Tensor, seqs: torch.Tensor, stream: int | None = None) -> None:
+        """Pages, positions and slots of a step in which request b brings new[b] tokens (er_pages_plan)."""
+        n, rows = lens.numel(), slots.numel()
+        self._ints(n, lens, new, lens_out)
+        self._ints(rows, positions, slots, seqs)
+        self._ints(n + 1, q_start)
+        self._ints(1, free_count, free_count_out)
+        self._ints(self.cfg.n_pages, free)
+        a = er.er_pages_plan_args(n, rows, self._table(tables, n), lens.data_ptr(), new.data_ptr(), free.data_ptr(),
+                                  free_count.data_ptr(), tables.data_ptr(), lens_out.data_ptr(),
+                                  free_count_out.data_ptr(), q_start.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+                                  seqs.data_ptr())
+        er.er_pages_plan(self.handle, a, self._stream(stream))
+
+    def release(self, done: torch.Tensor, lens: torch.Tensor, tables: torch.Tensor, free: torch.Tensor,
+                free_count: torch.Tensor, stream: int | None = None) -> None:
+        """Gives the pages of the requests with done[b] != 0 back to the free list (er_pages_release)."""
+        n = lens.numel()
+        self._ints(n, done, lens)
+        self._ints(1, free_count)
+        self._ints(self.cfg.n_pages, free)
+        er.er_pages_release(self.handle, n, done.data_ptr(), lens.data_ptr(), tables.data_ptr(),
+                            self._table(tables, n), free.data_ptr(), free_count.data_ptr(), self._stream(stream))
+
+    def append(self, layer: int, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+               positions: torch.Tensor | None, slots: torch.Tensor, q_out: torch.Tensor | None = None,
+               q_gain: torch.Tensor | None = None, k_gain: torch.Tensor | None = None, eps: float = 1e-5,
+               rope: torch.Tensor | None = None, rope_style: str = "pairs", stream: int | None = None) -> None:
+        """Norms and rotates q and k, writes q_out and puts k and v into their slots (er_pages_append)."""
+        n, hd = k.shape[0], self.head_dim
+        ks, vs = self._rows(k, n, self.n_kv_heads, None), self._rows(v, n, self.n_kv_heads, k.dtype)
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out go together")
+        qs = os_ = heads = 0
+        if q is not None:
+            heads = q.shape[1]
+            qs, os_ = self._rows(q, n, heads, k.dtype), self._rows(q_out, n, heads, k.dtype)
+        self._ints(n, slots)
+        for g in (q_gain, k_gain):
+            if g is not None and (g.dtype != torch.float32 or g.numel() != hd or not g.is_contiguous() or
+                                  g.device != self.device):
+                raise ValueError(f"a gain must be {hd} float32 values")
+        if rope is not None:
+            if rope.dtype != torch.float32 or not rope.is_contiguous() or rope.device != self.device or \
+                    rope.dim() != 3 or tuple(rope.shape[1:]) != (hd // 2, 2):
+                raise ValueError(f"the rope table must be float32 [positions, {hd // 2}, 2]")
+            if positions is None:
+                raise ValueError("a rope table needs positions")
+            self._ints(n, positions)
+        if rope_style not in _ROPE_STYLES:
+            raise ValueError(f"rope_style must be one of {sorted(_ROPE_STYLES)}")
+
+        def ptr(t):
+            return None if t is None else t.data_ptr()
+
+        a = er.er_pages_append_args(n, heads, _ROW_TYPES[k.dtype], _ROPE_STYLES[rope_style],
+                                    0 if rope is None else rope.shape[0], ptr(q), k.data_ptr(), v.data_ptr(), ptr(q_out),
+                                    qs, ks, vs, os_, ptr(q_gain), ptr(k_gain), ptr(rope),
+                                    None if rope is None else positions.data_ptr(), slots.data_ptr(), eps)
+        er.er_pages_append(self.handle, layer, a, self._stream(stream))
+
+    def read(self, layer: int, slots: torch.Tensor, k_out: torch.Tensor | None, v_out: torch.Tensor | None,
+             stream: int | None = None) -> None:
+        """Values of the rows at `slots` into dense k_out / v_out [n, n_kv_heads, head_dim] (er_pages_read)."""
+        n = slots.numel()
+        self._ints(n, slots)
+        dtype = None
+        for t in (k_out, v_out):
+            if t is not None:
+                if not t.is_contiguous():
+                    raise ValueError("k_out and v_out must be dense")
+                self._rows(t, n, self.n_kv_heads, dtype)
+                dtype = t.dtype
+        if dtype is None:
+            return
+        er.er_pages_read(self.handle, layer, n, slots.data_ptr(), _ROW_TYPES[dtype],
+                         None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
+                         self._stream(stream))
+
+    def attention(self, layer: int, q: torch.Tensor, out: torch.Tensor, q_start: torch.Tensor, lens: torch.Tensor,
+                  tables: torch.Tensor, scale: float = 0.0, window: int = 0, lse: torch.Tensor | None = None,
+                  stream: int | None = None) -> None:
+        """Attention of rows q_start[b] .. q_start[b + 1] - 1 of q over sequence b's lens[b] cached rows
+        (er_pages_attention)."""
+        n, heads, seqs = q.shape[0], q.shape[1], lens.numel()
+        qs, os_ = self._rows(q, n, heads, None), self._rows(out, n, heads, q.dtype)
+        self._ints(seqs, lens)
+        self._ints(seqs + 1, q_start)
+        if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != self.device or
+                                lse.numel() < n * heads):
+            raise ValueError("lse must be dense float32 [tokens, heads]")
+        a = er.er_pages_attention_args(seqs, n, heads, _ROW_TYPES[q.dtype], self._table(tables, seqs), window,
+                                       q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), qs, os_,
+                                       q_start.data_ptr(), lens.data_ptr(), tables.data_ptr(), scale)
+        er.er_pages_attention(self.handle, layer, a, self._stream(stream))
+
+    def error(self) -> tuple[int, int]:
+        """(status, flags) of the calls so far; synchronises (er_pages_error)."""
+        return er.er_pages_error(self.handle)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            er.er_pages_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        self.close()
