@@ -222,8 +222,10 @@ cudaError_t launch_rope_table(int hd, double base, int n, float *out, cudaStream
 cudaError_t launch_pages_append(const PagesView &p, const er_pages_append_args &a, int num_sms, cudaStream_t st);
 cudaError_t launch_pages_read(const PagesView &p, int n, const int32_t *slots, int type, void *k, void *v,
                               cudaStream_t st);
-cudaError_t launch_pages_attention(const PagesView &p, const er_pages_attention_args &a, int num_sms,
-                                   cudaStream_t st);
+cudaError_t launch_pages_attention(const PagesView &p, const er_pages_attention_args &a, float *part, int *cnt,
+                                   int num_sms, cudaStream_t st);
+size_t pages_attn_part_floats(int num_sms);  // `part`; cnt: one int per SM, zero
+cudaError_t pages_attn_prepare();            // kernel attributes
 
 // one device allocation outside any owner list, counted and failure-injectable like the library's own
 cudaError_t device_alloc(void **p, size_t bytes);
@@ -236,6 +238,7 @@ cudaError_t set_wait_limit_tc(unsigned long long ns);
 cudaError_t set_wait_limit_step_q8(unsigned long long ns);
 cudaError_t set_wait_limit_step_q4(unsigned long long ns);
 cudaError_t set_wait_limit_attn(unsigned long long ns);
+cudaError_t set_wait_limit_pages(unsigned long long ns);
 
 }  // namespace er
 
@@ -262,6 +265,8 @@ struct er_pages {
     int device, num_sms;
     int *flags;   // er_pages_error
     int *ticket;  // arrival counter of the plan kernel (zero between launches)
+    int *cnt;     // arrival counters of the attention kernel [SMs] (zero between launches)
+    float *part;  // states of units shared by several CTAs (pages_attn_part_floats)
 };
 
 struct er_layer_dev {

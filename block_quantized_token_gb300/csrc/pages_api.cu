@@ -72,15 +72,21 @@ er_status er_pages_create(const er_pages_config *cfg, void *pool, er_pages **out
     p->cfg = *cfg;
     p->pool = (uint8_t *)pool;
     p->layer_bytes = layer_bytes(cfg);
-    p->flags = p->ticket = nullptr;
+    p->flags = p->ticket = p->cnt = nullptr;
+    p->part = nullptr;
     cudaError_t e = cudaGetDevice(&p->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device);
+    if (e == cudaSuccess) e = pages_attn_prepare();
+    // one block: flags, ticket, counters (zero), then the attention kernel's states
+    const size_t ints = (128 + (size_t)(p->num_sms + 63) / 64 * 64) * sizeof(int);
     void *q = nullptr;
-    if (e == cudaSuccess) e = device_alloc(&q, 2 * 256);
+    if (e == cudaSuccess) e = device_alloc(&q, ints + pages_attn_part_floats(p->num_sms) * sizeof(float));
     if (e == cudaSuccess) {
         p->flags = (int *)q;
         p->ticket = p->flags + 64;
-        e = cudaMemset(q, 0, 2 * 256);
+        p->cnt = p->flags + 128;
+        p->part = (float *)((uint8_t *)q + ints);
+        e = cudaMemset(q, 0, ints);
     }
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
@@ -185,7 +191,7 @@ er_status er_pages_attention(er_pages *p, int32_t layer, const er_pages_attentio
         return er_fail_status(ER_EINVAL, "rows must be aligned to their type");
     if (a->out_dev == a->q_dev && a->out_stride != a->q_stride)
         return er_fail_status(ER_EINVAL, "out may be q only with the same stride");
-    return done(launch_pages_attention(view_of(p, layer), *a, p->num_sms, (cudaStream_t)stream), "er_pages_attention");
+    return done(launch_pages_attention(view_of(p, layer), *a, p->part, p->cnt, p->num_sms, (cudaStream_t)stream), "er_pages_attention");
 }
 
 er_status er_pages_error(er_pages *p, int32_t *code) {
@@ -195,6 +201,8 @@ er_status er_pages_error(er_pages *p, int32_t *code) {
     int f = 0;
     if (e == cudaSuccess) e = cudaMemcpy(&f, p->flags, sizeof(int), cudaMemcpyDeviceToHost);
     if (e == cudaSuccess) e = cudaMemset(p->flags, 0, sizeof(int));
+    // a kernel that gave up may have left its arrival counters short
+    if (e == cudaSuccess && (f & ER_FLAG_WAIT)) e = cudaMemset(p->cnt, 0, (size_t)p->num_sms * sizeof(int));
     if (e != cudaSuccess) return er_fail_cuda(e, "er_pages_error");
     *code = f & (ER_PAGES_FLAG_FULL | ER_PAGES_FLAG_RANGE | ER_FLAG_WAIT);
     return *code ? er_fail_status(ER_EDEVICE, "device flags set") : ER_OK;
