@@ -4,9 +4,8 @@
 // rescaled by 2^(m - m') when a score passes m by more than 8 (so p <= 2^15, an fp16 number, and most tiles skip the
 // rescale).
 //
-// What bounds it: the cache's bytes (18 / 32 a value); next, instructions: two a value to turn codes into fp16 pairs
-// and feed the tensor cores, so a tile's codes are laid out as the fragments take them and a mask and one FMA yield
-// a pair.
+// What bounds it: the cache's bytes (18 / 32 a value); next, instructions, two a value to turn codes into operands
+// and feed the tensor cores, so a tile's codes are laid out as the operands take them.
 //
 // Work split.  A unit is a (sequence, group of 8 query rows, KV head); a query row is a (token, head of the KV
 // head's group).  The 16-row tiles that the units attend form one list in order of unit; CTA c of C takes the
@@ -19,54 +18,66 @@
 // each slot with its mbarrier; the table entries of the next 32 tiles are held a lane each, so no copy waits for a
 // table.
 //
-// Arithmetic per tile (mma.sync m16n8k16, fp32 sums): A = the 8 query rows, rows 0..7 their hi fp16 half and 8..15 the lo
-// half (q = hi + lo to 2^-22 of the row's largest); B = K.  The accumulators' hi and lo rows sit in one lane, which adds
-// them.  The scores' layout is the A layout of P V; p = hi + lo again; B = V.  Cached values are fp16 numbers
-// (pages.cuh), so the only rounding next to fp32's is those 2^-22.
-//
+// Arithmetic per tile (mma.sync, fp32 sums), the cached side as the A operand, the 8 query rows as B's columns:
+//   S^T = K Q^T in fp8 (m16n8k32): a 4-bit code c is, as it stands in a byte, the e4m3 number c 2^-9, so two masks
+//         and a shift make 8 codes an operand.  Queries are cut into e4m3 pieces of 4 bits (bf16: 2, exact; fp16: 3,
+//         exact; fp32: 5, the last two with a scale of their own, 2^-20 of the row's largest).  Sums of such products
+//         are exact in fp32 (measured: equal to 64-bit sums).  One instruction is one 32-value block: its sum minus
+//         8 sum q (the accumulator's start) times the row's scale goes to the score.
+//   O^T += V^T P^T in fp16 (m16n8k16): one code word is a lane's whole A operand, a mask and one FMA a pair, exact
+//         (pages.cuh).  Probabilities go from the scores' layout to B's by movmatrix, as hi + lo halves
+//         (2^-22; bf16 outputs: hi alone, 2^-11).
 // Masks.  Tiles that some row of the unit attends only in part go through a path that masks scores and zeroes the
 // scales of rows nobody attends (they may hold anything); a NaN value that only some of the unit's tokens attend
 // is carried by their scores instead.
+#include <type_traits>
+
 #include "internal.h"
 #include "pages.cuh"
 
 namespace er {
 
-constexpr int PD_WARPS = 12;
+// 8 warps of up to 255 registers: 12 of 168 spill (fp32: 93 us against 72 for 16 x 8192, bf16 55 against 54)
+constexpr int PD_WARPS = 8;
 constexpr int PD_THREADS = PD_WARPS * 32;
-constexpr int PD_SLOTS = 5;
+constexpr int PD_SLOTS = 4;    // steps in a warp's ring
+constexpr int PD_STEP = 32;      // rows of a step: two tiles
 constexpr int PD_ROWS = 8;       // query rows of a unit
-constexpr int PD_MIN_TILES = 4;  // tiles of a CTA at least
+constexpr int PD_SEQS = 512;     // sequences of a launch (more: several launches)
+constexpr int PD_MIN_STEPS = 2;  // steps of a CTA at least
 constexpr float PD_UP = 7.f;     // p = 2^(s - m + PD_UP)
 constexpr float PD_SLACK = 8.f;  // scores may pass m by this much
+constexpr float PD_NONE = -3e38f;  // m before any score
 
+struct PdSeq {  // a sequence: its rows of q, its length, its steps (-1: rows with nothing to attend)
+    int q0, qn, len, ns;
+};
 template <int HD>
 struct PdCfg {
     static constexpr int TILE = pg_tile_bytes(HD);
     static constexpr int NB = HD / 32;               // 32-dim blocks
-    static constexpr int NTD = HD / 8;               // n8 tiles of P V
     static constexpr int STATE = PD_ROWS * HD + 16;  // floats of a state: o [8][HD], m [8], l [8]
-    static constexpr int RING = PD_SLOTS * TILE;     // a warp's; later its last segment's state
+    static constexpr int RING = PD_SLOTS * 2 * TILE; // a warp's; later its last segment's state
     static constexpr int OFF_FIRST = PD_WARPS * RING;
     static constexpr int OFF_W = OFF_FIRST + PD_WARPS * STATE * 4;
-    static constexpr int OFF_NT = OFF_W + (ER_PAGES_MAX_SEQS + 1) * 8;
-    static constexpr int OFF_T0 = OFF_NT + ER_PAGES_MAX_SEQS * 4;
-    static constexpr int OFF_BARS = OFF_T0 + ER_PAGES_MAX_SEQS * 4 + 8;
+    static constexpr int OFF_SEQ = OFF_W + (PD_SEQS + 2) * 8;
+    static constexpr int OFF_BARS = OFF_SEQ + PD_SEQS * (int)sizeof(PdSeq);
     static constexpr int OFF_MISC = OFF_BARS + PD_WARPS * PD_SLOTS * 8;
     static constexpr int SMEM = OFF_MISC + 2048;
-    static_assert(RING >= STATE * 4 && OFF_W % 8 == 0 && OFF_BARS % 8 == 0, "shared memory layout");
+    static_assert(RING >= STATE * 4 && OFF_W % 8 == 0 && OFF_BARS % 8 == 0 && SMEM <= 232448, "shared memory layout");
 };
 
 // a piece of a unit that some warp holds as a state
 struct PdSeg {
-    long long u0, u1;  // the unit's tiles in the list
+    long long u0, u1;  // the unit's steps in the list
     int b, rg, h;
     int off;  // byte offset of the state in shared memory, -1: none
 };
 struct PdMisc {
     PdSeg seg[2 * PD_WARPS];
     long long wsum[PD_WARPS];
-    int run[2 * PD_WARPS + 1];
+    int run[2 * PD_WARPS + 1];  // first of each run in ent
+    short ent[2 * PD_WARPS];    // the states that there are, in list order
     int n_runs;
     int wait_bad;
     int last[2];
@@ -77,7 +88,6 @@ ER_DEV float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-ER_DEV uint32_t h2_dup(uint32_t h2, int hi) { return prmt(h2, h2, hi ? 0x3232u : 0x1010u); }
 ER_DEV uint32_t h2_mul(uint32_t a, uint32_t b) {
     __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
     return *reinterpret_cast<uint32_t *>(&r);
@@ -97,6 +107,61 @@ ER_DEV uint32_t pd_code(uint32_t w) {
     return lop3_and_or(N == 0 ? w << 6 : N == 1 ? w << 2 : N == 2 ? w >> 2 : w >> 6, 0x03C003C0u, 0x4C004C00u);
 }
 constexpr uint32_t PD_M24 = 0xCE00CE00u;  // half2(-24, -24)
+// d += A B without volatile: the compiler may move it between the loads and conversions of other tiles
+ER_DEV void pd_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// d += A B over 8 k, fp16
+ER_DEV void pd_mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b));
+}
+// d = A B + c, e4m3
+ER_DEV void pd_mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+// the 8x8 transpose of a packed pair matrix
+ER_DEV uint32_t pd_trans(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// e4m3 of (a, b), a in the low byte, and their values taken off a and b and added to sum
+ER_DEV uint32_t pd_piece(float &a, float &b, float &sum) {
+    uint16_t p;
+    uint32_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(b), "f"(a));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    a -= v.x;
+    b -= v.y;
+    sum += v.x + v.y;
+    return p;
+}
+template <class T>
+struct PdType;  // pieces of a query value in two scales (the second 2^-PD_SUB of the first); whether p is hi + lo
+template <>
+struct PdType<float> {
+    static constexpr int NA = 3, NB = 2;
+    static constexpr bool SPLIT = true;
+};
+template <>
+struct PdType<__half> {
+    static constexpr int NA = 3, NB = 0;
+    static constexpr bool SPLIT = true;
+};
+template <>
+struct PdType<__nv_bfloat16> {
+    static constexpr int NA = 2, NB = 0;
+    static constexpr bool SPLIT = false;
+};
+constexpr int PD_SUB = 11;
 
 struct PdArgs {
     PagesView p;
@@ -104,6 +169,16 @@ struct PdArgs {
     float *part;  // [CTAs][2] states of units that several CTAs share
     int *cnt;     // [CTAs] arrivals, zero between launches
 };
+
+// the first row that any of a sequence's qn new tokens attends
+ER_DEV int pd_row0(int len, int qn, int window) { return window ? max(0, len - qn - window + 1) : 0; }
+// x / d for x >= 0, mostly below 2^32
+ER_DEV long long pd_div(long long x, int d) {
+    return (x >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)d) : x / d;
+}
+
+// the CTA of list entry i: the c with c N / C <= i < (c + 1) N / C
+ER_DEV int pd_cta(long long i, long long N, int C) { return (int)(((i + 1) * C - 1) / N); }
 
 // query row r of group rg of sequence b, KV head h: its token's row in q / out and its head
 ER_DEV void pd_row(int r, int rg, int G, int q0, int h, int &row, int &head, int &i) {
@@ -116,9 +191,10 @@ ER_DEV void pd_row(int r, int rg, int G, int q0, int h, int &row, int &head, int
 template <class T, int HD>
 __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArgs P) {
     using C = PdCfg<HD>;
+    using Y = PdType<T>;
     extern __shared__ __align__(128) uint8_t smem[];
     long long *W = reinterpret_cast<long long *>(smem + C::OFF_W);
-    int *NT = reinterpret_cast<int *>(smem + C::OFF_NT), *T0 = reinterpret_cast<int *>(smem + C::OFF_T0);
+    PdSeq *SQ = reinterpret_cast<PdSeq *>(smem + C::OFF_SEQ);
     PdMisc &ms = *reinterpret_cast<PdMisc *>(smem + C::OFF_MISC);
     static_assert(sizeof(PdMisc) <= 2048, "misc");
     const er_pages_attention_args &a = P.a;
@@ -133,7 +209,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
 
     // ---- the list: tiles of every sequence, prefix sums in W
     {
-        constexpr int PER = (ER_PAGES_MAX_SEQS + PD_THREADS - 1) / PD_THREADS;
+        constexpr int PER = (PD_SEQS + PD_THREADS - 1) / PD_THREADS;
         const int per = (a.n_seqs + PD_THREADS - 1) / PD_THREADS;
         long long own[PER], sum = 0;
 #pragma unroll
@@ -142,21 +218,18 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
             const int b = tid * per + k;
             if (k < per && b < a.n_seqs) {
                 const int q0 = a.q_start_dev[b], q1 = a.q_start_dev[b + 1], len = a.lens_dev[b];
-                int nt = 0, t0 = 0;
+                int ns = 0;
                 const bool bad = q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 ||
                                  (long long)len > (long long)a.table_stride * R;
                 if (bad) {
                     if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
                 } else if (q1 > q0 && len > 0) {
-                    const int lo = a.window ? max(0, len - (q1 - q0) - a.window + 1) : 0;
-                    t0 = lo >> 4;
-                    nt = ((len - 1) >> 4) - t0 + 1;
-                    own[k] = (long long)nt * ((((long long)(q1 - q0) * G + PD_ROWS - 1) / PD_ROWS) * KV);
+                    ns = (len - 1) / PD_STEP - pd_row0(len, q1 - q0, a.window) / PD_STEP + 1;
+                    own[k] = (long long)ns * ((((long long)(q1 - q0) * G + PD_ROWS - 1) / PD_ROWS) * KV);
                 } else if (q1 > q0) {
-                    nt = -1;  // rows without anything to attend: zeros, below
+                    ns = -1;
                 }
-                NT[b] = nt;
-                T0[b] = t0;
+                SQ[b] = {q0, q1 - q0, len, ns};
             }
             sum += own[k];
         }
@@ -183,9 +256,9 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
     }
     // sequences of length 0: zeros and -infinity
     for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
-        if (NT[b] != -1) continue;
-        const int q0 = a.q_start_dev[b];
-        const long long n = (long long)(a.q_start_dev[b + 1] - q0) * a.n_heads;
+        if (SQ[b].ns != -1) continue;
+        const int q0 = SQ[b].q0;
+        const long long n = (long long)SQ[b].qn * a.n_heads;
         for (long long i = tid; i < n * HD; i += PD_THREADS) {
             const int row = q0 + (int)(i / HD / a.n_heads), head = (int)(i / HD % a.n_heads);
             ((T *)a.out_dev)[row * a.out_stride + (size_t)head * HD + i % HD] = pg_cvt<T>(0.f);
@@ -195,10 +268,10 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
     }
     const long long N = W[a.n_seqs];
     if (N == 0) return;
-    const long long C_ = min((long long)gridDim.x, (N + PD_MIN_TILES - 1) / PD_MIN_TILES);
-    if ((long long)blockIdx.x >= C_) return;
-    const long long c0 = blockIdx.x * N / C_, c1 = (blockIdx.x + 1) * N / C_;
-    const long long w0 = c0 + warp * (c1 - c0) / PD_WARPS, w1 = c0 + (warp + 1) * (c1 - c0) / PD_WARPS;
+    const int C_ = (int)min((long long)gridDim.x, (N + PD_MIN_STEPS - 1) / PD_MIN_STEPS);
+    if ((int)blockIdx.x >= C_) return;
+    const long long c0 = pd_div(blockIdx.x * N, C_), c1 = pd_div((blockIdx.x + 1) * N, C_);
+    const long long w0 = c0 + pd_div(warp * (c1 - c0), PD_WARPS), w1 = c0 + pd_div((warp + 1) * (c1 - c0), PD_WARPS);
 
     auto seq_of = [&](long long i) {  // the sequence of list entry i: the last b with W[b] <= i (empty ones are skipped)
         int lo = 0, hi = a.n_seqs - 1;
@@ -209,281 +282,426 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
         }
         return lo;
     };
-    // where list entry i lies in the pool
-    auto source = [&](long long i) -> unsigned long long {
-        if (i >= w1) return 0;
-        const int b = seq_of(i), nt = NT[b];
-        const long long rem = i - W[b], unit = rem / nt;
-        const int row = (T0[b] + (int)(rem - unit * nt)) << 4, h = (int)(unit % KV);
-        const int blk = row / R;
-        int page = a.tables_dev[(size_t)b * a.table_stride + blk];
-        if (page < 0 || page >= P.p.n_pages) {
-            atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
-            page = 0;
-        }
-        return (((unsigned long long)page * KV + h) * (R >> 4) + ((row - blk * R) >> 4)) * C::TILE;
+    const int cnt = (int)(w1 - w0);  // this warp's steps
+    struct Unit {
+        long long u0, u1;
+        int q0, qn, len, rg, h, b;
     };
-    long long ibase = w0, inext = w0;  // entries ibase .. + 31 are in cur, the 32 after them in nxt; next to request
-    unsigned long long cur = source(w0 + lane), nxt = source(w0 + 32 + lane);
-    auto issue = [&]() {  // requests the next tile (whole warp)
-        if (inext >= w1) return;
-        if (inext - ibase == 32) {
-            ibase += 32;
-            cur = nxt;
-            nxt = source(ibase + 32 + lane);
+    auto unit_at = [&](int k) {
+        Unit u;
+        u.b = seq_of(w0 + k);
+        const PdSeq q = SQ[u.b];
+        const long long unit = pd_div(w0 + k - W[u.b], q.ns);
+        u.q0 = q.q0; u.qn = q.qn; u.len = q.len;
+        u.u0 = W[u.b] + unit * q.ns;
+        u.u1 = u.u0 + q.ns;
+        u.rg = (int)pd_div(unit, KV);
+        u.h = (int)(unit - (long long)u.rg * KV);
+        return u;
+    };
+    // the lane's part of a unit's queries: column g, dims 32 bb + 8 t .. + 7, as they are
+    const bool vec = ((uintptr_t)a.q_dev & 15) == 0 && (a.q_stride * sizeof(T)) % 16 == 0;
+    __align__(16) T raw[C::NB][8];
+    auto load_q = [&](const Unit &u) {
+        int row, head, tok;
+        pd_row(g, u.rg, G, u.q0, u.h, row, head, tok);
+        const T *src = (const T *)a.q_dev + row * a.q_stride + (size_t)head * HD + 8 * t;
+#pragma unroll
+        for (int bb = 0; bb < C::NB; ++bb) {
+            if (tok >= u.qn) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) raw[bb][e] = pg_cvt<T>(0.f);
+            } else if (vec) {
+#pragma unroll
+                for (int k = 0; k < (int)(8 * sizeof(T)) / 16; ++k)
+                    reinterpret_cast<uint4 *>(raw[bb])[k] = reinterpret_cast<const uint4 *>(src + 32 * bb)[k];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) raw[bb][e] = src[32 * bb + e];
+            }
         }
-        const unsigned long long off = __shfl_sync(0xffffffffu, cur, (int)(inext - ibase));
-        if (lane == 0) {
-            const int slot = (int)((inext - w0) % PD_SLOTS);
-            mbar_arrive_expect_tx(bars + slot, C::TILE);
-            bulk_g2s(ring + slot * C::TILE, P.p.pool + off, C::TILE, bars + slot);
+    };
+    Unit U;
+    if (cnt > 0) {
+        U = unit_at(0);
+        load_q(U);
+    }
+    // where the two tiles of step k lie, as tile numbers of the pool (it holds fewer than 2^32); ABSENT: one that lies
+    // outside the rows that the unit attends
+    constexpr uint32_t ABSENT = 0xFFFFFFFFu;
+    auto source = [&](int k, uint32_t &x0, uint32_t &x1) {
+        x0 = x1 = ABSENT;
+        if (k >= cnt) return;
+        const int b = seq_of(w0 + k);
+        const PdSeq q = SQ[b];
+        const long long rem = w0 + k - W[b], unit = pd_div(rem, q.ns);
+        const int lo = pd_row0(q.len, q.qn, a.window), h = (int)(unit - pd_div(unit, KV) * KV);
+        const int row = (lo / PD_STEP + (int)(rem - unit * q.ns)) * PD_STEP;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int rn = row + 16 * n;
+            if (rn >= q.len || rn + 15 < lo) continue;
+            const int blk = (int)((uint32_t)rn / (uint32_t)R);
+            int page = a.tables_dev[(size_t)b * a.table_stride + blk];
+            if (page < 0 || page >= P.p.n_pages) {
+                atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
+                page = 0;
+            }
+            (n ? x1 : x0) = ((uint32_t)page * KV + h) * (R >> 4) + ((rn - blk * R) >> 4);
+        }
+    };
+    // the 32 steps among which the next one to request lies are in cur, a lane each, the 32 after them in nxt
+    int inext = 0, islot = 0;
+    uint32_t cur0, cur1, nxt0 = 0, nxt1 = 0;
+    source(lane, cur0, cur1);
+    auto issue = [&]() {  // requests the next step: the lane that knows where it lies
+        if (inext >= cnt) return;
+        if ((inext & 31) == 0) {
+            if (inext) {
+                cur0 = nxt0;
+                cur1 = nxt1;
+            }
+            source((inext | 31) + 1 + lane, nxt0, nxt1);
+        }
+        if (lane == (inext & 31)) {
+            uint8_t *dst = ring + islot * (2 * C::TILE);
+            mbar_arrive_expect_tx(bars + islot, (cur0 != ABSENT ? C::TILE : 0) + (cur1 != ABSENT ? C::TILE : 0));
+            if (cur0 != ABSENT) bulk_g2s(dst, P.p.pool + (size_t)cur0 * C::TILE, C::TILE, bars + islot);
+            if (cur1 != ABSENT) bulk_g2s(dst + C::TILE, P.p.pool + (size_t)cur1 * C::TILE, C::TILE, bars + islot);
         }
         ++inext;
+        if (++islot == PD_SLOTS) islot = 0;
     };
     for (int k = 0; k < PD_SLOTS; ++k) issue();
 
     const float qscale = (a.scale != 0.f ? a.scale : 1.f / sqrtf((float)HD)) * 1.4426950408889634f;
-    const bool vec = ((uintptr_t)a.q_dev & 15) == 0 && (a.q_stride * sizeof(T)) % 16 == 0;
-    int wslot = 0;         // ring slot and parity of the next tile to consume
+    int wslot = 0;     // ring slot and parity of the next step to consume
     uint32_t wpar = 0;
-    bool bad = false;      // a wait gave up
+    bool bad = false;  // a wait gave up
 
-    for (long long i = w0; i < w1 && !bad;) {
-        // ---- the unit of entry i
-        const int b = seq_of(i), nt = NT[b], t0 = T0[b];
-        const long long unit = (i - W[b]) / nt, u0 = W[b] + unit * nt, u1 = u0 + nt;
-        const int h = (int)(unit % KV), rg = (int)(unit / KV);
-        const int q0 = a.q_start_dev[b], qn = a.q_start_dev[b + 1] - q0, len = a.lens_dev[b];
-        const long long send = min(u1, w1);
-        int row, head, tok;
-        pd_row(g, rg, G, q0, h, row, head, tok);
-        const bool real = tok < qn;
-        // rows that this lane's query row attends, and the ranges that all and any of the unit's rows attend
-        const int tok0 = rg * PD_ROWS / G, tok1 = min((rg * PD_ROWS + PD_ROWS - 1) / G, qn - 1);
-        const int pos = real ? len - qn + tok : -1;
-        const int first = a.window ? max(0, pos - a.window + 1) : 0;
-        const int any_lo = a.window ? max(0, len - qn + tok0 - a.window + 1) : 0, any_hi = len - qn + tok1;
-        const int all_lo = a.window ? max(0, len - qn + tok1 - a.window + 1) : 0, all_hi = len - qn + tok0;
+    for (int k0 = 0; k0 < cnt;) {
+        // rows that the lane's columns 2 t, 2 t + 1 attend, and the ranges that all and any of the unit's rows attend
+        const int past = U.len - U.qn;
+        const int tok0 = U.rg * PD_ROWS / G, tok1 = min((U.rg * PD_ROWS + PD_ROWS - 1) / G, U.qn - 1);
+        int pos[2], first[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int tok = (U.rg * PD_ROWS + 2 * t + c) / G;
+            pos[c] = tok < U.qn ? past + tok : -1;
+            first[c] = a.window ? max(0, pos[c] - a.window + 1) : 0;
+        }
+        const int any_lo = a.window ? max(0, past + tok0 - a.window + 1) : 0, any_hi = past + tok1;
+        const int all_lo = a.window ? max(0, past + tok1 - a.window + 1) : 0, all_hi = past + tok0;
 
-        uint32_t qa[2 * C::NB][4];  // k16 steps: dims 32 b + 8 t + 4 m .. + 3 of step 2 b + m
-        float down;
+        // the queries' pieces, in the order in which masks leave a word's codes
+        uint32_t qp[C::NB][Y::NA + Y::NB][2];
+        uint32_t bias;  // B of the scales' product: -8 2^-9 sum q of the blocks, hi halves, then lo halves
+        float down[2];
         {
-            float x[C::NB][8], top = 0.f;
-#pragma unroll
-            for (int bb = 0; bb < C::NB; ++bb) {
-                const T *src = (const T *)a.q_dev + row * a.q_stride + (size_t)head * HD + 32 * bb + 8 * t;
-                if (!real) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[bb][e] = 0.f;
-                } else if (vec) {
-                    __align__(16) T v[8];
-#pragma unroll
-                    for (int k = 0; k < (int)(8 * sizeof(T)) / 16; ++k)
-                        reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(src)[k];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[bb][e] = pg_ld<T>(v + e) * qscale;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[bb][e] = pg_ld<T>(src + e) * qscale;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[bb][e]));
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            int ex = 0;  // the row's largest goes to [2^14, 2^15), so the lo halves of all that matters are normal
-            if (top > 0.f && isfinite(top)) {
-                frexpf(top, &ex);
-                ex = min(max(15 - ex, -126), 126);
-            }
-            const float up = ldexpf(1.f, ex);
-            down = ldexpf(1.f, -ex);
+            float top = 0.f;
+            bool odd = false;  // infinite and NaN queries: their scores are NaN through `down`
 #pragma unroll
             for (int bb = 0; bb < C::NB; ++bb)
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    pd_split(x[bb][4 * m] * up, x[bb][4 * m + 1] * up, qa[2 * bb + m][0], qa[2 * bb + m][1]);
-                    pd_split(x[bb][4 * m + 2] * up, x[bb][4 * m + 3] * up, qa[2 * bb + m][2], qa[2 * bb + m][3]);
+                for (int e = 0; e < 8; ++e) {
+                    const float x = fabsf(pg_ld<T>(&raw[bb][e]));
+                    top = fmaxf(top, x);
+                    odd |= !(x <= 3.4028235e38f);
                 }
-        }
-        float m = -INFINITY, l = 0.f;
-        float o[C::NTD][4];
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            odd = __ballot_sync(0xffffffffu, odd) >> (lane & ~3) & 15;
+            // the row's largest goes to [2^7, 2^8) by a power of two, up: e4m3 ends at 448 and steps by 2^-9
+            const int ex = min(max((int)(__float_as_uint(top) >> 23), 8), 246);
+            const float up = odd ? 0.f : __uint_as_float((uint32_t)(261 - ex) << 23);
+            const float dn = odd ? NAN : __uint_as_float((uint32_t)(ex - 7) << 23);
+            float sums[C::NB];
 #pragma unroll
-        for (int j = 0; j < C::NTD; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+            for (int bb = 0; bb < C::NB; ++bb) {
+                float x[8], sum = 0.f, sum2 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = odd ? 0.f : pg_ld<T>(&raw[bb][e]) * up;
+#pragma unroll
+                for (int k = 0; k < Y::NA + Y::NB; ++k) {
+                    if (k == Y::NA)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] *= (float)(1 << PD_SUB);
+                    float &sm = k < Y::NA ? sum : sum2;
+                    qp[bb][k][0] = pd_piece(x[0], x[4], sm);
+                    qp[bb][k][0] |= pd_piece(x[1], x[5], sm) << 16;
+                    qp[bb][k][1] = pd_piece(x[2], x[6], sm);
+                    qp[bb][k][1] |= pd_piece(x[3], x[7], sm) << 16;
+                }
+                sums[bb] = (sum + sum2 * (1.f / (float)(1 << PD_SUB))) * (-8.f / 512.f);
+            }
+#pragma unroll
+            for (int bb = 0; bb < C::NB; ++bb) {
+                sums[bb] += __shfl_xor_sync(0xffffffffu, sums[bb], 1);
+                sums[bb] += __shfl_xor_sync(0xffffffffu, sums[bb], 2);
+            }
+            uint32_t hi[C::NB / 2], lo[C::NB / 2];
+#pragma unroll
+            for (int k = 0; k < C::NB / 2; ++k) pd_split(sums[2 * k], sums[2 * k + 1], hi[k], lo[k]);
+            if constexpr (HD == 128) bias = t == 0 ? hi[0] : t == 1 ? hi[C::NB / 2 - 1] : t == 2 ? lo[0] : lo[C::NB / 2 - 1];
+            else bias = t == 0 ? hi[0] : t == 1 ? lo[0] : 0u;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) down[c] = __shfl_sync(0xffffffffu, dn, 4 * (2 * t + c)) * (512.f * qscale);
+        }
+        float m[2] = {PD_NONE, PD_NONE}, l[2] = {0.f, 0.f};
+        float o[HD / 16][4];  // dims 16 j + g (0, 1) and + 8 (2, 3) of columns 2 t, 2 t + 1
+#pragma unroll
+        for (int j = 0; j < HD / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-        for (; i < send; ++i) {
+        // one step: rows r0 .. r0 + 31.  EDGE: some row of the unit does not attend all of them
+        auto step = [&](auto edge_tag, int r0) {
+            constexpr bool EDGE = decltype(edge_tag)::value;
+            const uint8_t *sl = ring + wslot * (2 * C::TILE);
+            // ---- scores: rows r0 + 16 n + g (x[n][0], x[n][1]) and + 8 (x[n][2], x[n][3]) of columns 2 t, 2 t + 1
+            float x[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const uint8_t *sn = sl + n * C::TILE;
+                uint32_t kw[2][C::NB], ks[2][C::NB / 2];
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int rr = 8 * v + g;
+                    if constexpr (HD == 128) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(sn + rr * 64 + t * 16);
+                        kw[v][0] = y.x; kw[v][1] = y.y; kw[v][2] = y.z; kw[v][3] = y.w;
+                        const uint2 z = *reinterpret_cast<const uint2 *>(sn + pg_off_ks(HD) + rr * 8);
+                        ks[v][0] = z.x; ks[v][1] = z.y;
+                    } else {
+                        const uint2 y = *reinterpret_cast<const uint2 *>(sn + rr * 32 + t * 8);
+                        kw[v][0] = y.x; kw[v][1] = y.y;
+                        ks[v][0] = *reinterpret_cast<const uint32_t *>(sn + pg_off_ks(HD) + rr * 4);
+                    }
+                }
+                float sc[4] = {0.f, 0.f, 0.f, 0.f};
+                [[maybe_unused]] float sc2[4] = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (HD == 128)
+                    pd_mma_k8(sc, (t & 1) ? ks[0][1] : ks[0][0], (t & 1) ? ks[1][1] : ks[1][0], bias);
+                else
+                    pd_mma_k8(sc, ks[0][0], ks[1][0], bias);
+#pragma unroll
+                for (int bb = 0; bb < C::NB; ++bb) {
+                    const uint32_t ka[4] = {kw[0][bb] & 0x0F0F0F0Fu, kw[1][bb] & 0x0F0F0F0Fu,
+                                            (kw[0][bb] >> 4) & 0x0F0F0F0Fu, (kw[1][bb] >> 4) & 0x0F0F0F0Fu};
+                    const float2 e0 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[0][bb >> 1]));
+                    const float2 e1 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[1][bb >> 1]));
+                    const float d0 = (bb & 1) ? e0.y : e0.x, d1 = (bb & 1) ? e1.y : e1.x;
+                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                    float acc[4];
+                    pd_mma8(acc, ka, qp[bb][0][0], qp[bb][0][1], zero);
+#pragma unroll
+                    for (int k = 1; k < Y::NA; ++k) pd_mma8(acc, ka, qp[bb][k][0], qp[bb][k][1], acc);
+                    sc[0] = fmaf(d0, acc[0], sc[0]); sc[1] = fmaf(d0, acc[1], sc[1]);
+                    sc[2] = fmaf(d1, acc[2], sc[2]); sc[3] = fmaf(d1, acc[3], sc[3]);
+                    if constexpr (Y::NB > 0) {
+                        pd_mma8(acc, ka, qp[bb][Y::NA][0], qp[bb][Y::NA][1], zero);
+#pragma unroll
+                        for (int k = Y::NA + 1; k < Y::NA + Y::NB; ++k)
+                            pd_mma8(acc, ka, qp[bb][k][0], qp[bb][k][1], acc);
+                        sc2[0] = fmaf(d0, acc[0], sc2[0]); sc2[1] = fmaf(d0, acc[1], sc2[1]);
+                        sc2[2] = fmaf(d1, acc[2], sc2[2]); sc2[3] = fmaf(d1, acc[3], sc2[3]);
+                    }
+                }
+                if constexpr (Y::NB > 0)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[k] = fmaf(sc2[k], 1.f / (float)(1 << PD_SUB), sc[k]);
+                if constexpr (EDGE) {
+                    bool vnan[2] = {false, false};  // rows g, g + 8 hold a NaN value: their scores carry it
+                    const unsigned short *vs = reinterpret_cast<const unsigned short *>(sn + pg_off_vs(HD));
+#pragma unroll
+                    for (int bb = 0; bb < C::NB; ++bb)
+#pragma unroll
+                        for (int v = 0; v < 2; ++v)
+                            vnan[v] |= (vs[(((g >> 1) * C::NB + bb) * 2 + v) * 2 + (g & 1)] & 0x7FFF) > 0x7C00;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = r0 + 16 * n + g + 8 * (k >> 1);
+                        if (vnan[k >> 1]) sc[k] = NAN;
+                        x[n][k] = r < first[k & 1] || r > pos[k & 1] ? -INFINITY : sc[k] * down[k & 1];
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[n][k] = sc[k] * down[k & 1];
+                }
+            }
+            // a score far above the reference: a new one for the column, and the sums follow
+            const float t0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+            const float t1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+            if (__any_sync(0xffffffffu, t0 > m[0] + PD_SLACK || t1 > m[1] + PD_SLACK)) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float mt = c ? t1 : t0;
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+                    const float mn = mt > m[c] + PD_SLACK ? mt : m[c];
+                    const float corr = mn == m[c] ? 1.f : ex2(m[c] - mn);
+                    l[c] *= corr;
+#pragma unroll
+                    for (int j = 0; j < HD / 16; ++j) {
+                        o[j][c] *= corr;
+                        o[j][2 + c] *= corr;
+                    }
+                    m[c] = mn;
+                }
+            }
+            uint32_t ph[2][2];  // B of P: rows 16 n + 8 v .. + 7
+            [[maybe_unused]] uint32_t pl[2][2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) p[k] = ex2(x[n][k] - (m[k & 1] - PD_UP));
+                l[0] += p[0] + p[2];
+                l[1] += p[1] + p[3];
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    if constexpr (Y::SPLIT) {
+                        pd_split(p[2 * v], p[2 * v + 1], ph[n][v], pl[n][v]);
+                        pl[n][v] = pd_trans(pl[n][v]);
+                    } else {
+                        ph[n][v] = pd_pack(p[2 * v], p[2 * v + 1]);
+                    }
+                    ph[n][v] = pd_trans(ph[n][v]);
+                }
+            }
+            // ---- o += p v
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const uint8_t *sn = sl + n * C::TILE;
+                // V scales of rows 2t, 2t + 1 (vd[.][0]) and 2t + 8, 2t + 9 (vd[.][1]), a pair a word
+                uint32_t vw[HD / 64][4], vd[C::NB][2];
+#pragma unroll
+                for (int k = 0; k < C::NB / 2; ++k) {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(sn + pg_off_vs(HD) + t * (C::NB * 8) + 16 * k);
+                    vd[2 * k][0] = y.x; vd[2 * k][1] = y.y; vd[2 * k + 1][0] = y.z; vd[2 * k + 1][1] = y.w;
+                }
+#pragma unroll
+                for (int q = 0; q < HD / 64; ++q) {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(sn + pg_off_v(HD) + q * 512 + lane * 16);
+                    vw[q][0] = y.x; vw[q][1] = y.y; vw[q][2] = y.z; vw[q][3] = y.w;
+                }
+                if constexpr (EDGE) {  // scales of rows that nobody attends, or that are NaN: 0
+#pragma unroll
+                    for (int bb = 0; bb < C::NB; ++bb)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = r0 + 16 * n + 2 * t + (k & 1) + 8 * (k >> 1);
+                            const uint32_t half = (k & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+                            if (((vd[bb][k >> 1] & half) & 0x7FFF7FFFu) > (0x7C007C00u & half) || r < any_lo || r > any_hi)
+                                vd[bb][k >> 1] &= ~half;
+                        }
+                }
+#pragma unroll
+                for (int bb = 0; bb < C::NB; ++bb) {
+                    const uint32_t d0 = vd[bb][0], d1 = vd[bb][1], z0 = h2_mul(d0, PD_M24), z1 = h2_mul(d1, PD_M24);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t w = vw[bb >> 1][2 * (bb & 1) + u];
+                        const uint32_t va[4] = {h2_fma(pd_code<0>(w), d0, z0), h2_fma(pd_code<1>(w), d0, z0),
+                                                h2_fma(pd_code<2>(w), d1, z1), h2_fma(pd_code<3>(w), d1, z1)};
+                        pd_mma(o[2 * bb + u], va, ph[n][0], ph[n][1]);
+                        if constexpr (Y::SPLIT) pd_mma(o[2 * bb + u], va, pl[n][0], pl[n][1]);
+                    }
+                }
+            }
+        };
+
+        const int kend = (int)(min(U.u1, w1) - w0);  // the segment: steps k0 .. kend - 1
+        int r0 = (pd_row0(U.len, U.qn, a.window) / PD_STEP + (int)(w0 + k0 - U.u0)) * PD_STEP;
+        for (int k = k0; k < kend; ++k, r0 += PD_STEP) {
             if (!__all_sync(0xffffffffu, mbar_wait(bars + wslot, wpar))) {
                 bad = true;
                 break;
             }
-            const uint32_t sl = smem_u32(ring + wslot * C::TILE);
-            const int r0 = (t0 + (int)(i - u0)) << 4;
-            const bool edge = r0 < all_lo || r0 + 15 > all_hi;
-            if (!(edge && (r0 > any_hi || r0 + 15 < any_lo))) {
-                // ---- scores of rows r0 .. + 15: two n8 tiles
-                float s[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-                    const int rr = 8 * n + g;
-                    uint32_t w[C::NB], ds[C::NB / 2];
-                    if constexpr (HD == 128) {
-                        const uint4 x = lds128(sl + rr * 64 + t * 16);
-                        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-                        const uint2 y = lds64(sl + pg_off_ks(HD) + rr * 8);
-                        ds[0] = y.x; ds[1] = y.y;
-                    } else {
-                        const uint2 x = lds64(sl + rr * 32 + t * 8);
-                        w[0] = x.x; w[1] = x.y;
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(ds[0]) : "r"(sl + pg_off_ks(HD) + rr * 4));
-                    }
-#pragma unroll
-                    for (int bb = 0; bb < C::NB; ++bb) {
-                        const uint32_t d = h2_dup(ds[bb >> 1], bb & 1), z = h2_mul(d, PD_M24);
-                        mma_16816(s[n], qa[2 * bb], h2_fma(pd_code<0>(w[bb]), d, z), h2_fma(pd_code<1>(w[bb]), d, z), s[n]);
-                        mma_16816(s[n], qa[2 * bb + 1], h2_fma(pd_code<2>(w[bb]), d, z), h2_fma(pd_code<3>(w[bb]), d, z), s[n]);
-                    }
-                }
-                // V scales of rows 2t, 2t + 1 (vd[.][0]) and 2t + 8, 2t + 9 (vd[.][1]), a pair a word
-                uint32_t vd[C::NB][2];
-#pragma unroll
-                for (int k = 0; k < C::NB / 2; ++k) {
-                    const uint4 x = lds128(sl + pg_off_vs(HD) + t * (C::NB * 8) + 16 * k);
-                    vd[2 * k][0] = x.x; vd[2 * k][1] = x.y; vd[2 * k + 1][0] = x.z; vd[2 * k + 1][1] = x.w;
-                }
-                // score k: row r0 + 2 t + (k & 1) + 8 (k >> 1)
-                float sc[4] = {(s[0][0] + s[0][2]) * down, (s[0][1] + s[0][3]) * down, (s[1][0] + s[1][2]) * down,
-                               (s[1][1] + s[1][3]) * down};
-                if (edge) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = r0 + 2 * t + (k & 1) + 8 * (k >> 1);
-                        const uint32_t half = (k & 1) ? 0xFFFF0000u : 0x0000FFFFu;
-                        bool nan = false;
-#pragma unroll
-                        for (int bb = 0; bb < C::NB; ++bb) {
-                            const uint32_t x = (vd[bb][k >> 1] & half) & 0x7FFF7FFFu;
-                            const bool n = x > (0x7C007C00u & half);
-                            nan |= n;
-                            if (n || r < any_lo || r > any_hi) vd[bb][k >> 1] &= ~half;
-                        }
-                        if (nan) sc[k] = NAN;
-                        if (r < first || r > pos) sc[k] = -INFINITY;
-                    }
-                }
-                float mt = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-                if (__any_sync(0xffffffffu, mt > m + PD_SLACK)) {
-                    const float mn = mt > m + PD_SLACK ? mt : m;
-                    const float corr = mn == m ? 1.f : ex2(m - mn);
-                    l *= corr;
-#pragma unroll
-                    for (int j = 0; j < C::NTD; ++j) {
-                        o[j][0] *= corr; o[j][1] *= corr; o[j][2] *= corr; o[j][3] *= corr;
-                    }
-                    m = mn;
-                }
-                const float base = (m == -INFINITY ? 0.f : m) - PD_UP;
-                float p[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) p[k] = ex2(sc[k] - base);
-                l += (p[0] + p[1]) + (p[2] + p[3]);
-                uint32_t pa[4];
-                pd_split(p[0], p[1], pa[0], pa[1]);
-                pd_split(p[2], p[3], pa[2], pa[3]);
-                // ---- o += p v: word u of run q holds dims 64 q + 16 u + g and + 8 of the lane's four rows
-#pragma unroll
-                for (int q = 0; q < HD / 64; ++q) {
-                    const uint4 x = lds128(sl + pg_off_v(HD) + q * 512 + lane * 16);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int hb = 0; hb < 2; ++hb) {
-                        const uint32_t d0 = vd[2 * q + hb][0], d1 = vd[2 * q + hb][1], z0 = h2_mul(d0, PD_M24),
-                                       z1 = h2_mul(d1, PD_M24);
-#pragma unroll
-                        for (int u = 2 * hb; u < 2 * hb + 2; ++u) {
-                            const int j = 8 * q + 2 * u;
-                            mma_16816(o[j], pa, h2_fma(pd_code<0>(w[u]), d0, z0), h2_fma(pd_code<2>(w[u]), d1, z1), o[j]);
-                            mma_16816(o[j + 1], pa, h2_fma(pd_code<1>(w[u]), d0, z0), h2_fma(pd_code<3>(w[u]), d1, z1),
-                                      o[j + 1]);
-                        }
-                    }
-                }
-            }
-            __syncwarp();  // every lane is done with the slot
+            if (r0 >= all_lo && r0 + PD_STEP - 1 <= all_hi) step(std::false_type{}, r0);
+            else if (r0 <= any_hi && r0 + PD_STEP - 1 >= any_lo) step(std::true_type{}, r0);
+            __syncwarp();  // every lane has read the slot
             issue();
             if (++wslot == PD_SLOTS) {
                 wslot = 0;
                 wpar ^= 1u;
             }
         }
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (bad) break;
-        const long long sbeg = max(u0, w0);
-        if (sbeg == u0 && send == u1) {  // the whole unit
-            if (real) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                T *out = (T *)a.out_dev + row * a.out_stride + (size_t)head * HD + 2 * t;
-                const bool pair = ((uintptr_t)out & (2 * sizeof(T) - 1)) == 0;
 #pragma unroll
-                for (int j = 0; j < C::NTD; ++j) {
-                    const float y0 = l == 0.f ? 0.f : (o[j][0] + o[j][2]) * inv, y1 = l == 0.f ? 0.f : (o[j][1] + o[j][3]) * inv;
-                    __align__(8) T v[2] = {pg_cvt<T>(y0), pg_cvt<T>(y1)};
-                    if (pair) {
-                        if constexpr (sizeof(T) == 4) *reinterpret_cast<uint2 *>(out + 8 * j) = *reinterpret_cast<uint2 *>(v);
-                        else *reinterpret_cast<uint32_t *>(out + 8 * j) = *reinterpret_cast<uint32_t *>(v);
-                    } else {
-                        out[8 * j] = v[0];
-                        out[8 * j + 1] = v[1];
-                    }
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], off);
+        if (bad) break;
+        const bool whole = U.u0 >= w0 + k0 && U.u1 <= w1;
+        const Unit D = U;  // done
+        if (kend < cnt) {  // the next unit's queries, while this one's results are written
+            U = unit_at(kend);
+            load_q(U);
+        }
+        k0 = kend;
+        if (whole) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                int row, head, tok;
+                pd_row(2 * t + c, D.rg, G, D.q0, D.h, row, head, tok);
+                if (tok >= D.qn) continue;
+                const float inv = 1.f / l[c];
+                T *out = (T *)a.out_dev + row * a.out_stride + (size_t)head * HD + g;
+#pragma unroll
+                for (int j = 0; j < HD / 16; ++j) {
+                    out[16 * j] = pg_cvt<T>(l[c] == 0.f ? 0.f : o[j][c] * inv);
+                    out[16 * j + 8] = pg_cvt<T>(l[c] == 0.f ? 0.f : o[j][2 + c] * inv);
                 }
-                if (a.lse_dev && t == 0)
+                if (a.lse_dev && g == 0)
                     a.lse_dev[(size_t)row * a.n_heads + head] =
-                        l == 0.f ? -INFINITY : (m - PD_UP + log2f(l)) * 0.6931471805599453f;
+                        l[c] == 0.f ? -INFINITY : (m[c] - PD_UP + log2f(l[c])) * 0.6931471805599453f;
             }
         } else {
             // a state: the last segment's goes into the ring (nothing is on its way there any more)
-            const int off = send == w1 ? warp * C::RING : C::OFF_FIRST + warp * C::STATE * 4;
+            const int off = kend == cnt ? warp * C::RING : C::OFF_FIRST + warp * C::STATE * 4;
             float *st = reinterpret_cast<float *>(smem + off);
 #pragma unroll
-            for (int j = 0; j < C::NTD; ++j)
-                *reinterpret_cast<float2 *>(st + g * HD + 8 * j + 2 * t) = make_float2(o[j][0] + o[j][2], o[j][1] + o[j][3]);
-            if (t == 0) {
-                st[PD_ROWS * HD + g] = m;
-                st[PD_ROWS * HD + 8 + g] = l;
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int j = 0; j < HD / 16; ++j) {
+                    st[(2 * t + c) * HD + 16 * j + g] = o[j][c];
+                    st[(2 * t + c) * HD + 16 * j + g + 8] = o[j][2 + c];
+                }
+                if (g == 0) {
+                    st[PD_ROWS * HD + 2 * t + c] = m[c];
+                    st[PD_ROWS * HD + 8 + 2 * t + c] = l[c];
+                }
             }
-            if (lane == 0) ms.seg[2 * warp + (send == w1)] = {u0, u1, b, rg, h, off};
+            if (lane == 0) ms.seg[2 * warp + (kend == cnt)] = {D.u0, D.u1, D.b, D.rg, D.h, off};
         }
     }
     if (bad) {
         if (lane == 0) atomicOr(P.p.flags, ER_FLAG_WAIT);
         ms.wait_bad = 1;
         // copies may still be landing: wait for them (each again with a limit)
-        for (long long k = inext - PD_SLOTS > w0 ? inext - PD_SLOTS : w0; k < inext; ++k)
-            mbar_wait(bars + (int)((k - w0) % PD_SLOTS), (uint32_t)(((k - w0) / PD_SLOTS) & 1));
+        for (int k = max(0, inext - PD_SLOTS); k < inext; ++k) mbar_wait(bars + k % PD_SLOTS, (k / PD_SLOTS) & 1);
     }
     __syncthreads();
-    if (tid == 0) {  // runs of neighbouring states of one unit
-        int n = 0, k = 0;
-        for (int e = 0; e < 2 * PD_WARPS; ++e)
-            if (ms.seg[e].off >= 0) {
-                if (n == 0 || ms.seg[n - 1].u0 != ms.seg[e].u0) ms.run[k++] = n;
-                ms.seg[n++] = ms.seg[e];
-            }
-        ms.run[k] = n;
-        ms.n_runs = ms.wait_bad ? 0 : k;
+    if (warp == 0) {  // runs of neighbouring states of one unit; lane e looks at the e-th place for one
+        static_assert(2 * PD_WARPS <= 32, "a lane for each state");
+        const bool there = lane < 2 * PD_WARPS && ms.seg[lane].off >= 0;
+        const unsigned all = __ballot_sync(0xffffffffu, there);
+        const int before = 31 - __clz((int)(all & ((1u << lane) - 1u)));  // the state before this one, or -1
+        const bool starts = there && (before < 0 || ms.seg[before].u0 != ms.seg[lane].u0);
+        const unsigned runs = __ballot_sync(0xffffffffu, starts);
+        if (there) ms.ent[__popc(all & ((1u << lane) - 1u))] = (short)lane;
+        if (starts) ms.run[__popc(runs & ((1u << lane) - 1u))] = __popc(all & ((1u << lane) - 1u));
+        if (lane == 0) {
+            ms.run[__popc(runs)] = __popc(all);
+            ms.n_runs = ms.wait_bad ? 0 : __popc(runs);
+        }
     }
     __syncthreads();
     const int n_runs = ms.n_runs;
     constexpr int V = HD / 32;  // dims of a lane
     // a row of a unit, joined: o of dims V lane .. , the reference m and sum l
     auto write_row = [&](const PdSeg &sg, int r, const float (&y)[V], float mm, float ll) {
-        const int q0 = a.q_start_dev[sg.b], qn = a.q_start_dev[sg.b + 1] - q0;
         int row, head, tok;
-        pd_row(r, sg.rg, G, q0, sg.h, row, head, tok);
-        if (tok >= qn) return;
+        pd_row(r, sg.rg, G, SQ[sg.b].q0, sg.h, row, head, tok);
+        if (tok >= SQ[sg.b].qn) return;
         T *out = (T *)a.out_dev + row * a.out_stride + (size_t)head * HD + V * lane;
 #pragma unroll
         for (int e = 0; e < V; ++e) out[e] = pg_cvt<T>(ll == 0.f ? 0.f : y[e] / ll);
@@ -491,29 +709,42 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
             a.lse_dev[(size_t)row * a.n_heads + head] =
                 ll == 0.f ? -INFINITY : (mm - PD_UP + log2f(ll)) * 0.6931471805599453f;
     };
+    // real rows of a unit
+    auto rows_of = [&](const PdSeg &sg) {
+        return (int)min((long long)PD_ROWS, (long long)SQ[sg.b].qn * G - (long long)sg.rg * PD_ROWS);
+    };
     for (int it = warp; it < n_runs * PD_ROWS; it += PD_WARPS) {
         const int run = it / PD_ROWS, r = it % PD_ROWS;
-        const int e0 = ms.run[run], e1 = ms.run[run + 1];
-        const PdSeg &sg = ms.seg[e0];
-        float M = -INFINITY;
-        for (int e = e0; e < e1; ++e) M = fmaxf(M, reinterpret_cast<float *>(smem + ms.seg[e].off)[PD_ROWS * HD + r]);
-        const float base = M == -INFINITY ? 0.f : M;
-        float y[V], L = 0.f;
+        const int e0 = ms.run[run], ne = ms.run[run + 1] - e0;
+        const PdSeg &sg = ms.seg[ms.ent[e0]];
+        if (r >= rows_of(sg)) continue;
+        // lane e: the weight of the run's e-th state
+        const int off = lane < ne ? ms.seg[ms.ent[e0 + lane]].off : 0;
+        const float *mine = reinterpret_cast<const float *>(smem + off);
+        float M = lane < ne ? mine[PD_ROWS * HD + r] : PD_NONE;
+        const float own = M;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        const float f = lane < ne ? ex2(own - M) : 0.f;
+        float L = lane < ne ? f * mine[PD_ROWS * HD + 8 + r] : 0.f;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+        float y[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) y[e] = 0.f;
-        for (int e = e0; e < e1; ++e) {
-            const float *st = reinterpret_cast<float *>(smem + ms.seg[e].off);
-            const float f = ex2(st[PD_ROWS * HD + r] - base);
-            L += f * st[PD_ROWS * HD + 8 + r];
+#pragma unroll 4
+        for (int e = 0; e < ne; ++e) {
+            const float fe = __shfl_sync(0xffffffffu, f, e);
+            const float *st = reinterpret_cast<const float *>(smem + __shfl_sync(0xffffffffu, off, e));
 #pragma unroll
-            for (int k = 0; k < V; ++k) y[k] += f * st[r * HD + V * lane + k];
+            for (int k = 0; k < V; ++k) y[k] += fe * st[r * HD + V * lane + k];
         }
         if (sg.u0 >= c0 && sg.u1 <= c1) {
             write_row(sg, r, y, M, L);
         } else {
             float *st = P.part + ((size_t)blockIdx.x * 2 + (sg.u0 < c0 ? 0 : 1)) * C::STATE;
-#pragma unroll
-            for (int k = 0; k < V; ++k) __stcg(st + r * HD + V * lane + k, y[k]);
+            if constexpr (V == 4) __stcg(reinterpret_cast<float4 *>(st + r * HD) + lane, make_float4(y[0], y[1], y[2], y[V - 1]));
+            else __stcg(reinterpret_cast<float2 *>(st + r * HD) + lane, make_float2(y[0], y[1]));
             if (lane == 0) {
                 __stcg(st + PD_ROWS * HD + r, M);
                 __stcg(st + PD_ROWS * HD + 8 + r, L);
@@ -523,82 +754,65 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
     // ---- units of several CTAs: the last to arrive joins their states in CTA order
     __threadfence();
     __syncthreads();
-    if (tid == 0) {
-        ms.last[0] = ms.last[1] = -1;
-        int k = 0;
-        for (int run = 0; run < n_runs; ++run) {
-            const PdSeg &sg = ms.seg[ms.run[run]];
-            if (sg.u0 >= c0 && sg.u1 <= c1) continue;
-            const int ca = (int)(((sg.u0 + 1) * C_ - 1) / N), cb = (int)((sg.u1 * C_ - 1) / N);
+    if (tid < 2) ms.last[tid] = -1;
+    __syncwarp();
+    if (tid < n_runs) {  // at most 2 * PD_WARPS runs; two of them reach into other CTAs
+        const PdSeg &sg = ms.seg[ms.ent[ms.run[tid]]];
+        if (sg.u0 < c0 || sg.u1 > c1) {
+            const int ca = pd_cta(sg.u0, N, C_), cb = pd_cta(sg.u1 - 1, N, C_);
             if (atom_add_acq_rel_gpu(P.cnt + ca, 1) == cb - ca) {
                 P.cnt[ca] = 0;
-                ms.last[k++] = run;
+                ms.last[sg.u0 < c0 ? 0 : 1] = tid;
             }
         }
     }
     __syncthreads();
-    float *wts = reinterpret_cast<float *>(smem);                      // [8][CTAs] weights (the ring is free)
-    float *acc = reinterpret_cast<float *>(smem) + PD_ROWS * 512;      // [warps][HD]
+    float *acc = reinterpret_cast<float *>(smem + C::OFF_FIRST);  // [warps][HD + 4], where the first states were
     for (int k = 0; k < 2; ++k) {
-        if (ms.last[k] < 0) break;
-        const PdSeg sg = ms.seg[ms.run[ms.last[k]]];
-        __syncthreads();  // the states in the ring are read before the weights go there
-        const int ca = (int)(((sg.u0 + 1) * C_ - 1) / N), cb = (int)((sg.u1 * C_ - 1) / N), nc = cb - ca + 1;
-        auto state = [&](int c) { return P.part + ((size_t)c * 2 + (sg.u0 < c * N / C_ ? 0 : 1)) * C::STATE; };
-        const int f0 = sg.rg * PD_ROWS, qn = a.q_start_dev[sg.b + 1] - a.q_start_dev[sg.b];
-        const int rows = (int)min((long long)PD_ROWS, (long long)qn * G - f0);
-        for (int r = warp; r < rows; r += PD_WARPS) {
-            float M = -INFINITY;
-            for (int c = lane; c < nc; c += 32) {
-                const float x = __ldcg(state(ca + c) + PD_ROWS * HD + r);
-                wts[r * 512 + c] = x;
-                M = fmaxf(M, x);
-            }
+        if (ms.last[k] < 0) continue;
+        const PdSeg sg = ms.seg[ms.ent[ms.run[ms.last[k]]]];
+        const int ca = pd_cta(sg.u0, N, C_), nc = pd_cta(sg.u1 - 1, N, C_) - ca + 1, rows = rows_of(sg);
+        auto state = [&](int c) {  // the unit's state of its c-th CTA
+            const int cta = ca + c;
+            return P.part + ((size_t)cta * 2 + (sg.u0 < pd_div(cta * N, C_) ? 0 : 1)) * C::STATE;
+        };
+        // warp (r, part): row r, the CTAs part, part + parts, ...
+        const int parts = max(1, PD_WARPS / rows), r = warp / parts, part = warp - r * parts;
+        float M = PD_NONE, L = 0.f, y[V];
 #pragma unroll
-            for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-            const float base = M == -INFINITY ? 0.f : M;
-            for (int c = lane; c < nc; c += 32) wts[r * 512 + c] = ex2(wts[r * 512 + c] - base);
-            if (lane == 0) acc[PD_WARPS * HD + r] = M;
-        }
-        __syncthreads();
-        // warp (r, part): every row's CTAs in `parts` pieces
-        const int parts = max(1, PD_WARPS / rows);
-        float y[V], L = 0.f;
-        const int r = warp / parts, part = warp % parts;
-        const int ra = (int)((long long)part * nc / parts), rb = (int)((long long)(part + 1) * nc / parts);
+        for (int e = 0; e < V; ++e) y[e] = 0.f;
         if (r < rows) {
+            for (int c = lane; c < nc; c += 32) M = fmaxf(M, __ldcg(state(c) + PD_ROWS * HD + r));
 #pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = 0.f;
-#pragma unroll 8
-            for (int c = ra; c < rb; ++c) {
-                const float *st = state(ca + c);
-                const float f = wts[r * 512 + c];
+            for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+#pragma unroll 4
+            for (int c = part; c < nc; c += parts) {
+                const float *st = state(c);
+                const float f = ex2(__ldcg(st + PD_ROWS * HD + r) - M);
                 L += f * __ldcg(st + PD_ROWS * HD + 8 + r);
                 if constexpr (V == 4) {
                     const float4 x = __ldcg(reinterpret_cast<const float4 *>(st + r * HD) + lane);
-                    y[0] += f * x.x; y[1] += f * x.y; y[2] += f * x.z; y[3] += f * x.w;
+                    y[0] += f * x.x; y[1] += f * x.y; y[2] += f * x.z; y[V - 1] += f * x.w;
                 } else {
                     const float2 x = __ldcg(reinterpret_cast<const float2 *>(st + r * HD) + lane);
                     y[0] += f * x.x; y[1] += f * x.y;
                 }
             }
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[warp * HD + V * lane + e] = y[e];
-            if (lane == 0) acc[PD_WARPS * HD + PD_ROWS + warp] = L;
         }
-        __syncthreads();
-        if (r < rows && part == 0) {
-            float z[V], LL = 0.f;
+        if (parts > 1) {
+            __syncthreads();  // the place is free: the states in it, or the other unit's sums, are read
 #pragma unroll
-            for (int e = 0; e < V; ++e) z[e] = 0.f;
-            for (int x = 0; x < parts; ++x) {
-                LL += acc[PD_WARPS * HD + PD_ROWS + warp + x];
+            for (int e = 0; e < V; ++e) acc[warp * (HD + 4) + V * lane + e] = y[e];
+            if (lane == 0) acc[warp * (HD + 4) + HD] = L;
+            __syncthreads();
+            if (part == 0 && r < rows)
+                for (int x = 1; x < parts; ++x) {
+                    L += acc[(warp + x) * (HD + 4) + HD];
 #pragma unroll
-                for (int e = 0; e < V; ++e) z[e] += acc[(warp + x) * HD + V * lane + e];
-            }
-            write_row(sg, r, z, acc[PD_WARPS * HD + r], LL);
+                    for (int e = 0; e < V; ++e) y[e] += acc[(warp + x) * (HD + 4) + V * lane + e];
+                }
         }
-        __syncthreads();
+        if (part == 0 && r < rows) write_row(sg, r, y, M, L);
     }
 }
 
@@ -618,7 +832,7 @@ cudaError_t pages_attn_prepare() {
 }
 
 template <class T>
-static cudaError_t attn_t(const PdArgs &P, int num_sms, cudaStream_t st) {
+static cudaError_t decode_t(const PdArgs &P, int num_sms, cudaStream_t st) {
     if (P.p.hd == 128) pages_decode_kernel<T, 128><<<num_sms, PD_THREADS, PdCfg<128>::SMEM, st>>>(P);
     else pages_decode_kernel<T, 64><<<num_sms, PD_THREADS, PdCfg<64>::SMEM, st>>>(P);
     return cudaGetLastError();
@@ -626,10 +840,18 @@ static cudaError_t attn_t(const PdArgs &P, int num_sms, cudaStream_t st) {
 
 cudaError_t launch_pages_attention(const PagesView &p, const er_pages_attention_args &a, float *part, int *cnt,
                                    int num_sms, cudaStream_t st) {
-    const PdArgs P = {p, a, part, cnt};
-    return a.type == ER_F32   ? attn_t<float>(P, num_sms, st)
-           : a.type == ER_F16 ? attn_t<__half>(P, num_sms, st)
-                              : attn_t<__nv_bfloat16>(P, num_sms, st);
+    for (int b = 0; b < a.n_seqs; b += PD_SEQS) {
+        PdArgs P = {p, a, part, cnt};
+        P.a.n_seqs = a.n_seqs - b < PD_SEQS ? a.n_seqs - b : PD_SEQS;
+        P.a.q_start_dev += b;
+        P.a.lens_dev += b;
+        P.a.tables_dev += (size_t)b * a.table_stride;
+        const cudaError_t e = a.type == ER_F32   ? decode_t<float>(P, num_sms, st)
+                              : a.type == ER_F16 ? decode_t<__half>(P, num_sms, st)
+                                                 : decode_t<__nv_bfloat16>(P, num_sms, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t set_wait_limit_pages(unsigned long long ns) { return set_wait_limit_here(ns); }
