@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "layout.cuh"
+#include "pages.h"
 
 using namespace er;
 

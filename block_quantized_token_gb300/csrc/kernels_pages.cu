@@ -1,8 +1,8 @@
 // The paged 4-bit K/V cache's calls other than attention: block tables and slot
 // maps from request lengths, release, rows in (norm, rotation, quantiser) and out.
 // Layout and quantiser: pages.cuh.
-#include "internal.h"
 #include "pages.cuh"
+#include "pages.h"
 
 namespace er {
 

@@ -32,8 +32,8 @@
 // is carried by their scores instead.
 #include <type_traits>
 
-#include "internal.h"
 #include "pages.cuh"
+#include "pages.h"
 
 namespace er {
 

@@ -1,10 +1,10 @@
-// Entry points of the paged 4-bit K/V cache (include/er.h, er_pages_*): argument checks and ownership.
+// Entry points of the paged 4-bit K/V cache (include/er_pages.h): argument checks and ownership.
 #include <math.h>
 
 #include <new>
 
-#include "internal.h"
 #include "pages.cuh"
+#include "pages.h"
 
 using namespace er;
 

@@ -1,4 +1,4 @@
-"""ctypes binding of liber.so: the same names as include/er.h, argument marshalling only.
+"""ctypes binding of liber.so: the same names as include/er.h and include/er_pages.h, argument marshalling only.
 
 Every function raises ErError when the C call returns a status other than
 ER_OK.  Device pointers are plain integers (e.g. ``tensor.data_ptr()``) and

@@ -173,7 +173,7 @@ def rope_table(head_dim: int, base: float, n_positions: int, device: str = "cuda
 
 
 class PagedCache:
-    """Owns an er_pages handle and, unless given, its pool: a paged 4-bit K/V cache (er_pages_* in er.h).
+    """Owns an er_pages handle and, unless given, its pool: a paged 4-bit K/V cache (er_pages_* in er_pages.h).
 
     Row tensors are [tokens, heads, head_dim] with dense heads and any stride between tokens; int tensors are dense
     int32; all on the cache's device.

@@ -1,5 +1,5 @@
 """Float64 oracle of the paged 4-bit K/V cache: its quantiser, the pool's bytes, block tables, rows and attention
-(test infrastructure; see package doc).  Written from the statement in include/er.h (er_pages_*): numpy, loops, no
+(test infrastructure; see package doc).  Written from the statement in include/er_pages.h: numpy, loops, no
 sharing with the library."""
 
 from __future__ import annotations
