@@ -880,7 +880,7 @@ er_status er_set_wait_limit_ns(uint64_t ns) {
     const unsigned long long v = ns ? (unsigned long long)ns : ER_WAIT_NS;
     cudaError_t (*set[])(unsigned long long) = {set_wait_limit_gemv, set_wait_limit_wide, set_wait_limit_tc,
                                                 set_wait_limit_step_q8, set_wait_limit_step_q4, set_wait_limit_attn,
-                                                set_wait_limit_pages};
+                                                set_wait_limit_pages, set_wait_limit_prompt};
     for (auto f : set) ER_CUDA(f(v));
     return ER_OK;
 }

@@ -166,6 +166,7 @@ constexpr int PD_SUB = 11;
 struct PdArgs {
     PagesView p;
     er_pages_attention_args a;
+    int max_rows;  // sequences with as many query rows a KV head, or more, are another kernel's
     float *part;  // [CTAs][2] states of units that several CTAs share
     int *cnt;     // [CTAs] arrivals, zero between launches
 };
@@ -223,6 +224,8 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
                                  (long long)len > (long long)a.table_stride * R;
                 if (bad) {
                     if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
+                } else if ((long long)(q1 - q0) * G >= P.max_rows) {
+                    ns = 0;
                 } else if (q1 > q0 && len > 0) {
                     ns = (len - 1) / PD_STEP - pd_row0(len, q1 - q0, a.window) / PD_STEP + 1;
                     own[k] = (long long)ns * ((((long long)(q1 - q0) * G + PD_ROWS - 1) / PD_ROWS) * KV);
@@ -823,6 +826,7 @@ static cudaError_t decode_prepare() {
     return cudaFuncSetAttribute(pages_decode_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, PdCfg<HD>::SMEM);
 }
 cudaError_t pages_attn_prepare() {
+    if (cudaError_t e = pages_prompt_prepare(); e != cudaSuccess) return e;
     cudaError_t e[6] = {decode_prepare<float, 64>(), decode_prepare<float, 128>(), decode_prepare<__half, 64>(),
                         decode_prepare<__half, 128>(), decode_prepare<__nv_bfloat16, 64>(),
                         decode_prepare<__nv_bfloat16, 128>()};
@@ -838,10 +842,18 @@ static cudaError_t decode_t(const PdArgs &P, int num_sms, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+// From this many query rows of a KV head on, a sequence goes to the prompt kernel.
+constexpr int PD_PROMPT_ROWS = 64;
+
 cudaError_t launch_pages_attention(const PagesView &p, const er_pages_attention_args &a, float *part, int *cnt,
                                    int num_sms, cudaStream_t st) {
+    // The lengths are on the device, so the split is made there, sequence by sequence; here only what the sizes
+    // rule out: no sequence that long, or (at most a token each on average) a decode step, which stays one launch.
+    const bool prompts = (long long)a.n_tokens * (a.n_heads / p.KV) >= PD_PROMPT_ROWS && (a.n_tokens > a.n_seqs || a.n_seqs == 1);
+    if (prompts)
+        if (cudaError_t e = launch_pages_prompt(p, a, PD_PROMPT_ROWS, st); e != cudaSuccess) return e;
     for (int b = 0; b < a.n_seqs; b += PD_SEQS) {
-        PdArgs P = {p, a, part, cnt};
+        PdArgs P = {p, a, prompts ? PD_PROMPT_ROWS : 2147483647, part, cnt};
         P.a.n_seqs = a.n_seqs - b < PD_SEQS ? a.n_seqs - b : PD_SEQS;
         P.a.q_start_dev += b;
         P.a.lens_dev += b;

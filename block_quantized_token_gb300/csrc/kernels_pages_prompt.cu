@@ -1,0 +1,707 @@
+// Attention over the paged 4-bit K/V cache (pages.cuh) for prompts: many query rows a sequence, on the tcgen05
+// tensor cores.  o = softmax(scale q k^T) v with a running reference m and sums, as in kernels_pages_attn.cu:
+//   p_r = 2^(s_r - m + 7),  l = sum p_r,  o = sum p_r v_r   (s in log2 units; rescaled when a score passes m by 8).
+//
+// Work.  A CTA takes one (sequence, KV head) and two tiles of 128 query rows (a row is a (token, head of the KV
+// head's group), so a group's heads share the cached rows), and walks the cached rows in blocks of 128.
+//   warps 0-3, 4-7  a tile's softmax: thread = row = TMEM lane.  Reads S, writes P over it (fp16, the A operand of
+//                   the second product), keeps m and l, rescales O when it has to, writes the output.
+//   warps 8-11      turn codes into fp16 operands in shared memory, exactly (pages.cuh), K and V K-major with the
+//                   128-byte swizzle; one of them requests the tiles (bulk copies into a ring of 16-row tiles).
+//   warp 12         one thread issues the products: S = Q K^T (M = 128, N = 128), O += P V (N = HD), the two tiles in turn,
+//                   so the tensor cores work on one tile while the other's softmax runs.
+// TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x HD).
+//
+// The block's rows are put in the order k' = 32 a + 8 t + 4 b + 2 i + e for row 32 a + 16 b + 8 i + 2 t + e, in K's rows,
+// hence S's and P's columns, and in V's K dimension: so a thread that holds a code word of V of two 16-row tiles
+// holds 16 bytes of the operand.
+//
+// fp32 rows (SPLIT): queries and probabilities enter as hi + lo fp16 halves (2^-22), two products each; K and V are
+// exact as they are, and have one stage of shared memory instead of two.
+//
+// What bounds it: the products (2 x 1024 cycles a block and two tiles at HD = 128) and next to them the exponentials.
+//
+// Masks.  Blocks that some row attends only in part mask S; there, rows of V that no row of the CTA attends are
+// zeroed (they may hold anything), and a NaN value of V is carried by K instead, so only rows that attend it see it.
+#include "pages.cuh"
+#include "pages.h"
+
+namespace er {
+
+constexpr int PP_WARPS = 16;  // 0-3, 4-7 softmax, 8-11 operands, 12 products (13-15 only give registers)
+constexpr int PP_THREADS = PP_WARPS * 32;
+constexpr int PP_BLOCK = 128;  // cached rows of a block
+constexpr int PP_RAW = 12;     // 16-row tiles in the ring
+constexpr float PP_UP = 7.f, PP_SLACK = 8.f, PP_NONE = -3e38f;
+
+template <int HD, bool SPLIT>
+struct PpCfg {
+    static constexpr int TILE = pg_tile_bytes(HD);
+    static constexpr int NB = HD / 32;
+    static constexpr int OP = 128 * HD * 2;  // bytes of a 128-row operand
+    static constexpr int PARTS = SPLIT ? 2 : 1;
+    static constexpr int NST = SPLIT ? 1 : 2;  // stages of K and of V
+    static constexpr int OFF_Q = 0;            // [tile][part]
+    static constexpr int OFF_K = OFF_Q + 2 * PARTS * OP;
+    static constexpr int OFF_V = OFF_K + NST * OP;
+    static constexpr int OFF_RAW = OFF_V + NST * OP;
+    static constexpr int OFF_BARS = OFF_RAW + PP_RAW * TILE;
+    static constexpr int SMEM = OFF_BARS + 512 + 1024;  // + alignment of the base
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct PpArgs {
+    PagesView p;
+    er_pages_attention_args a;
+    int min_rows;  // sequences with fewer query rows a KV head are another kernel's
+};
+
+struct PpBars {
+    uint64_t raw[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], done;
+    uint32_t tmem;
+    int abort_;
+    int item[4];  // sequence, first query row, KV head, found
+};
+static_assert(sizeof(PpBars) <= 512, "barriers");
+
+// ---------------------------------------------------------------------------
+// tcgen05 wrappers
+// ---------------------------------------------------------------------------
+ER_DEV void pp_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+ER_DEV void pp_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// K-major operand, 128-byte swizzle: atoms of 8 rows x 128 bytes, 1024 bytes apart
+ER_DEV uint64_t pp_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16: fp16 A and B (both K-major), fp32 D, M = 128
+constexpr uint32_t pp_idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24); }
+// D (+)= A B^T, A in shared memory / in TMEM
+ER_DEV void pp_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+ER_DEV void pp_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+ER_DEV void pp_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+ER_DEV void pp_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// 32 consecutive 32-bit columns of this thread's lane
+ER_DEV void pp_st32(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+ER_DEV void pp_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// the loaded registers are valid after pp_wait_ld, which takes them through so that no use moves ahead of it
+ER_DEV void pp_ld32(uint32_t taddr, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+ER_DEV void pp_wait_ld(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
+}
+ER_DEV float pp_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+ER_DEV uint32_t pp_pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// nibble N of each half of w (bits 4 N ..) as the fp16 pair 16 + c, and c's value with scale pair d, z = -24 d
+template <int N>
+ER_DEV uint32_t pp_val(uint32_t w, uint32_t d, uint32_t z) {
+    return h2_fma(lop3_and_or(N == 0 ? w << 6 : N == 1 ? w << 2 : N == 2 ? w >> 2 : w >> 6, 0x03C003C0u, 0x4C004C00u), d, z);
+}
+ER_DEV uint32_t pp_m24(uint32_t d) {
+    __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&d), __halves2half2(__ushort_as_half(0xCE00), __ushort_as_half(0xCE00)));
+    return *reinterpret_cast<uint32_t *>(&r);
+}
+// row of a block at place k' (see the header) and the place of row r
+__host__ __device__ constexpr int pp_row(int k) {
+    return (k & ~31) + ((k >> 2) & 1) * 16 + ((k >> 1) & 1) * 8 + ((k >> 3) & 3) * 2 + (k & 1);
+}
+__host__ __device__ constexpr int pp_place(int r) {
+    return (r & ~31) + ((r >> 1) & 3) * 8 + ((r >> 4) & 1) * 4 + ((r >> 3) & 1) * 2 + (r & 1);
+}
+
+template <class T, int HD>
+__global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArgs P) {
+    constexpr bool SPLIT = sizeof(T) == 4;
+    using C = PpCfg<HD, SPLIT>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // swizzle atoms: 1024-aligned
+    PpBars &B = *reinterpret_cast<PpBars *>(smem + C::OFF_BARS);
+    const er_pages_attention_args &a = P.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int KV = P.p.KV, G = a.n_heads / KV, R = P.p.page_rows;
+
+    // ---- which item this CTA is: (sequence, pair of tiles, KV head), heads fastest, a sequence's last tiles first
+    if (warp == 0) {
+        const int x = blockIdx.x / KV;
+        int found = 0, base = 0;
+        for (int b0 = 0; b0 < a.n_seqs && !found; b0 += 32) {
+            const int b = b0 + lane;
+            int n = 0;
+            if (b < a.n_seqs) {
+                const int q0 = a.q_start_dev[b], q1 = a.q_start_dev[b + 1], len = a.lens_dev[b];
+                if (q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 || (long long)len > (long long)a.table_stride * R) {
+                    if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
+                } else if ((long long)(q1 - q0) * G >= P.min_rows) {
+                    n = (int)(((long long)(q1 - q0) * G + 255) / 256);
+                }
+            }
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const int first = base + inc - n;
+            const bool mine = x >= first && x < first + n;
+            if (mine) {
+                B.item[0] = b;
+                B.item[1] = (n - 1 - (x - first)) * 256;
+                B.item[2] = blockIdx.x % KV;
+            }
+            found = __any_sync(0xffffffffu, mine);
+            base += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) B.item[3] = found;
+    }
+    __syncthreads();
+    if (!B.item[3]) return;
+    const int b = B.item[0], f0 = B.item[1], h = B.item[2];
+    const int q0 = a.q_start_dev[b], qn = a.q_start_dev[b + 1] - q0, len = a.lens_dev[b], past = len - qn;
+    const int nf = (int)min((long long)qn * G - f0, 256ll);  // query rows of this CTA
+    const int nx = nf > 128 ? 2 : 1;                         // tiles
+    // rows that any of them attends, and the blocks of 128 from a 16-row boundary on
+    const int any_hi = past + (f0 + nf - 1) / G;
+    const int any_lo = a.window ? max(0, past + f0 / G - a.window + 1) : 0;
+    const int base = any_lo & ~15;
+    const int nblk = any_hi < 0 ? 0 : (any_hi - base) / PP_BLOCK + 1;
+    // blocks whose rows all of them attend: rows all_lo .. all_hi
+    const int all_hi = past + f0 / G;
+    const int all_lo = a.window ? max(0, any_hi - a.window + 1) : 0;
+
+    if (tid == 0) {
+        for (int i = 0; i < PP_RAW; ++i) mbar_init(B.raw + i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(B.kfull + i, 4);
+            mbar_init(B.kempty + i, 1);
+            mbar_init(B.vfull + i, 4);
+            mbar_init(B.vempty + i, 1);
+            mbar_init(B.s + i, 1);
+            mbar_init(B.p + i, 4);
+            mbar_init(B.o + i, 1);
+        }
+        mbar_init(&B.done, 4);
+        B.abort_ = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // ---- queries: thread = row, a power of two brings its largest value to [2^14, 2^15)
+    const int X = warp >> 2;             // softmax warps: their tile
+    const int r = tid & 127;             // and row of it
+    const bool soft = warp < 8 && X < nx;
+    int row = 0, head = 0, tok = 0;
+    float down = 0.f;
+    if (soft) {
+        const int f = f0 + X * 128 + r;
+        const bool real = X * 128 + r < nf;
+        tok = f / G;
+        row = q0 + tok;
+        head = h * G + (f - tok * G);
+        const T *src = (const T *)a.q_dev + row * a.q_stride + (size_t)head * HD;
+        const bool vec = ((uintptr_t)a.q_dev & 15) == 0 && (a.q_stride * sizeof(T)) % 16 == 0;
+        auto load8 = [&](int c, float (&x)[8]) {
+            __align__(16) T v[8];
+            if (!real) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = pg_cvt<T>(0.f);
+            } else if (vec) {
+#pragma unroll
+                for (int k = 0; k < (int)(8 * sizeof(T)) / 16; ++k)
+                    reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(src + 8 * c)[k];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = src[8 * c + e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = pg_ld<T>(v + e);
+        };
+        float top = 0.f;
+        bool odd = false;
+#pragma unroll 4
+        for (int c = 0; c < HD / 8; ++c) {
+            float x[8];
+            load8(c, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                top = fmaxf(top, fabsf(x[e]));
+                odd |= !(fabsf(x[e]) <= 3.4028235e38f);
+            }
+        }
+        // an infinite or NaN query: the row is NaN, and so are its scores
+        const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 253);
+        const float scale = a.scale != 0.f ? a.scale : 1.f / sqrtf((float)HD);
+        const float up = odd ? NAN : copysignf(__uint_as_float((uint32_t)(268 - ex) << 23), scale);
+        // (a factor too small for fp32 still has to leave -infinity as it is)
+        down = fmaxf(__uint_as_float((uint32_t)(ex - 14) << 23) * (fabsf(scale) * 1.4426950408889634f), 1.2e-38f);
+        uint8_t *dst = smem + C::OFF_Q + X * C::PARTS * C::OP + r * 128;
+#pragma unroll 4
+        for (int c = 0; c < HD / 8; ++c) {
+            float x[8];
+            load8(c, x);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float y0 = x[2 * k] * up, y1 = x[2 * k + 1] * up;
+                hi[k] = pp_pack(y0, y1);
+                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
+                lo[k] = pp_pack(y0 - z.x, y1 - z.y);
+            }
+            uint8_t *d = dst + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (SPLIT) *reinterpret_cast<uint4 *>(d + C::OP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+    }
+    pp_fence_before();
+    __syncthreads();
+    pp_fence_after();
+    const uint32_t tmem = B.tmem;
+    volatile int *abort_s = &B.abort_;
+    auto fail = [&]() {
+        atomicOr(P.p.flags, ER_FLAG_WAIT);
+        *abort_s = 1;
+    };
+    // whole warp: false once a wait gave up here or anywhere
+    auto wait = [&](uint64_t *bar, uint32_t par) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, par));
+        if (!ok && lane == 0) fail();
+        return ok && __all_sync(0xffffffffu, *abort_s == 0);
+    };
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        if (X < nx) {
+            const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
+            const uint32_t tS = tl + X * 128, tO = tl + 256 + X * HD;
+            const bool real = X * 128 + r < nf;
+            const int pos = real ? past + tok : -1;
+            const int first = a.window ? max(0, pos - a.window + 1) : 0;
+            float m = PP_NONE, l = 0.f;
+            bool ok = true;
+            for (int j = 0; j < nblk; ++j) {
+                ok = wait(B.s + X, j & 1);
+                if (!ok) break;
+                pp_fence_after();
+                float s[128];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) pp_ld32(tS + 32 * k, s + 32 * k);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) pp_wait_ld(s + 32 * k);
+                const int r0 = base + PP_BLOCK * j;
+                if (__any_sync(0xffffffffu, r0 < first || r0 + PP_BLOCK - 1 > pos)) {
+                    const int lo = first - r0, hi = pos - r0;
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        if (pp_row(k) < lo || pp_row(k) > hi) s[k] = -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int k = 4; k < 128; k += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[k + e]);
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * down;
+                if (__any_sync(0xffffffffu, mt > m + PP_SLACK)) {
+                    const float mn = mt > m + PP_SLACK ? mt : m;
+                    const float corr = mn == m ? 1.f : pp_ex2(m - mn);
+                    l *= corr;
+                    m = mn;
+                    if (j > 0) {
+#pragma unroll
+                        for (int k = 0; k < HD / 32; ++k) {
+                            float o[32];
+                            pp_ld32(tO + 32 * k, o);
+                            pp_wait_ld(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= corr;
+                            pp_st32(tO + 32 * k, reinterpret_cast<uint32_t *>(o));
+                        }
+                    }
+                }
+                const float nb = PP_UP - m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t ph[32];
+                [[maybe_unused]] uint32_t pl[32];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float p0 = pp_ex2(fmaf(s[64 * half + 2 * k], down, nb)),
+                                    p1 = pp_ex2(fmaf(s[64 * half + 2 * k + 1], down, nb));
+                        sum[(2 * k) & 3] += p0;
+                        sum[(2 * k + 1) & 3] += p1;
+                        ph[k] = pp_pack(p0, p1);
+                        if constexpr (SPLIT) {
+                            const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&ph[k]));
+                            pl[k] = pp_pack(p0 - z.x, p1 - z.y);
+                        }
+                    }
+                    pp_st32(tS + 32 * half, ph);
+                    if constexpr (SPLIT) pp_st32(tS + 64 + 32 * half, pl);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                pp_wait_st();
+                pp_fence_before();
+                __syncwarp();
+                if (lane == 0) pp_arrive(B.p + X);
+            }
+            if (ok && nblk > 0) ok = wait(B.o + X, 0);
+            if (ok) {
+                pp_fence_after();
+                T *out = (T *)a.out_dev + row * a.out_stride + (size_t)head * HD;
+                const bool vec = ((uintptr_t)a.out_dev & 15) == 0 && (a.out_stride * sizeof(T)) % 16 == 0;
+                const float inv = 1.f / l;
+#pragma unroll 1
+                for (int k = 0; k < HD / 32; ++k) {
+                    float o[32];
+                    if (nblk > 0) {
+                        pp_ld32(tO + 32 * k, o);
+                        pp_wait_ld(o);
+                    }
+                    if (!real) continue;
+                    __align__(16) T v[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = pg_cvt<T>(l == 0.f ? 0.f : o[e] * inv);
+                    if (vec) {
+#pragma unroll
+                        for (int e = 0; e < (int)(32 * sizeof(T)) / 16; ++e)
+                            reinterpret_cast<uint4 *>(out + 32 * k)[e] = reinterpret_cast<uint4 *>(v)[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) out[32 * k + e] = v[e];
+                    }
+                }
+                if (real && a.lse_dev)
+                    a.lse_dev[(size_t)row * a.n_heads + head] =
+                        l == 0.f ? -INFINITY : (m - PP_UP + log2f(l)) * 0.6931471805599453f;
+            }
+        }
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        // ---- operands.  16-row tile i of the walk (block i / 8) goes through ring slot i % PP_RAW
+        const int pw = warp - 8, g = lane >> 2, t = lane & 3;
+        const uint8_t *ring = smem + C::OFF_RAW;
+        const int ntile = 8 * nblk;
+        // warp 8, lane: the page of the next tile that the lane requests; tiles i % 8 == lane
+        auto tile_row = [&](int i) { return base + 16 * i; };
+        auto page_of = [&](int i) {
+            if (i >= ntile || tile_row(i) > any_hi) return -2;  // nothing to read there
+            int page = a.tables_dev[(size_t)b * a.table_stride + tile_row(i) / R];
+            if (page < 0 || page >= P.p.n_pages) {
+                atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
+                page = 0;
+            }
+            return page;
+        };
+        auto request = [&](int i, int page) {
+            if (i >= ntile) return;
+            const int slot = i % PP_RAW;
+            mbar_arrive_expect_tx(B.raw + slot, page >= 0 ? C::TILE : 0);
+            if (page >= 0)
+                bulk_g2s(smem + C::OFF_RAW + slot * C::TILE,
+                         P.p.pool + (((size_t)page * KV + h) * (R >> 4) + ((tile_row(i) % R) >> 4)) * C::TILE, C::TILE,
+                         B.raw + slot);
+        };
+        int want = lane, page = -2;  // the next tile that this lane requests, and its page
+        if (pw == 0) {
+            if (lane < 8) {
+                request(lane, page_of(lane));
+                if (lane < PP_RAW - 8) request(8 + lane, page_of(8 + lane));
+                want = lane < PP_RAW - 8 ? 16 + lane : 8 + lane;
+                page = page_of(want);
+            }
+        }
+        bool ok = true;
+        int j = 0;
+        for (; j < nblk; ++j) {
+            const int st = C::NST == 2 ? j & 1 : 0, ph = C::NST == 2 ? (j >> 1) & 1 : j & 1;
+            for (int i = 8 * j; ok && i < 8 * j + 8; ++i) ok = wait(B.raw + i % PP_RAW, (i / PP_RAW) & 1);
+            if (!ok) break;
+            const int r0 = base + PP_BLOCK * j;
+            const bool edge = r0 < all_lo || r0 + PP_BLOCK - 1 > all_hi;
+            // ---- K: a job is 8 rows, a lane one row's words of quad lane t
+            if (j >= C::NST) ok = wait(B.kempty + st, ph ^ 1);
+            if (!ok) break;
+            uint8_t *kd = smem + C::OFF_K + st * C::OP;
+#pragma unroll 2
+            for (int job = 0; job < 4; ++job) {
+                const int rr = 8 * (4 * pw + job) + g, in = rr & 15;
+                const uint8_t *src = ring + ((8 * j + (rr >> 4)) % PP_RAW) * C::TILE;
+                uint32_t w[C::NB], ds[C::NB / 2];
+                if constexpr (HD == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src + in * 64 + t * 16);
+                    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[C::NB - 1] = x.w;
+                    const uint2 y = *reinterpret_cast<const uint2 *>(src + pg_off_ks(HD) + in * 8);
+                    ds[0] = y.x; ds[C::NB / 2 - 1] = y.y;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(src + in * 32 + t * 8);
+                    w[0] = x.x; w[1] = x.y;
+                    ds[0] = *reinterpret_cast<const uint32_t *>(src + pg_off_ks(HD) + in * 4);
+                }
+                if (edge) {  // a row with a NaN value: its K carries it
+                    const unsigned short *vs = reinterpret_cast<const unsigned short *>(src + pg_off_vs(HD));
+                    bool nan = false;
+#pragma unroll
+                    for (int bb = 0; bb < C::NB; ++bb) nan |= (vs[pg_vs_half(in, bb, HD)] & 0x7FFF) > 0x7C00;
+                    if (nan)
+#pragma unroll
+                        for (int k = 0; k < C::NB / 2; ++k) ds[k] = 0x7FFF7FFFu;
+                }
+                const int n = pp_place(rr);
+                uint8_t *dst = kd + n * 128;
+                // an odd row writes its blocks in the other order: 8 lanes then cover all the bank groups
+#pragma unroll
+                for (int k = 0; k < C::NB; ++k) {
+                    const uint32_t ww = (g & 1) ? w[k ^ 1] : w[k];
+                    const int bb = (g & 1) ? k ^ 1 : k;
+                    const uint32_t dd = ds[k >> 1], d = prmt(dd, dd, (bb & 1) ? 0x3232u : 0x1010u), z = pp_m24(d);
+                    *reinterpret_cast<uint4 *>(dst + (k >> 1) * 16384 + (((4 * (bb & 1) + t) ^ (n & 7)) << 4)) =
+                        make_uint4(pp_val<0>(ww, d, z), pp_val<1>(ww, d, z), pp_val<2>(ww, d, z), pp_val<3>(ww, d, z));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.kfull + st);
+            // ---- V: a lane holds 4 rows of one dim of two tiles: 16 bytes of the operand
+            if (j >= C::NST) ok = wait(B.vempty + st, ph ^ 1);
+            if (!ok) break;
+            uint8_t *vd = smem + C::OFF_V + st * C::OP;
+            const int half = pw >> 1, q = HD == 128 ? pw & 1 : 0;
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+                const int pair = 2 * half + (k ^ (g & 1));  // odd g takes the pairs in the other order (bank groups again)
+                const uint8_t *sa = ring + ((8 * j + 2 * pair) % PP_RAW) * C::TILE,
+                              *sb = ring + ((8 * j + 2 * pair + 1) % PP_RAW) * C::TILE;
+                constexpr int NU = HD == 128 ? 4 : 2;  // words of a lane (HD = 64: a warp takes half of them)
+                const int u0 = HD == 128 ? 0 : 2 * (pw & 1);
+                uint32_t wa[NU], wb[NU], da[NU / 2][2], db[NU / 2][2];
+                if constexpr (HD == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(sa + pg_off_v(HD) + q * 512 + lane * 16);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(sb + pg_off_v(HD) + q * 512 + lane * 16);
+                    wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[NU - 1] = x.w;
+                    wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[NU - 1] = y.w;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(sa + pg_off_vs(HD) + t * 32 + 16 * q);
+                    const uint4 z = *reinterpret_cast<const uint4 *>(sb + pg_off_vs(HD) + t * 32 + 16 * q);
+                    da[0][0] = v.x; da[0][1] = v.y; da[NU / 2 - 1][0] = v.z; da[NU / 2 - 1][1] = v.w;
+                    db[0][0] = z.x; db[0][1] = z.y; db[NU / 2 - 1][0] = z.z; db[NU / 2 - 1][1] = z.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(sa + pg_off_v(HD) + lane * 16 + 4 * u0);
+                    const uint2 y = *reinterpret_cast<const uint2 *>(sb + pg_off_v(HD) + lane * 16 + 4 * u0);
+                    wa[0] = x.x; wa[1] = x.y;
+                    wb[0] = y.x; wb[1] = y.y;
+                    const uint2 v = *reinterpret_cast<const uint2 *>(sa + pg_off_vs(HD) + t * 16 + 4 * u0);
+                    const uint2 z = *reinterpret_cast<const uint2 *>(sb + pg_off_vs(HD) + t * 16 + 4 * u0);
+                    da[0][0] = v.x; da[0][1] = v.y;
+                    db[0][0] = z.x; db[0][1] = z.y;
+                }
+                if (edge) {  // scales of rows that nobody attends, or that are NaN: 0
+#pragma unroll
+                    for (int x = 0; x < NU / 2; ++x)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t part = e ? 0xFFFF0000u : 0x0000FFFFu, inf = 0x7C007C00u & part;
+                                const int ra = r0 + 32 * pair + 2 * t + e + 8 * i, rb = ra + 16;
+                                if ((da[x][i] & 0x7FFF7FFFu & part) > inf || ra < any_lo || ra > any_hi) da[x][i] &= ~part;
+                                if ((db[x][i] & 0x7FFF7FFFu & part) > inf || rb < any_lo || rb > any_hi) db[x][i] &= ~part;
+                            }
+                }
+                uint8_t *dst = vd + half * (HD * 128) + ((((pair & 1) * 4 + t) ^ g) << 4);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    const uint32_t a0 = da[u >> 1][0], a1 = da[u >> 1][1], b0 = db[u >> 1][0], b1 = db[u >> 1][1];
+                    const uint32_t za0 = pp_m24(a0), za1 = pp_m24(a1), zb0 = pp_m24(b0), zb1 = pp_m24(b1);
+                    const int d = 64 * q + 16 * (u0 + u) + g;
+                    *reinterpret_cast<uint4 *>(dst + d * 128) =
+                        make_uint4(pp_val<0>(wa[u], a0, za0), pp_val<2>(wa[u], a1, za1), pp_val<0>(wb[u], b0, zb0),
+                                   pp_val<2>(wb[u], b1, zb1));
+                    *reinterpret_cast<uint4 *>(dst + (d + 8) * 128) =
+                        make_uint4(pp_val<1>(wa[u], a0, za0), pp_val<3>(wa[u], a1, za1), pp_val<1>(wb[u], b0, zb0),
+                                   pp_val<3>(wb[u], b1, zb1));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.vfull + st);
+            // the block's raw tiles are read by all four warps: their slots take the next ones
+            if (lane == 0) pp_arrive(&B.done);
+            if (pw == 0) {
+                ok = wait(&B.done, j & 1);
+                if (!ok) break;
+                if (lane < 8) {  // tiles 8 j + PP_RAW .. + 7, each by the lane that holds its page
+                    request(want, page);
+                    want += 8;
+                    page = page_of(want);
+                }
+                __syncwarp();
+            }
+        }
+        // given up: copies may still be landing
+        if (!ok && pw == 0) {
+            __syncwarp();
+            const int last = min(ntile, 8 * j + PP_RAW);
+            for (int i = max(0, last - PP_RAW); i < last; ++i) mbar_wait(B.raw + i % PP_RAW, (i / PP_RAW) & 1);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 12 && nblk > 0) {
+            // ---- products, issued by one thread; the whole warp waits
+            const uint32_t qb = smem_u32(smem + C::OFF_Q), kb = smem_u32(smem + C::OFF_K), vb = smem_u32(smem + C::OFF_V);
+            constexpr uint32_t ID_S = pp_idesc(128), ID_O = pp_idesc(HD);
+            auto score = [&](int x, int st) {  // S_x = Q_x K^T
+#pragma unroll
+                for (int part = 0; part < C::PARTS; ++part)
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) {
+                        const uint32_t at = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
+                        pp_mma_ss(tmem + x * 128, pp_desc(qb + (x * C::PARTS + part) * C::OP + at), pp_desc(kb + st * C::OP + at),
+                                  ID_S, part + k > 0);
+                    }
+            };
+            auto value = [&](int x, int st, bool more) {  // O_x (+)= P_x V
+#pragma unroll
+                for (int part = 0; part < C::PARTS; ++part)
+#pragma unroll
+                    for (int k = 0; k < PP_BLOCK / 16; ++k)
+                        pp_mma_ts(tmem + 256 + x * HD, tmem + x * 128 + part * 64 + k * 8,
+                                  pp_desc(vb + st * C::OP + (k >> 2) * (HD * 128) + (k & 3) * 32), ID_O, more || part + k > 0);
+            };
+            bool ok = wait(B.kfull + 0, 0);
+            if (ok) {
+                pp_fence_after();
+                if (lane == 0) {
+                    for (int x = 0; x < nx; ++x) {
+                        score(x, 0);
+                        pp_commit(B.s + x);
+                    }
+                    pp_commit(B.kempty + 0);
+                }
+                __syncwarp();
+            }
+            for (int j = 0; ok && j < nblk; ++j) {
+                const int st = C::NST == 2 ? j & 1 : 0, ph = C::NST == 2 ? (j >> 1) & 1 : j & 1;
+                const int j1 = j + 1, st1 = C::NST == 2 ? j1 & 1 : 0, ph1 = C::NST == 2 ? (j1 >> 1) & 1 : j1 & 1;
+                ok = wait(B.vfull + st, ph);
+                for (int x = 0; ok && x < nx; ++x) {
+                    ok = wait(B.p + x, j & 1);
+                    if (!ok) break;
+                    pp_fence_after();
+                    if (lane == 0) {
+                        value(x, st, j > 0);
+                        if (x == nx - 1) pp_commit(B.vempty + st);
+                        if (j1 == nblk) pp_commit(B.o + x);
+                    }
+                    __syncwarp();
+                    if (j1 < nblk) {
+                        if (x == 0) ok = wait(B.kfull + st1, ph1);
+                        if (!ok) break;
+                        pp_fence_after();
+                        if (lane == 0) {
+                            score(x, st1);
+                            pp_commit(B.s + x);
+                            if (x == nx - 1) pp_commit(B.kempty + st1);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (!ok) {  // given up: products in flight read shared memory and TMEM until they end
+                if (lane == 0) pp_commit(B.o);
+                __syncwarp();
+                for (int k = 0; k < 2; ++k) mbar_wait(B.o, k);
+            }
+        }
+    }
+    __syncwarp();
+    pp_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        pp_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+template <class T, int HD>
+static cudaError_t prompt_prepare() {
+    return cudaFuncSetAttribute(pages_prompt_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PpCfg<HD, sizeof(T) == 4>::SMEM);
+}
+cudaError_t pages_prompt_prepare() {
+    cudaError_t e[6] = {prompt_prepare<float, 64>(), prompt_prepare<float, 128>(), prompt_prepare<__half, 64>(),
+                        prompt_prepare<__half, 128>(), prompt_prepare<__nv_bfloat16, 64>(),
+                        prompt_prepare<__nv_bfloat16, 128>()};
+    for (cudaError_t x : e)
+        if (x != cudaSuccess) return x;
+    return cudaSuccess;
+}
+
+template <class T>
+static cudaError_t prompt_t(const PpArgs &P, unsigned grid, cudaStream_t st) {
+    constexpr bool S = sizeof(T) == 4;
+    if (P.p.hd == 128) pages_prompt_kernel<T, 128><<<grid, PP_THREADS, PpCfg<128, S>::SMEM, st>>>(P);
+    else pages_prompt_kernel<T, 64><<<grid, PP_THREADS, PpCfg<64, S>::SMEM, st>>>(P);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_prompt(const PagesView &p, const er_pages_attention_args &a, int min_rows, cudaStream_t st) {
+    const PpArgs P = {p, a, min_rows};
+    const long long G = a.n_heads / p.KV;
+    const long long items = ((long long)a.n_tokens * G + 255) / 256 + (a.n_seqs < a.n_tokens ? a.n_seqs : a.n_tokens);
+    if (items * p.KV > 2147483647ll) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)(items * p.KV);
+    return a.type == ER_F32   ? prompt_t<float>(P, grid, st)
+           : a.type == ER_F16 ? prompt_t<__half>(P, grid, st)
+                              : prompt_t<__nv_bfloat16>(P, grid, st);
+}
+
+cudaError_t set_wait_limit_prompt(unsigned long long ns) { return set_wait_limit_here(ns); }
+
+}  // namespace er

@@ -29,6 +29,10 @@ cudaError_t launch_pages_attention(const PagesView &p, const er_pages_attention_
                                    int num_sms, cudaStream_t st);
 size_t pages_attn_part_floats(int num_sms);  // `part`; cnt: one int per SM, zero
 cudaError_t pages_attn_prepare();            // kernel attributes
+// sequences with at least min_rows query rows a KV head (kernels_pages_prompt.cu)
+cudaError_t launch_pages_prompt(const PagesView &p, const er_pages_attention_args &a, int min_rows, cudaStream_t st);
+cudaError_t pages_prompt_prepare();
+cudaError_t set_wait_limit_prompt(unsigned long long ns);
 cudaError_t set_wait_limit_pages(unsigned long long ns);
 
 }  // namespace er
