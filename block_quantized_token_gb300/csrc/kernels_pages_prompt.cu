@@ -7,9 +7,10 @@
 //   warps 0-3, 4-7  a tile's softmax: thread = row = TMEM lane.  Reads S, writes P over it (fp16, the A operand of
 //                   the second product), keeps m and l, rescales O when it has to, writes the output.
 //   warps 8-11      turn codes into fp16 operands in shared memory, exactly (pages.cuh), K and V K-major with the
-//                   128-byte swizzle; one of them requests the tiles (bulk copies into a ring of 16-row tiles).
+//                   128-byte swizzle.
 //   warp 12         one thread issues the products: S = Q K^T (M = 128, N = 128), O += P V (N = HD), the two tiles in turn,
 //                   so the tensor cores work on one tile while the other's softmax runs.
+//   warp 13         requests the cached tiles: bulk copies into a ring of half blocks, each used by two operand warps.
 // TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x HD).
 //
 // The block's rows are put in the order k' = 32 a + 8 t + 4 b + 2 i + e for row 32 a + 16 b + 8 i + 2 t + e, in K's rows,
@@ -28,10 +29,10 @@
 
 namespace er {
 
-constexpr int PP_WARPS = 16;  // 0-3, 4-7 softmax, 8-11 operands, 12 products (13-15 only give registers)
+constexpr int PP_WARPS = 16;  // 0-3, 4-7 softmax, 8-11 operands, 12 products, 13 copies (14, 15 only give registers)
 constexpr int PP_THREADS = PP_WARPS * 32;
 constexpr int PP_BLOCK = 128;  // cached rows of a block
-constexpr int PP_RAW = 12;     // 16-row tiles in the ring
+constexpr int PP_RAW = 3;      // half blocks (four 16-row tiles) in the ring
 constexpr float PP_UP = 7.f, PP_SLACK = 8.f, PP_NONE = -3e38f;
 
 template <int HD, bool SPLIT>
@@ -45,7 +46,7 @@ struct PpCfg {
     static constexpr int OFF_K = OFF_Q + 2 * PARTS * OP;
     static constexpr int OFF_V = OFF_K + NST * OP;
     static constexpr int OFF_RAW = OFF_V + NST * OP;
-    static constexpr int OFF_BARS = OFF_RAW + PP_RAW * TILE;
+    static constexpr int OFF_BARS = OFF_RAW + PP_RAW * 4 * TILE;
     static constexpr int SMEM = OFF_BARS + 512 + 1024;  // + alignment of the base
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -57,9 +58,8 @@ struct PpArgs {
 };
 
 struct PpBars {
-    uint64_t raw[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], done;
+    uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2];
     uint32_t tmem;
-    int abort_;
     int item[4];  // sequence, first query row, KV head, found
 };
 static_assert(sizeof(PpBars) <= 512, "barriers");
@@ -76,22 +76,35 @@ ER_DEV uint64_t pp_desc(uint32_t saddr) {
 }
 // kind::f16: fp16 A and B (both K-major), fp32 D, M = 128
 constexpr uint32_t pp_idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24); }
-// D (+)= A B^T, A in shared memory / in TMEM
-ER_DEV void pp_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The products are issued by code that the whole warp runs with equal operands (so they can sit in uniform
+// registers); only the lane with `one` set issues.  D (+)= A B^T, A in shared memory / in TMEM.
+ER_DEV void pp_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate), "r"(one)
         : "memory");
 }
-ER_DEV void pp_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+ER_DEV void pp_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(accumulate), "r"(one)
         : "memory");
 }
-ER_DEV void pp_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+// the mbarrier arrives once every product that this thread issued before has completed
+ER_DEV void pp_commit(uint64_t *bar, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(one)
+        : "memory");
+}
+ER_DEV uint32_t pp_elect() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
 }
 ER_DEV void pp_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -105,6 +118,13 @@ ER_DEV void pp_st32(uint32_t taddr, const uint32_t *v) {
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
         "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+ER_DEV void pp_st16(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 ER_DEV void pp_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -132,6 +152,24 @@ ER_DEV float pp_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// two fp32 operations an instruction
+ER_DEV float2 pp_fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)), "l"(*reinterpret_cast<uint64_t *>(&c)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+ER_DEV float2 pp_add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+ER_DEV float pp_max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 ER_DEV uint32_t pp_pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -162,7 +200,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // swizzle atoms: 1024-aligned
     PpBars &B = *reinterpret_cast<PpBars *>(smem + C::OFF_BARS);
     const er_pages_attention_args &a = P.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // so that the compiler knows it is the same in the whole warp
     const int KV = P.p.KV, G = a.n_heads / KV, R = P.p.page_rows;
 
     // ---- which item this CTA is: (sequence, pair of tiles, KV head), heads fastest, a sequence's last tiles first
@@ -214,7 +253,10 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
     const int all_lo = a.window ? max(0, any_hi - a.window + 1) : 0;
 
     if (tid == 0) {
-        for (int i = 0; i < PP_RAW; ++i) mbar_init(B.raw + i, 1);
+        for (int i = 0; i < PP_RAW; ++i) {
+            mbar_init(B.raw + i, 1);
+            mbar_init(B.rawfree + i, 2);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(B.kfull + i, 4);
             mbar_init(B.kempty + i, 1);
@@ -224,8 +266,6 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
             mbar_init(B.p + i, 4);
             mbar_init(B.o + i, 1);
         }
-        mbar_init(&B.done, 4);
-        B.abort_ = 0;
         fence_mbar_init();
     }
     if (warp == 12) {
@@ -303,21 +343,18 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
     pp_fence_before();
     __syncthreads();
     pp_fence_after();
-    const uint32_t tmem = B.tmem;
-    volatile int *abort_s = &B.abort_;
-    auto fail = [&]() {
-        atomicOr(P.p.flags, ER_FLAG_WAIT);
-        *abort_s = 1;
-    };
-    // whole warp: false once a wait gave up here or anywhere
+    // the whole of TMEM is allocated: it starts at 0, which keeps its addresses constants
+    constexpr uint32_t tmem = 0;
+    // Whole warp: false once a wait gave up.  What depends on a warp that gave up waits in vain and gives up too, so
+    // every wait ends.
     auto wait = [&](uint64_t *bar, uint32_t par) {
         const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, par));
-        if (!ok && lane == 0) fail();
-        return ok && __all_sync(0xffffffffu, *abort_s == 0);
+        if (!ok && lane == 0) atomicOr(P.p.flags, ER_FLAG_WAIT);
+        return ok;
     };
 
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         if (X < nx) {
             const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
             const uint32_t tS = tl + X * 128, tO = tl + 256 + X * HD;
@@ -344,10 +381,10 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int k = 4; k < 128; k += 4)
+                for (int k = 4; k < 124; k += 8)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[k + e]);
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * down;
+                    for (int e = 0; e < 4; ++e) mx[e] = pp_max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
+                const float mt = pp_max3(pp_max3(mx[0], mx[1], fmaxf(s[124], s[125])), pp_max3(mx[2], mx[3], s[126]), s[127]) * down;
                 if (__any_sync(0xffffffffu, mt > m + PP_SLACK)) {
                     const float mn = mt > m + PP_SLACK ? mt : m;
                     const float corr = mn == m ? 1.f : pp_ex2(m - mn);
@@ -365,28 +402,28 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                         }
                     }
                 }
-                const float nb = PP_UP - m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t ph[32];
-                [[maybe_unused]] uint32_t pl[32];
+                const float2 nb = make_float2(PP_UP - m, PP_UP - m), dn = make_float2(down, down);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int q = 0; q < 4; ++q) {  // 32 columns of S become 16 of P: few registers beside S itself
+                    uint32_t ph[16];
+                    [[maybe_unused]] uint32_t pl[16];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float p0 = pp_ex2(fmaf(s[64 * half + 2 * k], down, nb)),
-                                    p1 = pp_ex2(fmaf(s[64 * half + 2 * k + 1], down, nb));
-                        sum[(2 * k) & 3] += p0;
-                        sum[(2 * k + 1) & 3] += p1;
-                        ph[k] = pp_pack(p0, p1);
+                    for (int k = 0; k < 16; ++k) {
+                        float2 x = pp_fma2(make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), dn, nb);
+                        x.x = pp_ex2(x.x);
+                        x.y = pp_ex2(x.y);
+                        sum[k & 1] = pp_add2(sum[k & 1], x);
+                        ph[k] = pp_pack(x.x, x.y);
                         if constexpr (SPLIT) {
                             const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&ph[k]));
-                            pl[k] = pp_pack(p0 - z.x, p1 - z.y);
+                            pl[k] = pp_pack(x.x - z.x, x.y - z.y);
                         }
                     }
-                    pp_st32(tS + 32 * half, ph);
-                    if constexpr (SPLIT) pp_st32(tS + 64 + 32 * half, pl);
+                    pp_st16(tS + 16 * q, ph);
+                    if constexpr (SPLIT) pp_st16(tS + 64 + 16 * q, pl);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 pp_wait_st();
                 pp_fence_before();
                 __syncwarp();
@@ -424,46 +461,18 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
             }
         }
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        // ---- operands.  16-row tile i of the walk (block i / 8) goes through ring slot i % PP_RAW
-        const int pw = warp - 8, g = lane >> 2, t = lane & 3;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        // ---- operands.  Half block i of the walk (block i / 2) lies in ring slot i % PP_RAW; warps 8, 9 use the first
+        // halves, 10 and 11 the second
+        const int pw = warp - 8, g = lane >> 2, t = lane & 3, half = pw >> 1;
         const uint8_t *ring = smem + C::OFF_RAW;
-        const int ntile = 8 * nblk;
-        // warp 8, lane: the page of the next tile that the lane requests; tiles i % 8 == lane
-        auto tile_row = [&](int i) { return base + 16 * i; };
-        auto page_of = [&](int i) {
-            if (i >= ntile || tile_row(i) > any_hi) return -2;  // nothing to read there
-            int page = a.tables_dev[(size_t)b * a.table_stride + tile_row(i) / R];
-            if (page < 0 || page >= P.p.n_pages) {
-                atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
-                page = 0;
-            }
-            return page;
-        };
-        auto request = [&](int i, int page) {
-            if (i >= ntile) return;
-            const int slot = i % PP_RAW;
-            mbar_arrive_expect_tx(B.raw + slot, page >= 0 ? C::TILE : 0);
-            if (page >= 0)
-                bulk_g2s(smem + C::OFF_RAW + slot * C::TILE,
-                         P.p.pool + (((size_t)page * KV + h) * (R >> 4) + ((tile_row(i) % R) >> 4)) * C::TILE, C::TILE,
-                         B.raw + slot);
-        };
-        int want = lane, page = -2;  // the next tile that this lane requests, and its page
-        if (pw == 0) {
-            if (lane < 8) {
-                request(lane, page_of(lane));
-                if (lane < PP_RAW - 8) request(8 + lane, page_of(8 + lane));
-                want = lane < PP_RAW - 8 ? 16 + lane : 8 + lane;
-                page = page_of(want);
-            }
-        }
         bool ok = true;
-        int j = 0;
-        for (; j < nblk; ++j) {
+        int slot = half, par = 0;  // of half block 2 j + half
+        for (int j = 0; j < nblk; ++j) {
             const int st = C::NST == 2 ? j & 1 : 0, ph = C::NST == 2 ? (j >> 1) & 1 : j & 1;
-            for (int i = 8 * j; ok && i < 8 * j + 8; ++i) ok = wait(B.raw + i % PP_RAW, (i / PP_RAW) & 1);
+            ok = wait(B.raw + slot, par);
             if (!ok) break;
+            const uint8_t *raw = ring + slot * (4 * C::TILE);
             const int r0 = base + PP_BLOCK * j;
             const bool edge = r0 < all_lo || r0 + PP_BLOCK - 1 > all_hi;
             // ---- K: a job is 8 rows, a lane one row's words of quad lane t
@@ -473,7 +482,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
 #pragma unroll 2
             for (int job = 0; job < 4; ++job) {
                 const int rr = 8 * (4 * pw + job) + g, in = rr & 15;
-                const uint8_t *src = ring + ((8 * j + (rr >> 4)) % PP_RAW) * C::TILE;
+                const uint8_t *src = raw + ((rr >> 4) & 3) * C::TILE;
                 uint32_t w[C::NB], ds[C::NB / 2];
                 if constexpr (HD == 128) {
                     const uint4 x = *reinterpret_cast<const uint4 *>(src + in * 64 + t * 16);
@@ -513,12 +522,11 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
             if (j >= C::NST) ok = wait(B.vempty + st, ph ^ 1);
             if (!ok) break;
             uint8_t *vd = smem + C::OFF_V + st * C::OP;
-            const int half = pw >> 1, q = HD == 128 ? pw & 1 : 0;
+            const int q = HD == 128 ? pw & 1 : 0;
 #pragma unroll 1
             for (int k = 0; k < 2; ++k) {
                 const int pair = 2 * half + (k ^ (g & 1));  // odd g takes the pairs in the other order (bank groups again)
-                const uint8_t *sa = ring + ((8 * j + 2 * pair) % PP_RAW) * C::TILE,
-                              *sb = ring + ((8 * j + 2 * pair + 1) % PP_RAW) * C::TILE;
+                const uint8_t *sa = raw + (2 * pair & 3) * C::TILE, *sb = sa + C::TILE;
                 constexpr int NU = HD == 128 ? 4 : 2;  // words of a lane (HD = 64: a warp takes half of them)
                 const int u0 = HD == 128 ? 0 : 2 * (pw & 1);
                 uint32_t wa[NU], wb[NU], da[NU / 2][2], db[NU / 2][2];
@@ -571,39 +579,28 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) pp_arrive(B.vfull + st);
-            // the block's raw tiles are read by all four warps: their slots take the next ones
-            if (lane == 0) pp_arrive(&B.done);
-            if (pw == 0) {
-                ok = wait(&B.done, j & 1);
-                if (!ok) break;
-                if (lane < 8) {  // tiles 8 j + PP_RAW .. + 7, each by the lane that holds its page
-                    request(want, page);
-                    want += 8;
-                    page = page_of(want);
-                }
-                __syncwarp();
+            if (lane == 0) pp_arrive(B.rawfree + slot);
+            slot += 2;
+            if (slot >= PP_RAW) {
+                slot -= PP_RAW;
+                par ^= 1;
             }
         }
-        // given up: copies may still be landing
-        if (!ok && pw == 0) {
-            __syncwarp();
-            const int last = min(ntile, 8 * j + PP_RAW);
-            for (int i = max(0, last - PP_RAW); i < last; ++i) mbar_wait(B.raw + i % PP_RAW, (i / PP_RAW) & 1);
-        }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
         if (warp == 12 && nblk > 0) {
             // ---- products, issued by one thread; the whole warp waits
             const uint32_t qb = smem_u32(smem + C::OFF_Q), kb = smem_u32(smem + C::OFF_K), vb = smem_u32(smem + C::OFF_V);
             constexpr uint32_t ID_S = pp_idesc(128), ID_O = pp_idesc(HD);
+            const uint32_t one = pp_elect();
             auto score = [&](int x, int st) {  // S_x = Q_x K^T
 #pragma unroll
                 for (int part = 0; part < C::PARTS; ++part)
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k) {
                         const uint32_t at = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
-                        pp_mma_ss(tmem + x * 128, pp_desc(qb + (x * C::PARTS + part) * C::OP + at), pp_desc(kb + st * C::OP + at),
-                                  ID_S, part + k > 0);
+                        pp_mma_ss(tmem + x * 128, pp_desc(qb + (x * C::PARTS + part) * C::OP) + (at >> 4),
+                                  pp_desc(kb + st * C::OP) + (at >> 4), ID_S, part + k > 0, one);
                     }
             };
             auto value = [&](int x, int st, bool more) {  // O_x (+)= P_x V
@@ -612,19 +609,17 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
 #pragma unroll
                     for (int k = 0; k < PP_BLOCK / 16; ++k)
                         pp_mma_ts(tmem + 256 + x * HD, tmem + x * 128 + part * 64 + k * 8,
-                                  pp_desc(vb + st * C::OP + (k >> 2) * (HD * 128) + (k & 3) * 32), ID_O, more || part + k > 0);
+                                  pp_desc(vb + st * C::OP) + (((k >> 2) * (HD * 128) + (k & 3) * 32) >> 4), ID_O,
+                                  more || part + k > 0, one);
             };
             bool ok = wait(B.kfull + 0, 0);
             if (ok) {
                 pp_fence_after();
-                if (lane == 0) {
-                    for (int x = 0; x < nx; ++x) {
-                        score(x, 0);
-                        pp_commit(B.s + x);
-                    }
-                    pp_commit(B.kempty + 0);
+                for (int x = 0; x < nx; ++x) {
+                    score(x, 0);
+                    pp_commit(B.s + x, one);
                 }
-                __syncwarp();
+                pp_commit(B.kempty + 0, one);
             }
             for (int j = 0; ok && j < nblk; ++j) {
                 const int st = C::NST == 2 ? j & 1 : 0, ph = C::NST == 2 ? (j >> 1) & 1 : j & 1;
@@ -634,30 +629,59 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                     ok = wait(B.p + x, j & 1);
                     if (!ok) break;
                     pp_fence_after();
-                    if (lane == 0) {
-                        value(x, st, j > 0);
-                        if (x == nx - 1) pp_commit(B.vempty + st);
-                        if (j1 == nblk) pp_commit(B.o + x);
-                    }
-                    __syncwarp();
-                    if (j1 < nblk) {
+                    value(x, st, j > 0);
+                    if (x == nx - 1) pp_commit(B.vempty + st, one);
+                    if (j1 == nblk) {
+                        pp_commit(B.o + x, one);
+                    } else {
                         if (x == 0) ok = wait(B.kfull + st1, ph1);
                         if (!ok) break;
                         pp_fence_after();
-                        if (lane == 0) {
-                            score(x, st1);
-                            pp_commit(B.s + x);
-                            if (x == nx - 1) pp_commit(B.kempty + st1);
-                        }
-                        __syncwarp();
+                        score(x, st1);
+                        pp_commit(B.s + x, one);
+                        if (x == nx - 1) pp_commit(B.kempty + st1, one);
                     }
                 }
             }
             if (!ok) {  // given up: products in flight read shared memory and TMEM until they end
-                if (lane == 0) pp_commit(B.o);
-                __syncwarp();
+                pp_commit(B.o, one);
                 for (int k = 0; k < 2; ++k) mbar_wait(B.o, k);
             }
+        } else if (warp == 13 && nblk > 0) {
+            // ---- copies: lane i < 4 requests tile i of each half block; the pages are looked up one half block ahead
+            const int nhalf = 2 * nblk;
+            auto page_of = [&](int i) {  // the table's entry for tile `lane` of half block i; -1: nothing to read there
+                const int row = base + 64 * i + 16 * lane;
+                return lane < 4 && i < nhalf && row <= any_hi ? a.tables_dev[(size_t)b * a.table_stride + row / R] : -1;
+            };
+            int page = page_of(0), slot = 0, par = 1;
+            bool ok = true;
+            int i = 0;
+            for (; i < nhalf; ++i) {
+                if (i >= PP_RAW) ok = wait(B.rawfree + slot, par);
+                if (!ok) break;
+                const int row = base + 64 * i + 16 * lane;
+                const bool there = lane < 4 && row <= any_hi;
+                if (there && (page < 0 || page >= P.p.n_pages)) {
+                    atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
+                    page = 0;
+                }
+                const int n = __popc(__ballot_sync(0xffffffffu, there));
+                if (lane == 0) mbar_arrive_expect_tx(B.raw + slot, n * C::TILE);
+                __syncwarp();
+                if (there)
+                    bulk_g2s(smem + C::OFF_RAW + (slot * 4 + lane) * C::TILE,
+                             P.p.pool + (((size_t)page * KV + h) * (R >> 4) + ((row % R) >> 4)) * C::TILE, C::TILE,
+                             B.raw + slot);
+                page = page_of(i + 1);
+                if (++slot == PP_RAW) {
+                    slot = 0;
+                    par ^= 1;
+                }
+            }
+            // given up: copies may still be landing
+            if (!ok)
+                for (int k = max(0, i - PP_RAW); k < i; ++k) mbar_wait(B.raw + k % PP_RAW, (k / PP_RAW) & 1);
         }
     }
     __syncwarp();
