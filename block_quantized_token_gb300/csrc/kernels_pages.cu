@@ -286,236 +286,457 @@ cudaError_t launch_rope_table(int hd, double base, int n, float *out, cudaStream
 }
 
 // ---------------------------------------------------------------------------
-// append: one warp per (token, head), heads 0 .. H - 1 queries, then KV keys, then KV values
+// append and read.  A row is worked by a group of HD / 8 lanes, 8 values a lane: lane c holds the dims 8 c .. + 7 or,
+// for the "halves" rotation, 4 c .. + 3 of each half of the head, so that a pair is in one lane.
+//
+// What bounds append: the bytes of the rows (a token's queries are read and written once, keys and values read
+// once and leave in 18 / 32 byte a value).  Queries and keys: a group keeps its token's (cos, sin) and both gains in
+// registers over several heads, the next head's values on their way.  Values: a warp takes a run of tokens whose
+// slots follow one another inside a tile, so that a prompt's tiles leave as whole 16-byte words although a V word
+// mixes four rows; a lone row leaves as bytes.
 // ---------------------------------------------------------------------------
 constexpr int AP_WARPS = 8;
+constexpr int AP_BLOCKS = 4;  // blocks an SM: latency, not registers, costs (2: 139 us, 3: 104, 4: 97 for 8192 bf16 tokens, append + read)
 
-// max / min over the 32 / W lanes that share a block
-template <int LANES>
-ER_DEV float group_max(float v) {
+template <class T>
+ER_DEV void ld8(const T *p, bool vec, float (&x)[8]) {
+    __align__(16) T v[8];
+    if (vec) {
 #pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+        for (int k = 0; k < (int)(8 * sizeof(T)) / 16; ++k) reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(p)[k];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = p[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = pg_ld<T>(v + e);
+}
+template <class T>
+ER_DEV void st8(T *p, bool vec, const float (&x)[8]) {
+    __align__(16) T v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = pg_cvt<T>(x[e]);
+    if (vec) {
+#pragma unroll
+        for (int k = 0; k < (int)(8 * sizeof(T)) / 16; ++k) reinterpret_cast<uint4 *>(p)[k] = reinterpret_cast<uint4 *>(v)[k];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = v[e];
+    }
+}
+// 4 consecutive values (8 or 16 bytes)
+template <class T>
+ER_DEV void ld4(const T *p, bool vec, float *x) {
+    __align__(16) T v[4];
+    if (vec) {
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
+        else *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = p[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = pg_ld<T>(v + e);
+}
+template <class T>
+ER_DEV void st4(T *p, bool vec, const float *x) {
+    __align__(16) T v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = pg_cvt<T>(x[e]);
+    if (vec) {
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<uint4 *>(v);
+        else *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = v[e];
+    }
+}
+// a row in lane c's order (see above)
+template <class T, int HD, bool HALVES>
+ER_DEV void ld_row(const T *row, int c, bool vec, float (&x)[8]) {
+    if constexpr (HALVES) {
+        ld4<T>(row + 4 * c, vec, x);
+        ld4<T>(row + HD / 2 + 4 * c, vec, x + 4);
+    } else {
+        ld8<T>(row + 8 * c, vec, x);
+    }
+}
+template <class T, int HD, bool HALVES>
+ER_DEV void st_row(T *row, int c, bool vec, const float (&x)[8]) {
+    if constexpr (HALVES) {
+        st4<T>(row + 4 * c, vec, x);
+        st4<T>(row + HD / 2 + 4 * c, vec, x + 4);
+    } else {
+        st8<T>(row + 8 * c, vec, x);
+    }
 }
 
-// Dims of element e of a lane.  PAIRS: HD / 32 consecutive dims; HALVES: half of them in each half of the head,
-// so that a pair is in one lane in both styles.
-template <int HD, bool HALVES>
-ER_DEV constexpr int ap_dim(int lane, int e) {
-    constexpr int E = HD / 32;
-    return HALVES ? (e / (E / 2)) * (HD / 2) + (E / 2) * lane + e % (E / 2) : E * lane + e;
-}
+// Codes of a row's blocks, 4 bits each in lane order (value e at bits 4 e), and their scales: d[s] of block
+// s of the lane (HALVES: one in each half of the head, else d[0]).  The lanes of a block are neighbours; whole warps call
+// this.  A quotient comes from the scale's reciprocal where that leaves no doubt about its code, else from the division.
+//
+// CHECK: y is off the exact row by at most AP_ERR times |a| + |b| of its rotated pair (a, b), hence by 2 AP_ERR times
+// the pair's larger value, hence by E = 2 AP_ERR max |m| over the blocks that hold the lane's pairs (that block and,
+// for halves, its counterpart in the other half, which the same lanes hold).  Returns whether some code or scale is
+// not certain within E.
+// AP_ERR: the sum of HD squares takes at most 10 float32 steps (half of that in its root), the reciprocal root 3, two
+// products 2, the rotation 3: below 14 steps of 2^-24.
+constexpr float AP_ERR = 14.f * 5.9604645e-8f;
 
-// Codes of a warp's row y (ap_dim order) into cs[HD] (warp's shared memory) and its scales into d[]: element e's
-// block scale.  err: bound of |y - exact|; returns whether some code or scale is not certain within it.
-template <int HD, bool HALVES, bool CHECK>
-ER_DEV bool ap_quant(const float (&y)[HD / 32], const float (&err)[HD / 32], uint8_t *cs, float (&d)[HD / 32],
-                     int lane) {
-    constexpr int E = HD / 32, S = HALVES ? 2 : 1, EP = E / S, LANES = 32 / EP;  // a block: EP elements of LANES lanes
-    bool unsure = false;
+template <bool HALVES, bool CHECK>
+ER_DEV bool ap_quant(const float (&y)[8], uint32_t &codes, float (&d)[2], int lane) {
+    constexpr int S = HALVES ? 2 : 1, EP = 8 / S, LANES = 32 / EP;  // a block: EP values of LANES lanes
+    float mx[S], mn[S], m[S];
+    bool odd = false;  // NaN, or (exact rows) two values of the largest size and different signs
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        // the largest size: NaN counts as the largest of all (its bits are above infinity's)
-        unsigned big = 0;
-#pragma unroll
-        for (int e = 0; e < EP; ++e) big = max(big, __float_as_uint(y[s * EP + e]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = 1; o < LANES; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-        // of those of that size the first one's sign: key = index * 2 + sign
-        unsigned key = 0xffffu;
-#pragma unroll
-        for (int e = EP - 1; e >= 0; --e) {
-            const unsigned u = __float_as_uint(y[s * EP + e]);
-            if ((u & 0x7fffffffu) == big) key = (unsigned)(((EP * lane + e) & 31) * 2) | (u >> 31);
-        }
-#pragma unroll
-        for (int o = 1; o < LANES; o <<= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
-        const float m = __uint_as_float(big | (key << 31));
-        const float dd = pg_scale(m);
-        if (CHECK) {
-            float lo = 0.f, hi = 0.f;  // the exact largest size lies in [lo, hi]
-#pragma unroll
-            for (int e = 0; e < EP; ++e) {
-                lo = fmaxf(lo, fabsf(y[s * EP + e]) - err[s * EP + e]);
-                hi = fmaxf(hi, fabsf(y[s * EP + e]) + err[s * EP + e]);
-            }
-            lo = group_max<LANES>(lo);
-            hi = group_max<LANES>(hi);
-            unsure |= pg_scale(lo) != pg_scale(hi);
-#pragma unroll
-            for (int e = 0; e < EP; ++e)  // could a value of the other sign be the largest?
-                unsure |= fabsf(y[s * EP + e]) + err[s * EP + e] >= lo && (__float_as_uint(y[s * EP + e]) >> 31) != (key & 1u);
-        }
+        mx[s] = mn[s] = y[s * EP];
 #pragma unroll
         for (int e = 0; e < EP; ++e) {
-            const float r = y[s * EP + e] / dd;
-            d[s * EP + e] = dd;
-            cs[ap_dim<HD, HALVES>(lane, s * EP + e)] =
-                (uint8_t)(dd != 0.f && !isnan(dd) ? (int)fminf(fmaxf(roundf(r) + 8.f, 0.f), 15.f) : 8);
-            if (CHECK && dd != 0.f) {
-                const float t = fabsf(r);
-                // distance of |r| from the border between two codes; its own rounding is at most t 2^-24
-                unsure |= fabsf(t - (floorf(t) + 0.5f)) <= err[s * EP + e] / fabsf(dd) * 1.0001f + t * 1.2e-7f;
-            }
+            mx[s] = fmaxf(mx[s], y[s * EP + e]);
+            mn[s] = fminf(mn[s], y[s * EP + e]);
+            odd |= isnan(y[s * EP + e]);
         }
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) {
+            mx[s] = fmaxf(mx[s], __shfl_xor_sync(0xffffffffu, mx[s], o));
+            mn[s] = fminf(mn[s], __shfl_xor_sync(0xffffffffu, mn[s], o));
+        }
+        m[s] = mx[s] > -mn[s] ? mx[s] : mn[s];
+        if (!CHECK) odd |= mx[s] == -mn[s] && mx[s] != 0.f;
+    }
+    bool unsure = CHECK && odd;
+    if (!CHECK && __any_sync(0xffffffffu, odd)) {
+        // the first value of the largest size decides; NaN counts as the largest of all (its bits are above infinity's)
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            unsigned big = 0, key = 0xffffu;
+#pragma unroll
+            for (int e = 0; e < EP; ++e) big = max(big, __float_as_uint(y[s * EP + e]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = 1; o < LANES; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+#pragma unroll
+            for (int e = EP - 1; e >= 0; --e) {
+                const unsigned u = __float_as_uint(y[s * EP + e]);
+                if ((u & 0x7fffffffu) == big) key = (unsigned)((EP * (lane & (LANES - 1)) + e) * 2) | (u >> 31);
+            }
+#pragma unroll
+            for (int o = 1; o < LANES; o <<= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
+            m[s] = __uint_as_float(big | (key << 31));
+        }
+    }
+    codes = 0;
+    float E = 0.f;
+    if (CHECK) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) E = fmaxf(E, fabsf(m[s]));
+        E *= 2.f * AP_ERR;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const float dd = pg_scale(m[s]), inv = 1.f / dd;
+        d[s] = dd;
+        // within this of a border between codes the quotient is taken again: the reciprocal's and the product's rounding of at
+        // most 8.5 (1 + 2^-8), and the row's own error
+        const float near = 3e-6f + (CHECK ? E * fabsf(inv) : 0.f);
+        if (CHECK) unsure |= pg_scale(fabsf(m[s]) + E) != pg_scale(fabsf(m[s]) - E) || fabsf(mx[s] + mn[s]) <= 2.f * E;
+        const bool none = dd == 0.f || isnan(dd);
+#pragma unroll
+        for (int e = 0; e < EP; ++e) {
+            const float r = y[s * EP + e] * inv + 8.5f, f = floorf(r);
+            int c = min(max((int)f, 0), 15);
+            if (r - f < near || r - f > 1.f - near) {
+                if (CHECK) unsure = true;
+                else c = (int)fminf(fmaxf(roundf(y[s * EP + e] / dd) + 8.f, 0.f), 15.f);
+            }
+            codes |= (uint32_t)(none ? 8 : c) << (4 * (s * EP + e));
+        }
+        if (CHECK && none) unsure = true;
     }
     return unsure;
 }
 
+// 8 codes of consecutive dims (dim j at bits 4 j) -> K's word: dim 2 i + e at bits 4 i + 16 e
+ER_DEV uint32_t ap_kword(uint32_t c) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w |= ((c >> (4 * j)) & 15u) << (4 * (j >> 1) + 16 * (j & 1));
+    return w;
+}
+
+struct AppendArgs {
+    PagesView p;
+    er_pages_append_args a;
+    int parts;      // groups that share a token's queries and keys
+    int qk_blocks;  // blocks of queries and keys; those after them take the values
+    int chunk;      // tokens of a value warp's chunk (1 or 16)
+};
+
+// whether token t has a row to write; flags what is out of range
+ER_DEV bool ap_there(const AppendArgs &A, int t, int slot, int pos) {
+    if (slot < 0) return false;
+    if ((long long)slot >= (long long)A.p.n_pages * A.p.page_rows || (A.a.rope_dev && (pos < 0 || pos >= A.a.rope_positions))) {
+        atomicOr(A.p.flags, ER_PAGES_FLAG_RANGE);
+        return false;
+    }
+    return true;
+}
+
 template <class T, int HD, bool HALVES>
-__global__ void __launch_bounds__(AP_WARPS * 32) pages_append_kernel(PagesView p, er_pages_append_args a) {
-    constexpr int E = HD / 32;
-    __shared__ __align__(16) uint8_t codes[AP_WARPS][HD];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int heads = a.n_heads + 2 * p.KV;
-    const long long items = (long long)a.n_tokens * heads;
-    for (long long it = (long long)blockIdx.x * AP_WARPS + warp; it < items; it += (long long)gridDim.x * AP_WARPS) {
-        const int t = (int)(it / heads), h = (int)(it - (long long)t * heads);
-        const int slot = a.slots_dev[t];
-        if (slot < 0) continue;
-        const int pos = a.rope_dev ? a.positions_dev[t] : 0;
-        if ((long long)slot >= (long long)p.n_pages * p.page_rows ||
-            (a.rope_dev && (pos < 0 || pos >= a.rope_positions))) {
-            if (lane == 0) atomicOr(p.flags, ER_PAGES_FLAG_RANGE);
-            continue;
+ER_DEV void append_qk(const AppendArgs &A) {
+    constexpr int LG = HD / 8, GPW = 32 / LG;  // lanes of a group, groups of a warp
+    const er_pages_append_args &a = A.a;
+    const PagesView &p = A.p;
+    const int lane = threadIdx.x & 31, c = lane % LG;
+    const long long grp = ((long long)blockIdx.x * AP_WARPS + (threadIdx.x >> 5)) * GPW + lane / LG;
+    const int rows = a.n_heads + p.KV;
+    const int t = (int)(grp / A.parts), part = (int)(grp - (long long)t * A.parts);
+    const bool in = t < a.n_tokens;
+    const int slot = in ? a.slots_dev[t] : -1;
+    const int pos = in && a.rope_dev && slot >= 0 ? a.positions_dev[t] : 0;
+    const bool there = ap_there(A, t, slot, pos);
+    if (!__any_sync(0xffffffffu, there)) return;
+    auto aligned = [](const void *x, int64_t stride) { return ((uintptr_t)x & 15) == 0 && (stride * sizeof(T)) % 16 == 0; };
+    const bool vq = aligned(a.q_dev, a.q_stride), vk = aligned(a.k_dev, a.k_stride), vo = aligned(a.q_out_dev, a.q_out_stride);
+    // the lane's pairs i: values (2 i, 2 i + 1), or (i, i + 4) for halves; their (cos, sin) and the two gains
+    const bool turn = a.rope_dev != nullptr;
+    float2 cs[4];
+    float gain[2][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        cs[i] = turn && there ? __ldg(reinterpret_cast<const float2 *>(a.rope_dev) + (size_t)pos * (HD / 2) + 4 * c + i)
+                              : make_float2(1.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float *gp = k ? a.k_gain_dev : a.q_gain_dev;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            gain[k][e] = gp ? __ldg(gp + (HALVES ? (e >> 2) * (HD / 2) + 4 * c + (e & 3) : 8 * c + e)) : 1.f;
+    }
+    auto source = [&](int r, bool &vec) {
+        const bool key = r >= a.n_heads;
+        vec = key ? vk : vq;
+        return key ? (const T *)a.k_dev + t * a.k_stride + (size_t)(r - a.n_heads) * HD
+                   : (const T *)a.q_dev + t * a.q_stride + (size_t)r * HD;
+    };
+    float nx[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) nx[e] = 0.f;
+    if (there && part < rows) {
+        bool vec;
+        const T *src = source(part, vec);
+        ld_row<T, HD, HALVES>(src, c, vec, nx);
+    }
+    // whole warps go round together (its groups' tokens and parts may differ by one row)
+    for (int r0 = 0; r0 < rows; r0 += A.parts) {
+        const int r = r0 + part;
+        const bool live = there && r < rows;
+        float x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = nx[e];
+            y[e] = nx[e];
         }
-        const int what = h < a.n_heads ? 0 : h < a.n_heads + p.KV ? 1 : 2;  // query, key, value
-        const int hh = what == 0 ? h : what == 1 ? h - a.n_heads : h - a.n_heads - p.KV;
-        const T *src = (what == 0   ? (const T *)a.q_dev + t * a.q_stride
-                        : what == 1 ? (const T *)a.k_dev + t * a.k_stride
-                                    : (const T *)a.v_dev + t * a.v_stride) + (size_t)hh * HD;
-        const float *gain = what == 0 ? a.q_gain_dev : what == 1 ? a.k_gain_dev : nullptr;
-        const bool turn = a.rope_dev && what < 2;
-        float x[E], y[E], err[E], cs_[E], sn_[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            x[e] = pg_ld<T>(src + ap_dim<HD, HALVES>(lane, e));
-            y[e] = x[e];
-            err[e] = 0.f;
+        if (there && r + A.parts < rows) {
+            bool vec;
+            const T *src = source(r + A.parts, vec);
+            ld_row<T, HD, HALVES>(src, c, vec, nx);
         }
-        if (gain) {
-            float ss = 0.f;
+        const bool key = r >= a.n_heads;
+        const bool norm = key ? a.k_gain_dev != nullptr : a.q_gain_dev != nullptr;
+        float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float rs = 1.f / sqrtf(ss / HD + a.eps);
+        for (int o = 1; o < LG; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (norm) {
+            const float rs = rsqrtf(ss * (1.f / HD) + a.eps);
 #pragma unroll
-            for (int e = 0; e < E; ++e) y[e] = x[e] * rs * gain[ap_dim<HD, HALVES>(lane, e)];
+            for (int e = 0; e < 8; ++e) y[e] = x[e] * rs * (key ? gain[1][e] : gain[0][e]);
         }
         if (turn) {
-            const float2 *tab = reinterpret_cast<const float2 *>(a.rope_dev) + (size_t)pos * (HD / 2);
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-                const int e0 = HALVES ? i : 2 * i, e1 = HALVES ? i + E / 2 : 2 * i + 1;
-                const float2 c = tab[HALVES ? ap_dim<HD, true>(lane, i) : (E * lane) / 2 + i];
-                cs_[e0] = c.x;
-                sn_[e0] = c.y;
+            for (int i = 0; i < 4; ++i) {
+                const int e0 = HALVES ? i : 2 * i, e1 = HALVES ? i + 4 : 2 * i + 1;
                 const float ya = y[e0], yb = y[e1];
-                y[e0] = ya * c.x - yb * c.y;
-                y[e1] = yb * c.x + ya * c.y;
-                err[e0] = err[e1] = fabsf(ya) + fabsf(yb);
+                y[e0] = ya * cs[i].x - yb * cs[i].y;
+                y[e1] = yb * cs[i].x + ya * cs[i].y;
             }
-        } else if (gain) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) err[e] = fabsf(y[e]);
         }
-        if (what == 0) {
-            T *dst = (T *)a.q_out_dev + t * a.q_out_stride + (size_t)hh * HD;
+        if (live && !key) st_row<T, HD, HALVES>((T *)a.q_out_dev + t * a.q_out_stride + (size_t)r * HD, c, vo, y);
+        if (!__any_sync(0xffffffffu, live && key)) continue;
+        uint32_t codes;
+        float d[2];
+        if (!a.k_gain_dev && !turn) {
+            ap_quant<HALVES, false>(y, codes, d, lane);  // keys as they are
+        } else if (__any_sync(0xffffffffu, ap_quant<HALVES, true>(y, codes, d, lane) && live && key)) {
+            // those rows again in float64: their codes are those of the formula whatever the float32 steps were
+            double z[8], zs = 0.0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) dst[ap_dim<HD, HALVES>(lane, e)] = pg_cvt<T>(y[e]);
-            continue;
+            for (int e = 0; e < 8; ++e) {
+                z[e] = (double)x[e];
+                zs += z[e] * z[e];
+            }
+#pragma unroll
+            for (int o = 1; o < LG; o <<= 1) zs += __shfl_xor_sync(0xffffffffu, zs, o);
+            if (norm) {
+                const double rs = 1.0 / sqrt(zs / HD + (double)a.eps);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = z[e] * rs * (double)gain[1][e];
+            }
+            if (turn) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e0 = HALVES ? i : 2 * i, e1 = HALVES ? i + 4 : 2 * i + 1;
+                    const double za = z[e0], zb = z[e1], co = (double)cs[i].x, sn = (double)cs[i].y;
+                    z[e0] = za * co - zb * sn;
+                    z[e1] = zb * co + za * sn;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = (float)z[e];
+            ap_quant<HALVES, false>(y, codes, d, lane);
         }
-        float d[E];
-        if (what == 1 && (gain || turn)) {
-            // float32 rounding of y: the sum of HD squares at most 9 steps of 2^-24 (half of that in its root), the
-            // division, the root and two products 4 more, the rotation 3: below 12 * 2^-24 of |a| + |b|
-#pragma unroll
-            for (int e = 0; e < E; ++e) err[e] *= 12.f * 5.9604645e-8f;
-            const bool unsure = ap_quant<HD, HALVES, true>(y, err, codes[warp], d, lane);
-            if (__any_sync(0xffffffffu, unsure)) {
-                // the row again in float64: its codes are those of the formula whatever the float32 steps were
-                double z[E], ss = 0.0;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    z[e] = (double)x[e];
-                    ss += z[e] * z[e];
-                }
-                if (gain) {
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const double rs = sqrt(ss / HD + (double)a.eps);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) z[e] = z[e] / rs * (double)gain[ap_dim<HD, HALVES>(lane, e)];
-                }
-                if (turn) {
-#pragma unroll
-                    for (int i = 0; i < E / 2; ++i) {
-                        const int e0 = HALVES ? i : 2 * i, e1 = HALVES ? i + E / 2 : 2 * i + 1;
-                        const double za = z[e0], zb = z[e1], c = (double)cs_[e0], sn = (double)sn_[e0];
-                        z[e0] = za * c - zb * sn;
-                        z[e1] = zb * c + za * sn;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = (float)z[e];
-                __syncwarp();
-                ap_quant<HD, HALVES, false>(y, err, codes[warp], d, lane);
+        const uint32_t mate = __shfl_xor_sync(0xffffffffu, codes, 1);
+        if (!live || !key) continue;
+        uint8_t *tile = pg_tile(p.pool, p.page_rows, p.KV, HD, slot, r - a.n_heads);
+        const int in16 = (slot % p.page_rows) & 15;
+        __half *ks = reinterpret_cast<__half *>(tile + pg_off_ks(HD)) + in16 * (HD / 32);
+        if constexpr (HALVES) {
+            // two lanes make a word: the even one that of the first half, the odd one that of the second
+            const bool odd = c & 1;
+            const uint32_t lo = odd ? mate >> 16 : codes & 0xFFFFu, hi = odd ? codes >> 16 : mate & 0xFFFFu;
+            const int dim = (odd ? HD / 2 : 0) + 8 * (c >> 1);
+            *reinterpret_cast<uint32_t *>(tile + pg_k_word(in16, ((dim & 31) >> 3) * (HD / 32) + (dim >> 5), HD)) =
+                ap_kword(lo | hi << 16);
+            if ((c & 7) == 0) {
+                ks[c >> 3] = __float2half_rn(d[0]);
+                ks[HD / 64 + (c >> 3)] = __float2half_rn(d[1]);
             }
         } else {
-            ap_quant<HD, HALVES, false>(y, err, codes[warp], d, lane);
+            *reinterpret_cast<uint32_t *>(tile + pg_k_word(in16, (c & 3) * (HD / 32) + (c >> 2), HD)) = ap_kword(codes);
+            if ((c & 3) == 0) ks[c >> 2] = __float2half_rn(d[0]);
+        }
+    }
+}
+
+template <class T, int HD>
+ER_DEV void append_v(const AppendArgs &A, uint32_t (&cw)[16][HD / 8 + 2], unsigned short (&sc)[16][HD / 32]) {
+    constexpr int LG = HD / 8, GPW = 32 / LG;
+    const er_pages_append_args &a = A.a;
+    const PagesView &p = A.p;
+    const int lane = threadIdx.x & 31, c = lane % LG, gi = lane / LG;
+    const long long item = (long long)(blockIdx.x - A.qk_blocks) * AP_WARPS + (threadIdx.x >> 5);
+    const int chunk = (int)(item / p.KV), h = (int)(item - (long long)chunk * p.KV);
+    const int t0 = chunk * A.chunk;
+    if (t0 >= a.n_tokens) return;
+    const bool vec = ((uintptr_t)a.v_dev & 15) == 0 && (a.v_stride * sizeof(T)) % 16 == 0;
+    // lane i: token t0 + i; a run starts where a token does not follow the one before it inside a tile
+    const int ti = t0 + lane;
+    const int slot = ti < a.n_tokens ? a.slots_dev[ti] : -1;
+    const int prev = ti < a.n_tokens && ti > 0 ? a.slots_dev[ti - 1] : -2;
+    const int pos = ti < a.n_tokens && a.rope_dev && slot >= 0 ? a.positions_dev[ti] : 0;
+    const int ppos = ti < a.n_tokens && a.rope_dev && ti > 0 && prev >= 0 ? a.positions_dev[ti - 1] : 0;
+    const bool there = ap_there(A, ti, slot, pos);
+    auto good = [&](int s, int q) {
+        return s >= 0 && (long long)s < (long long)p.n_pages * p.page_rows && (!a.rope_dev || (q >= 0 && q < a.rope_positions));
+    };
+    const bool starts = there && (slot % 16 == 0 || slot != prev + 1 || !good(prev, ppos));
+    const unsigned sm = __ballot_sync(0xffffffffu, starts), tm = __ballot_sync(0xffffffffu, there);
+    // the runs that start among the chunk's tokens (one may reach past it, up to 15 tokens on)
+    for (unsigned left = sm & (A.chunk == 32 ? 0xffffffffu : (1u << A.chunk) - 1u); left; left &= left - 1) {
+        const int first = __ffs(left) - 1;
+        const unsigned stop = (sm | ~tm) & ~((2u << first) - 1u);  // the next start, or the next token without a row
+        const int n = min((stop ? __ffs(stop) - 1 : 32) - first, 16);
+        const int s0 = __shfl_sync(0xffffffffu, slot, first), r0 = (s0 % p.page_rows) & 15;
+        // rows k = gi, gi + GPW, ... of the run: codes and scales to shared memory
+        const T *src = (const T *)a.v_dev + (t0 + first) * a.v_stride + (size_t)h * HD + 8 * c;
+#pragma unroll 4
+        for (int k0 = 0; k0 < n; k0 += GPW) {
+            const int k = k0 + gi;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            if (k < n) ld8<T>(src + k * a.v_stride, vec, x);
+            uint32_t codes;
+            float d[2];
+            ap_quant<false, false>(x, codes, d, lane);
+            if (k < n) {
+                cw[r0 + k][c] = codes;
+                if ((c & 3) == 0) sc[r0 + k][c >> 2] = __half_as_ushort(__float2half_rn(d[0]));
+            }
         }
         __syncwarp();
-        uint8_t *tile = pg_tile(p.pool, p.page_rows, p.KV, HD, slot, hh);
-        const int r = (slot % p.page_rows) & 15;
-        const uint8_t *cs = codes[warp];
-        if (what == 1) {
-            if (lane < HD / 8) {  // word w: dims 32 b + 8 t .. + 7
-                const int tq = lane / (HD / 32), b = lane % (HD / 32);
-                const uint2 c8 = *reinterpret_cast<const uint2 *>(cs + 32 * b + 8 * tq);
-                uint32_t w = 0;
+        uint8_t *tile = pg_tile(p.pool, p.page_rows, p.KV, HD, s0, h);
+        // lane (g, t): words u of run q: dims 64 q + 16 u + g and + 8 of rows 2 t, 2 t + 8, 2 t + 1, 2 t + 9
+        const int g = lane >> 2, t = lane & 3;
+        auto has = [&](int r) { return r >= r0 && r < r0 + n; };
+        const bool all = has(2 * t) && has(2 * t + 1) && has(2 * t + 8) && has(2 * t + 9);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+        for (int q = 0; q < HD / 64; ++q) {
+            uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = 2 * i + e;
-                        w |= (((j < 4 ? c8.x : c8.y) >> (8 * (j & 3))) & 15u) << (4 * i + 16 * e);
-                    }
-                *reinterpret_cast<uint32_t *>(tile + pg_k_word(r, lane, HD)) = w;
+            for (int u = 0; u < 4; ++u) {
+                w[u] = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {  // byte b: row 2 t + (b >> 1) + 8 (b & 1)
+                    const uint2 y = *reinterpret_cast<const uint2 *>(&cw[2 * t + (b >> 1) + 8 * (b & 1)][8 * q + 2 * u]);
+                    w[u] |= (((y.x >> (4 * g)) & 15u) | ((y.y >> (4 * g)) & 15u) << 4) << (8 * b);
+                }
             }
-        } else {
+            uint8_t *dst = tile + pg_off_v(HD) + q * 512 + lane * 16;
+            if (all) {
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < HD / 64; ++i) {
-                const int j = lane + 32 * i, dim = 16 * (j >> 3) + (j & 7);
-                tile[pg_off_v(HD) + pg_v_byte(r, j, HD)] = (uint8_t)(cs[dim] | cs[dim + 8] << 4);
+                for (int b = 0; b < 4; ++b)
+                    if (has(2 * t + (b >> 1) + 8 * (b & 1)))
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) dst[4 * u + b] = (uint8_t)(w[u] >> (8 * b));
             }
         }
-        // the lane that holds a block's first dim writes its scale
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int dim = ap_dim<HD, HALVES>(lane, e);
-            if ((dim & 31) == 0) {
-                __half *sc = reinterpret_cast<__half *>(tile + (what == 1 ? pg_off_ks(HD) : pg_off_vs(HD)));
-                sc[what == 1 ? r * (HD / 32) + dim / 32 : pg_vs_half(r, dim / 32, HD)] = __float2half_rn(d[e]);
-            }
+        unsigned short *vs = reinterpret_cast<unsigned short *>(tile + pg_off_vs(HD));
+        for (int k = lane; k < n * (HD / 32); k += 32) {
+            const int r = r0 + k / (HD / 32), blk = k % (HD / 32);
+            vs[pg_vs_half(r, blk, HD)] = sc[r][blk];
         }
         __syncwarp();
     }
 }
 
+template <class T, int HD, bool HALVES>
+__global__ void __launch_bounds__(AP_WARPS * 32, AP_BLOCKS) pages_append_kernel(const AppendArgs A) {
+    __shared__ __align__(16) uint32_t cw[AP_WARPS][16][HD / 8 + 2];
+    __shared__ unsigned short sc[AP_WARPS][16][HD / 32];
+    if ((int)blockIdx.x < A.qk_blocks) append_qk<T, HD, HALVES>(A);
+    else append_v<T, HD>(A, cw[threadIdx.x >> 5], sc[threadIdx.x >> 5]);
+}
+
 template <class T>
 static cudaError_t append_t(const PagesView &p, const er_pages_append_args &a, int num_sms, cudaStream_t st) {
-    const long long items = (long long)a.n_tokens * (a.n_heads + 2 * p.KV);
-    long long blocks = (items + AP_WARPS - 1) / AP_WARPS;
-    if (blocks > 64ll * num_sms) blocks = 64ll * num_sms;
-    if (blocks < 1) return cudaSuccess;
+    AppendArgs A = {p, a, 1, 0, 16};
+    const int rows = a.n_heads + p.KV;
+    // Groups (of HD / 8 lanes) enough for twice the GPU's threads, and no more than one a row: a step's few tokens are
+    // spread row by row, a prompt's groups keep their token's table row and gains for several heads.
+    const long long want = 2ll * num_sms * 2048 / (p.hd / 8);
+    const long long parts = (want + a.n_tokens - 1) / a.n_tokens;
+    A.parts = (int)(parts < 1 ? 1 : parts > rows ? rows : parts);
+    const long long per = AP_WARPS * 32 / (p.hd / 8);
+    const long long qk = ((long long)a.n_tokens * A.parts + per - 1) / per;
+    // Chunks of 16 tokens where that still makes a warp for every scheduler, else a token each
+    A.chunk = (long long)a.n_tokens * p.KV / 16 >= 4ll * num_sms ? 16 : 1;
+    const long long chunks = ((long long)a.n_tokens + A.chunk - 1) / A.chunk;
+    const long long v = (chunks * p.KV + AP_WARPS - 1) / AP_WARPS;
+    if (qk + v > 2147483647ll) return cudaErrorInvalidValue;
+    A.qk_blocks = (int)qk;
+    const unsigned blocks = (unsigned)(qk + v);
     const bool halves = a.rope_style == ER_ROPE_HALVES;
     if (p.hd == 128)
-        halves ? pages_append_kernel<T, 128, true><<<(unsigned)blocks, AP_WARPS * 32, 0, st>>>(p, a)
-               : pages_append_kernel<T, 128, false><<<(unsigned)blocks, AP_WARPS * 32, 0, st>>>(p, a);
+        halves ? pages_append_kernel<T, 128, true><<<blocks, AP_WARPS * 32, 0, st>>>(A)
+               : pages_append_kernel<T, 128, false><<<blocks, AP_WARPS * 32, 0, st>>>(A);
     else
-        halves ? pages_append_kernel<T, 64, true><<<(unsigned)blocks, AP_WARPS * 32, 0, st>>>(p, a)
-               : pages_append_kernel<T, 64, false><<<(unsigned)blocks, AP_WARPS * 32, 0, st>>>(p, a);
+        halves ? pages_append_kernel<T, 64, true><<<blocks, AP_WARPS * 32, 0, st>>>(A)
+               : pages_append_kernel<T, 64, false><<<blocks, AP_WARPS * 32, 0, st>>>(A);
     return cudaGetLastError();
 }
 
@@ -526,53 +747,52 @@ cudaError_t launch_pages_append(const PagesView &p, const er_pages_append_args &
 }
 
 // ---------------------------------------------------------------------------
-// rows out: one warp per (slot, head), K then V
+// rows out: a group of HD / 8 lanes per (slot, head), 8 consecutive dims a lane
 // ---------------------------------------------------------------------------
 template <class T, int HD>
-__global__ void __launch_bounds__(256) pages_read_kernel(PagesView p, int n, const int32_t *slots, T *k, T *v) {
-    const int lane = threadIdx.x & 31;
-    const long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(256) pages_read_kernel(PagesView p, int n, const int32_t *slots, T *k, T *v, bool vec) {
+    constexpr int LG = HD / 8;
+    const int c = threadIdx.x % LG;
+    const long long it = (long long)blockIdx.x * (256 / LG) + threadIdx.x / LG;
     if (it >= (long long)n * p.KV) return;
+    // heads fastest: neighbouring groups write neighbouring rows
     const int t = (int)(it / p.KV), h = (int)(it - (long long)t * p.KV);
     const int slot = slots[t];
     if (slot < 0) return;
     if ((long long)slot >= (long long)p.n_pages * p.page_rows) {
-        if (lane == 0) atomicOr(p.flags, ER_PAGES_FLAG_RANGE);
+        if (c == 0) atomicOr(p.flags, ER_PAGES_FLAG_RANGE);
         return;
     }
     const uint8_t *tile = pg_tile(p.pool, p.page_rows, p.KV, HD, slot, h);
     const int r = (slot % p.page_rows) & 15;
-    const size_t out = (size_t)it * HD;
-    const __half *ks = reinterpret_cast<const __half *>(tile + pg_off_ks(HD));
-    const __half *vs = reinterpret_cast<const __half *>(tile + pg_off_vs(HD));
-    if (k && lane < HD / 8) {
-        const int tq = lane / (HD / 32), b = lane % (HD / 32);
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(tile + pg_k_word(r, lane, HD));
-        const float d = __half2float(ks[r * (HD / 32) + b]);
+    const size_t out = (size_t)it * HD + 8 * c;
+    float x[8];
+    if (k) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(tile + pg_k_word(r, (c & 3) * (HD / 32) + (c >> 2), HD));
+        const float d = __half2float(reinterpret_cast<const __half *>(tile + pg_off_ks(HD))[r * (HD / 32) + (c >> 2)]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                k[out + 32 * b + 8 * tq + 2 * i + e] = pg_cvt<T>(d * (float)((int)((w >> (4 * i + 16 * e)) & 15u) - 8));
+        for (int j = 0; j < 8; ++j) x[j] = d * (float)((int)((w >> (4 * (j >> 1) + 16 * (j & 1))) & 15u) - 8);
+        st8<T>(k + out, vec, x);
     }
     if (v) {
+        // dims 8 c .. + 7: nibbles c & 1 of 8 bytes, 64 apart
+        const uint8_t *src = tile + pg_off_v(HD) + pg_v_byte(r, 8 * (c >> 1), HD);
+        const float d = __half2float(reinterpret_cast<const __half *>(tile + pg_off_vs(HD))[pg_vs_half(r, c >> 2, HD)]);
 #pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-            const int j = lane + 32 * i, dim = 16 * (j >> 3) + (j & 7);
-            const int c = tile[pg_off_v(HD) + pg_v_byte(r, j, HD)];
-            const float d = __half2float(vs[pg_vs_half(r, dim / 32, HD)]);
-            v[out + dim] = pg_cvt<T>(d * (float)((c & 15) - 8));
-            v[out + dim + 8] = pg_cvt<T>(d * (float)((c >> 4) - 8));
-        }
+        for (int j = 0; j < 8; ++j) x[j] = d * (float)((int)((src[64 * j] >> (4 * (c & 1))) & 15) - 8);
+        st8<T>(v + out, vec, x);
     }
 }
 
 template <class T>
 static cudaError_t read_t(const PagesView &p, int n, const int32_t *slots, void *k, void *v, cudaStream_t st) {
-    const long long blocks = ((long long)n * p.KV + 7) / 8;
+    const int per = 256 / (p.hd / 8);
+    const long long blocks = ((long long)n * p.KV + per - 1) / per;
     if (blocks < 1) return cudaSuccess;
-    if (p.hd == 128) pages_read_kernel<T, 128><<<(unsigned)blocks, 256, 0, st>>>(p, n, slots, (T *)k, (T *)v);
-    else pages_read_kernel<T, 64><<<(unsigned)blocks, 256, 0, st>>>(p, n, slots, (T *)k, (T *)v);
+    if (blocks > 2147483647ll) return cudaErrorInvalidValue;
+    const bool vec = (((uintptr_t)k | (uintptr_t)v) & 15) == 0;
+    if (p.hd == 128) pages_read_kernel<T, 128><<<(unsigned)blocks, 256, 0, st>>>(p, n, slots, (T *)k, (T *)v, vec);
+    else pages_read_kernel<T, 64><<<(unsigned)blocks, 256, 0, st>>>(p, n, slots, (T *)k, (T *)v, vec);
     return cudaGetLastError();
 }
 
