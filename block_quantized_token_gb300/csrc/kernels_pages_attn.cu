@@ -18,15 +18,14 @@
 // each slot with its mbarrier; the table entries of the next 32 tiles are held a lane each, so no copy waits for a
 // table.
 //
-// Arithmetic per tile (mma.sync, fp32 sums), the cached side as the A operand, the 8 query rows as B's columns:
-//   S^T = K Q^T in fp8 (m16n8k32): a 4-bit code c is, as it stands in a byte, the e4m3 number c 2^-9, so two masks
-//         and a shift make 8 codes an operand.  Queries are cut into e4m3 pieces of 4 bits (bf16: 2, exact; fp16: 3,
-//         exact; fp32: 5, the last two with a scale of their own, 2^-20 of the row's largest).  Sums of such products
-//         are exact in fp32 (measured: equal to 64-bit sums).  One instruction is one 32-value block: its sum minus
-//         8 sum q (the accumulator's start) times the row's scale goes to the score.
-//   O^T += V^T P^T in fp16 (m16n8k16): one code word is a lane's whole A operand, a mask and one FMA a pair, exact
-//         (pages.cuh).  Probabilities go from the scores' layout to B's by movmatrix, as hi + lo halves
-//         (2^-22; bf16 outputs: hi alone, 2^-11).
+// Arithmetic (mma.sync m16n8k16, fp32 sums), the cached side as the A operand, the 8 query rows as B's columns:
+//   S^T = K Q^T.  fp32 and fp16 queries: K's values as they are (fp16 numbers, pages.cuh), Q exact (fp16) or as hi + lo
+//         halves (fp32: 2^-22 of the row's largest).  bf16 queries: K's codes without scale or offset, 1024 + c and 64 +
+//         c as a mask leaves them (5 instructions for 8 codes against 14); the accumulator starts at minus the
+//         offsets' sum and the row's scale multiplies the block's sum.  That costs 2^-23 of 1032 sum |q|, 2^-15 of
+//         scale sum |q||k| at worst, where a bf16 output keeps 2^-9.
+//   O^T += V^T P^T.  One code word is a lane's whole A operand, a mask and one FMA a pair, exact.  Probabilities go from
+//         the scores' layout to B's by movmatrix, as hi + lo halves (2^-22; bf16 outputs: hi alone, 2^-11).
 // Masks.  Tiles that some row of the unit attends only in part go through a path that masks scores and zeroes the
 // scales of rows nobody attends (they may hold anything); a NaN value that only some of the unit's tokens attend
 // is carried by their scores instead.
@@ -44,7 +43,7 @@ constexpr int PD_SLOTS = 4;    // steps in a warp's ring
 constexpr int PD_STEP = 32;      // rows of a step: two tiles
 constexpr int PD_ROWS = 8;       // query rows of a unit
 constexpr int PD_SEQS = 512;     // sequences of a launch (more: several launches)
-constexpr int PD_MIN_STEPS = 2;  // steps of a CTA at least
+constexpr int PD_MIN_STEPS = 8;  // steps of a CTA at least: one a warp (fewer only add states to join)
 constexpr float PD_UP = 7.f;     // p = 2^(s - m + PD_UP)
 constexpr float PD_SLACK = 8.f;  // scores may pass m by this much
 constexpr float PD_NONE = -3e38f;  // m before any score
@@ -114,15 +113,9 @@ ER_DEV void pd_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// d += A B over 8 k, fp16
-ER_DEV void pd_mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(b));
-}
-// d = A B + c, e4m3
-ER_DEV void pd_mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+// d = A B + c
+ER_DEV void pd_mma_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
@@ -132,36 +125,20 @@ ER_DEV uint32_t pd_trans(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// e4m3 of (a, b), a in the low byte, and their values taken off a and b and added to sum
-ER_DEV uint32_t pd_piece(float &a, float &b, float &sum) {
-    uint16_t p;
-    uint32_t h;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(b), "f"(a));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p));
-    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    a -= v.x;
-    b -= v.y;
-    sum += v.x + v.y;
-    return p;
-}
 template <class T>
-struct PdType;  // pieces of a query value in two scales (the second 2^-PD_SUB of the first); whether p is hi + lo
+struct PdType;  // RAW: K enters as codes (bf16); QLO: queries have a lo half; PLO: probabilities have one
 template <>
 struct PdType<float> {
-    static constexpr int NA = 3, NB = 2;
-    static constexpr bool SPLIT = true;
+    static constexpr bool RAW = false, QLO = true, PLO = true;
 };
 template <>
 struct PdType<__half> {
-    static constexpr int NA = 3, NB = 0;
-    static constexpr bool SPLIT = true;
+    static constexpr bool RAW = false, QLO = false, PLO = true;
 };
 template <>
 struct PdType<__nv_bfloat16> {
-    static constexpr int NA = 2, NB = 0;
-    static constexpr bool SPLIT = false;
+    static constexpr bool RAW = true, QLO = false, PLO = false;
 };
-constexpr int PD_SUB = 11;
 
 struct PdArgs {
     PagesView p;
@@ -396,9 +373,10 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
         const int any_lo = a.window ? max(0, past + tok0 - a.window + 1) : 0, any_hi = past + tok1;
         const int all_lo = a.window ? max(0, past + tok1 - a.window + 1) : 0, all_hi = past + tok0;
 
-        // the queries' pieces, in the order in which masks leave a word's codes
-        uint32_t qp[C::NB][Y::NA + Y::NB][2];
-        uint32_t bias;  // B of the scales' product: -8 2^-9 sum q of the blocks, hi halves, then lo halves
+        // the queries as B: k16 steps 2 bb + i, the lane's dims 32 bb + 8 t + 4 i .. + 3 of column g
+        uint32_t qh[2 * C::NB][2];
+        [[maybe_unused]] uint32_t ql[2 * C::NB][2];
+        [[maybe_unused]] float bias[C::NB][4];  // RAW: minus the offsets' sum of columns 2 t, 2 t + 1 (twice)
         float down[2];
         {
             float top = 0.f;
@@ -414,53 +392,48 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             odd = __ballot_sync(0xffffffffu, odd) >> (lane & ~3) & 15;
-            // the row's largest goes to [2^7, 2^8) by a power of two, up: e4m3 ends at 448 and steps by 2^-9
-            const int ex = min(max((int)(__float_as_uint(top) >> 23), 8), 246);
-            const float up = odd ? 0.f : __uint_as_float((uint32_t)(261 - ex) << 23);
-            const float dn = odd ? NAN : __uint_as_float((uint32_t)(ex - 7) << 23);
-            float sums[C::NB];
+            // a power of two, up, brings the row's largest to [2^TOP, 2^(TOP + 1)): 14 keeps its lo halves normal, 0
+            // keeps the offsets' sums small
+            constexpr int TOP = Y::RAW ? 0 : 14;
+            const int ex = min(max((int)(__float_as_uint(top) >> 23), TOP + 1), 253);
+            const float up = odd ? 0.f : __uint_as_float((uint32_t)(254 + TOP - ex) << 23);
+            const float dn = odd ? NAN : __uint_as_float((uint32_t)(ex - TOP) << 23);
 #pragma unroll
             for (int bb = 0; bb < C::NB; ++bb) {
-                float x[8], sum = 0.f, sum2 = 0.f;
+                float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = odd ? 0.f : pg_ld<T>(&raw[bb][e]) * up;
-#pragma unroll
-                for (int k = 0; k < Y::NA + Y::NB; ++k) {
-                    if (k == Y::NA)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] *= (float)(1 << PD_SUB);
-                    float &sm = k < Y::NA ? sum : sum2;
-                    qp[bb][k][0] = pd_piece(x[0], x[4], sm);
-                    qp[bb][k][0] |= pd_piece(x[1], x[5], sm) << 16;
-                    qp[bb][k][1] = pd_piece(x[2], x[6], sm);
-                    qp[bb][k][1] |= pd_piece(x[3], x[7], sm) << 16;
+                for (int i = 0; i < 4; ++i) {
+                    const float x0 = odd ? 0.f : pg_ld<T>(&raw[bb][2 * i]) * up, x1 = odd ? 0.f : pg_ld<T>(&raw[bb][2 * i + 1]) * up;
+                    if constexpr (Y::QLO) {
+                        pd_split(x0, x1, qh[2 * bb + (i >> 1)][i & 1], ql[2 * bb + (i >> 1)][i & 1]);
+                    } else {
+                        qh[2 * bb + (i >> 1)][i & 1] = pd_pack(x0, x1);
+                    }
+                    if constexpr (Y::RAW) {
+                        const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&qh[2 * bb + (i >> 1)][i & 1]));
+                        sum += (z.x + z.y) * ((i & 1) ? -72.f : -1032.f);
+                    }
                 }
-                sums[bb] = (sum + sum2 * (1.f / (float)(1 << PD_SUB))) * (-8.f / 512.f);
+                if constexpr (Y::RAW) {
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    bias[bb][0] = bias[bb][2] = __shfl_sync(0xffffffffu, sum, 8 * t);
+                    bias[bb][1] = bias[bb][3] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+                }
             }
 #pragma unroll
-            for (int bb = 0; bb < C::NB; ++bb) {
-                sums[bb] += __shfl_xor_sync(0xffffffffu, sums[bb], 1);
-                sums[bb] += __shfl_xor_sync(0xffffffffu, sums[bb], 2);
-            }
-            uint32_t hi[C::NB / 2], lo[C::NB / 2];
-#pragma unroll
-            for (int k = 0; k < C::NB / 2; ++k) pd_split(sums[2 * k], sums[2 * k + 1], hi[k], lo[k]);
-            if constexpr (HD == 128) bias = t == 0 ? hi[0] : t == 1 ? hi[C::NB / 2 - 1] : t == 2 ? lo[0] : lo[C::NB / 2 - 1];
-            else bias = t == 0 ? hi[0] : t == 1 ? lo[0] : 0u;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) down[c] = __shfl_sync(0xffffffffu, dn, 4 * (2 * t + c)) * (512.f * qscale);
+            for (int c = 0; c < 2; ++c) down[c] = __shfl_sync(0xffffffffu, dn, 4 * (2 * t + c)) * qscale;
         }
         float m[2] = {PD_NONE, PD_NONE}, l[2] = {0.f, 0.f};
         float o[HD / 16][4];  // dims 16 j + g (0, 1) and + 8 (2, 3) of columns 2 t, 2 t + 1
 #pragma unroll
         for (int j = 0; j < HD / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-        // one step: rows r0 .. r0 + 31.  EDGE: some row of the unit does not attend all of them
-        auto step = [&](auto edge_tag, int r0) {
+        // A step (rows r0 .. r0 + 31, in the ring at sl) is three parts: its scores, its probabilities, its products with V.
+        // EDGE: some row of the unit may not attend all of them.
+        // Scores: rows r0 + 16 n + g (x[n][0], x[n][1]) and + 8 (x[n][2], x[n][3]) of columns 2 t, 2 t + 1.
+        auto scores = [&](auto edge_tag, const uint8_t *sl, int r0, float (&x)[2][4]) {
             constexpr bool EDGE = decltype(edge_tag)::value;
-            const uint8_t *sl = ring + wslot * (2 * C::TILE);
-            // ---- scores: rows r0 + 16 n + g (x[n][0], x[n][1]) and + 8 (x[n][2], x[n][3]) of columns 2 t, 2 t + 1
-            float x[2][4];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const uint8_t *sn = sl + n * C::TILE;
@@ -480,37 +453,44 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
                     }
                 }
                 float sc[4] = {0.f, 0.f, 0.f, 0.f};
-                [[maybe_unused]] float sc2[4] = {0.f, 0.f, 0.f, 0.f};
-                if constexpr (HD == 128)
-                    pd_mma_k8(sc, (t & 1) ? ks[0][1] : ks[0][0], (t & 1) ? ks[1][1] : ks[1][0], bias);
-                else
-                    pd_mma_k8(sc, ks[0][0], ks[1][0], bias);
+                if constexpr (Y::RAW) {
 #pragma unroll
-                for (int bb = 0; bb < C::NB; ++bb) {
-                    const uint32_t ka[4] = {kw[0][bb] & 0x0F0F0F0Fu, kw[1][bb] & 0x0F0F0F0Fu,
-                                            (kw[0][bb] >> 4) & 0x0F0F0F0Fu, (kw[1][bb] >> 4) & 0x0F0F0F0Fu};
-                    const float2 e0 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[0][bb >> 1]));
-                    const float2 e1 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[1][bb >> 1]));
-                    const float d0 = (bb & 1) ? e0.y : e0.x, d1 = (bb & 1) ? e1.y : e1.x;
-                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                    float acc[4];
-                    pd_mma8(acc, ka, qp[bb][0][0], qp[bb][0][1], zero);
-#pragma unroll
-                    for (int k = 1; k < Y::NA; ++k) pd_mma8(acc, ka, qp[bb][k][0], qp[bb][k][1], acc);
-                    sc[0] = fmaf(d0, acc[0], sc[0]); sc[1] = fmaf(d0, acc[1], sc[1]);
-                    sc[2] = fmaf(d1, acc[2], sc[2]); sc[3] = fmaf(d1, acc[3], sc[3]);
-                    if constexpr (Y::NB > 0) {
-                        pd_mma8(acc, ka, qp[bb][Y::NA][0], qp[bb][Y::NA][1], zero);
-#pragma unroll
-                        for (int k = Y::NA + 1; k < Y::NA + Y::NB; ++k)
-                            pd_mma8(acc, ka, qp[bb][k][0], qp[bb][k][1], acc);
-                        sc2[0] = fmaf(d0, acc[0], sc2[0]); sc2[1] = fmaf(d0, acc[1], sc2[1]);
-                        sc2[2] = fmaf(d1, acc[2], sc2[2]); sc2[3] = fmaf(d1, acc[3], sc2[3]);
+                    for (int bb = 0; bb < C::NB; ++bb) {
+                        const uint32_t w0 = kw[0][bb], w1 = kw[1][bb], u0 = w0 >> 8, u1 = w1 >> 8;
+                        const uint32_t a0[4] = {lop3_and_or(w0, 0x000F000Fu, 0x64006400u), lop3_and_or(w1, 0x000F000Fu, 0x64006400u),
+                                                lop3_and_or(w0, 0x00F000F0u, 0x54005400u), lop3_and_or(w1, 0x00F000F0u, 0x54005400u)};
+                        const uint32_t a1[4] = {lop3_and_or(u0, 0x000F000Fu, 0x64006400u), lop3_and_or(u1, 0x000F000Fu, 0x64006400u),
+                                                lop3_and_or(u0, 0x00F000F0u, 0x54005400u), lop3_and_or(u1, 0x00F000F0u, 0x54005400u)};
+                        const float2 e0 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[0][bb >> 1]));
+                        const float2 e1 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[1][bb >> 1]));
+                        const float d0 = (bb & 1) ? e0.y : e0.x, d1 = (bb & 1) ? e1.y : e1.x;
+                        float acc[4];
+                        pd_mma_c(acc, a0, qh[2 * bb][0], qh[2 * bb][1], bias[bb]);
+                        pd_mma(acc, a1, qh[2 * bb + 1][0], qh[2 * bb + 1][1]);
+                        sc[0] = fmaf(d0, acc[0], sc[0]); sc[1] = fmaf(d0, acc[1], sc[1]);
+                        sc[2] = fmaf(d1, acc[2], sc[2]); sc[3] = fmaf(d1, acc[3], sc[3]);
                     }
-                }
-                if constexpr (Y::NB > 0)
+                } else {
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};  // a second chain of products
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[k] = fmaf(sc2[k], 1.f / (float)(1 << PD_SUB), sc[k]);
+                    for (int bb = 0; bb < C::NB; ++bb) {
+                        const uint32_t w0 = kw[0][bb], w1 = kw[1][bb];
+                        const uint32_t d0 = prmt(ks[0][bb >> 1], 0u, (bb & 1) ? 0x3232u : 0x1010u), z0 = h2_mul(d0, PD_M24);
+                        const uint32_t d1 = prmt(ks[1][bb >> 1], 0u, (bb & 1) ? 0x3232u : 0x1010u), z1 = h2_mul(d1, PD_M24);
+                        const uint32_t a0[4] = {h2_fma(pd_code<0>(w0), d0, z0), h2_fma(pd_code<0>(w1), d1, z1),
+                                                h2_fma(pd_code<1>(w0), d0, z0), h2_fma(pd_code<1>(w1), d1, z1)};
+                        const uint32_t a1[4] = {h2_fma(pd_code<2>(w0), d0, z0), h2_fma(pd_code<2>(w1), d1, z1),
+                                                h2_fma(pd_code<3>(w0), d0, z0), h2_fma(pd_code<3>(w1), d1, z1)};
+                        pd_mma(sc, a0, qh[2 * bb][0], qh[2 * bb][1]);
+                        pd_mma(part, a1, qh[2 * bb + 1][0], qh[2 * bb + 1][1]);
+                        if constexpr (Y::QLO) {
+                            pd_mma(sc, a0, ql[2 * bb][0], ql[2 * bb][1]);
+                            pd_mma(part, a1, ql[2 * bb + 1][0], ql[2 * bb + 1][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[k] += part[k];
+                }
                 if constexpr (EDGE) {
                     bool vnan[2] = {false, false};  // rows g, g + 8 hold a NaN value: their scores carry it
                     const unsigned short *vs = reinterpret_cast<const unsigned short *>(sn + pg_off_vs(HD));
@@ -530,6 +510,10 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
                     for (int k = 0; k < 4; ++k) x[n][k] = sc[k] * down[k & 1];
                 }
             }
+        };
+        uint32_t ph[2][2];  // B of P: rows 16 n + 8 v .. + 7
+        [[maybe_unused]] uint32_t pl[2][2];
+        auto reference = [&](const float (&x)[2][4]) {
             // a score far above the reference: a new one for the column, and the sums follow
             const float t0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
             const float t1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
@@ -550,8 +534,8 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
                     m[c] = mn;
                 }
             }
-            uint32_t ph[2][2];  // B of P: rows 16 n + 8 v .. + 7
-            [[maybe_unused]] uint32_t pl[2][2];
+        };
+        auto probabilities = [&](const float (&x)[2][4]) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 float p[4];
@@ -561,7 +545,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
                 l[1] += p[1] + p[3];
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    if constexpr (Y::SPLIT) {
+                    if constexpr (Y::PLO) {
                         pd_split(p[2 * v], p[2 * v + 1], ph[n][v], pl[n][v]);
                         pl[n][v] = pd_trans(pl[n][v]);
                     } else {
@@ -570,7 +554,11 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
                     ph[n][v] = pd_trans(ph[n][v]);
                 }
             }
-            // ---- o += p v
+        };
+        // o += p v.  fp32: a tile's products are summed from 0 and added to o rounded to nearest: the tensor cores' sums
+        // truncate, and over thousands of rows that shows.
+        auto values = [&](auto edge_tag, const uint8_t *sl, int r0) {
+            constexpr bool EDGE = decltype(edge_tag)::value;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const uint8_t *sn = sl + n * C::TILE;
@@ -605,8 +593,16 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
                         const uint32_t w = vw[bb >> 1][2 * (bb & 1) + u];
                         const uint32_t va[4] = {h2_fma(pd_code<0>(w), d0, z0), h2_fma(pd_code<1>(w), d0, z0),
                                                 h2_fma(pd_code<2>(w), d1, z1), h2_fma(pd_code<3>(w), d1, z1)};
-                        pd_mma(o[2 * bb + u], va, ph[n][0], ph[n][1]);
-                        if constexpr (Y::SPLIT) pd_mma(o[2 * bb + u], va, pl[n][0], pl[n][1]);
+                        if constexpr (Y::QLO) {
+                            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                            pd_mma(sum, va, ph[n][0], ph[n][1]);
+                            pd_mma(sum, va, pl[n][0], pl[n][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[2 * bb + u][e] += sum[e];
+                        } else {
+                            pd_mma(o[2 * bb + u], va, ph[n][0], ph[n][1]);
+                            if constexpr (Y::PLO) pd_mma(o[2 * bb + u], va, pl[n][0], pl[n][1]);
+                        }
                     }
                 }
             }
@@ -614,18 +610,47 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
 
         const int kend = (int)(min(U.u1, w1) - w0);  // the segment: steps k0 .. kend - 1
         int r0 = (pd_row0(U.len, U.qn, a.window) / PD_STEP + (int)(w0 + k0 - U.u0)) * PD_STEP;
-        for (int k = k0; k < kend; ++k, r0 += PD_STEP) {
-            if (!__all_sync(0xffffffffu, mbar_wait(bars + wslot, wpar))) {
-                bad = true;
-                break;
-            }
-            if (r0 >= all_lo && r0 + PD_STEP - 1 <= all_hi) step(std::false_type{}, r0);
-            else if (r0 <= any_hi && r0 + PD_STEP - 1 >= any_lo) step(std::true_type{}, r0);
-            __syncwarp();  // every lane has read the slot
-            issue();
-            if (++wslot == PD_SLOTS) {
-                wslot = 0;
-                wpar ^= 1u;
+        // Software pipeline: a step's products with V and the next one's scores stand in one piece of code, so that two
+        // chains of conversions and products are in flight in a warp (there are only two warps a scheduler).
+        auto arrived = [&]() {  // the step at wslot, wpar
+            if (__all_sync(0xffffffffu, mbar_wait(bars + wslot, wpar))) return true;
+            bad = true;
+            return false;
+        };
+        auto plain = [&](int r) { return r >= all_lo && r + PD_STEP - 1 <= all_hi; };
+        float x[2][4];
+        const uint8_t *sl = ring + wslot * (2 * C::TILE);
+        if (arrived()) {
+            scores(std::true_type{}, sl, r0, x);
+            for (int k = k0;; ++k) {
+                const bool more = k + 1 < kend;
+                const uint8_t *here = sl;
+                if (++wslot == PD_SLOTS) {
+                    wslot = 0;
+                    wpar ^= 1u;
+                }
+                if (more) {
+                    sl = ring + wslot * (2 * C::TILE);
+                    if (!arrived()) break;
+                }
+                reference(x);
+                probabilities(x);
+                if (more && plain(r0) && plain(r0 + PD_STEP)) {
+                    float y[2][4];
+                    scores(std::false_type{}, sl, r0 + PD_STEP, y);
+                    values(std::false_type{}, here, r0);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[n][e] = y[n][e];
+                } else {
+                    values(std::true_type{}, here, r0);
+                    if (more) scores(std::true_type{}, sl, r0 + PD_STEP, x);
+                }
+                __syncwarp();  // every lane has read the slot
+                issue();
+                r0 += PD_STEP;
+                if (!more) break;
             }
         }
 #pragma unroll
@@ -775,10 +800,8 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
         if (ms.last[k] < 0) continue;
         const PdSeg sg = ms.seg[ms.ent[ms.run[ms.last[k]]]];
         const int ca = pd_cta(sg.u0, N, C_), nc = pd_cta(sg.u1 - 1, N, C_) - ca + 1, rows = rows_of(sg);
-        auto state = [&](int c) {  // the unit's state of its c-th CTA
-            const int cta = ca + c;
-            return P.part + ((size_t)cta * 2 + (sg.u0 < pd_div(cta * N, C_) ? 0 : 1)) * C::STATE;
-        };
+        // the unit's state of its c-th CTA: the first one's second place (the unit starts there), the others' first
+        auto state = [&](int c) { return P.part + (size_t)((ca + c) * 2 + (c == 0)) * C::STATE; };
         // warp (r, part): row r, the CTAs part, part + parts, ...
         const int parts = max(1, PD_WARPS / rows), r = warp / parts, part = warp - r * parts;
         float M = PD_NONE, L = 0.f, y[V];
@@ -788,17 +811,31 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
             for (int c = lane; c < nc; c += 32) M = fmaxf(M, __ldcg(state(c) + PD_ROWS * HD + r));
 #pragma unroll
             for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-#pragma unroll 4
-            for (int c = part; c < nc; c += parts) {
-                const float *st = state(c);
-                const float f = ex2(__ldcg(st + PD_ROWS * HD + r) - M);
-                L += f * __ldcg(st + PD_ROWS * HD + 8 + r);
-                if constexpr (V == 4) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(st + r * HD) + lane);
-                    y[0] += f * x.x; y[1] += f * x.y; y[2] += f * x.z; y[V - 1] += f * x.w;
-                } else {
-                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(st + r * HD) + lane);
-                    y[0] += f * x.x; y[1] += f * x.y;
+            // 8 states' loads at a time
+            for (int c0_ = part; c0_ < nc; c0_ += 8 * parts) {
+                float f[8], ll[8], z[8][V];
+#pragma unroll
+                for (int k2 = 0; k2 < 8; ++k2) {
+                    const int c = min(c0_ + k2 * parts, nc - 1);
+                    const float *st = state(c);
+                    f[k2] = __ldcg(st + PD_ROWS * HD + r);
+                    ll[k2] = __ldcg(st + PD_ROWS * HD + 8 + r);
+                    if constexpr (V == 4) {
+                        const float4 q = __ldcg(reinterpret_cast<const float4 *>(st + r * HD) + lane);
+                        z[k2][0] = q.x; z[k2][1] = q.y; z[k2][2] = q.z; z[k2][V - 1] = q.w;
+                    } else {
+                        const float2 q = __ldcg(reinterpret_cast<const float2 *>(st + r * HD) + lane);
+                        z[k2][0] = q.x; z[k2][1] = q.y;
+                    }
+                }
+#pragma unroll
+                for (int k2 = 0; k2 < 8; ++k2) {
+                    const float w = c0_ + k2 * parts < nc ? ex2(f[k2] - M) : 0.f;
+                    if (c0_ + k2 * parts < nc) {
+                        L += w * ll[k2];
+#pragma unroll
+                        for (int e = 0; e < V; ++e) y[e] += w * z[k2][e];
+                    }
                 }
             }
         }
