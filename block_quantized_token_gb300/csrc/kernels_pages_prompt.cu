@@ -2,25 +2,31 @@
 // tensor cores.  o = softmax(scale q k^T) v with a running reference m and sums, as in kernels_pages_attn.cu:
 //   p_r = 2^(s_r - m + 7),  l = sum p_r,  o = sum p_r v_r   (s in log2 units; rescaled when a score passes m by 8).
 //
-// Work.  A CTA takes one (sequence, KV head) and two tiles of 128 query rows (a row is a (token, head of the KV
-// head's group), so a group's heads share the cached rows), and walks the cached rows in blocks of 128.
-//   warps 0-3, 4-7  a tile's softmax: thread = row = TMEM lane.  Reads S, writes P over it (fp16, the A operand of
-//                   the second product), keeps m and l, rescales O when it has to, writes the output.
-//   warps 8-11      turn codes into fp16 operands in shared memory, exactly (pages.cuh), K and V K-major with the
-//                   128-byte swizzle.
-//   warp 12         one thread issues the products: S = Q K^T (M = 128, N = 128), O += P V (N = HD), the two tiles in turn,
-//                   so the tensor cores work on one tile while the other's softmax runs.
-//   warp 13         requests the cached tiles: bulk copies into a ring of half blocks, each used by two operand warps.
-// TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x HD).
+// Work.  A CTA takes one (sequence, KV head) and some query rows (a row is a (token, head of the KV head's group), so
+// a group's heads share the cached rows), and walks the cached rows in blocks of 128.
+//   16-bit rows (pages_prompt_kernel): two tiles of 128 query rows.
+//     warps 0-3, 4-7  a tile's softmax: thread = row = TMEM lane.  Reads S, writes P over it (fp16, the A operand of
+//                     the second product), keeps m and l, rescales O when it has to, writes the output.
+//     warp 12         one thread issues the products: S = Q K^T (M = 128, N = 128), O += P V (N = HD), the two tiles in
+//                     turn, so the tensor cores work on one tile while the other's softmax runs.
+//     TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x HD).
+//   fp32 rows (pages_prompt32_kernel): one tile; queries and probabilities enter as hi + lo fp16 halves (2^-22), two
+//   products each.  The tensor cores' sums truncate (over thousands of rows 2^-18 of the output and growing), so a block's
+//   O starts from 0 and warps 4-7 add it to sums in registers, rounded to nearest.
+//     warps 0-3       softmax, as above; leaves each block's rescale factor in shared memory
+//     warps 4-7       o = o * factor + the block's O; writes the output
+//     warp 12         S of the block after next goes to the buffer whose P is used up, so the softmax never waits for it
+//     TMEM: two buffers of S/P, two of a block's O.
+//   Both: warps 8-11 turn codes into fp16 operands in shared memory, exactly (pages.cuh), K and V K-major with the
+//   128-byte swizzle, two stages each; warp 13 requests the cached tiles: bulk copies into a ring of half blocks, each
+//   used by two operand warps.
 //
 // The block's rows are put in the order k' = 32 a + 8 t + 4 b + 2 i + e for row 32 a + 16 b + 8 i + 2 t + e, in K's rows,
 // hence S's and P's columns, and in V's K dimension: so a thread that holds a code word of V of two 16-row tiles
 // holds 16 bytes of the operand.
 //
-// fp32 rows (SPLIT): queries and probabilities enter as hi + lo fp16 halves (2^-22), two products each; K and V are
-// exact as they are, and have one stage of shared memory instead of two.
-//
-// What bounds it: the products (2 x 1024 cycles a block and two tiles at HD = 128) and next to them the exponentials.
+// What bounds it: the products (2 x 1024 cycles a block and two tiles at HD = 128, 2048 a block for fp32) and the
+// softmax's latency between them.
 //
 // Masks.  Blocks that some row attends only in part mask S; there, rows of V that no row of the CTA attends are
 // zeroed (they may hold anything), and a NaN value of V is carried by K instead, so only rows that attend it see it.
@@ -35,19 +41,19 @@ constexpr int PP_BLOCK = 128;  // cached rows of a block
 constexpr int PP_RAW = 3;      // half blocks (four 16-row tiles) in the ring
 constexpr float PP_UP = 7.f, PP_SLACK = 8.f, PP_NONE = -3e38f;
 
-template <int HD, bool SPLIT>
+// 128-row operands in shared memory: Q of two tiles (fp32: hi and lo of one), two stages of K and of V; the ring
+template <int HD>
 struct PpCfg {
     static constexpr int TILE = pg_tile_bytes(HD);
     static constexpr int NB = HD / 32;
-    static constexpr int OP = 128 * HD * 2;  // bytes of a 128-row operand
-    static constexpr int PARTS = SPLIT ? 2 : 1;
-    static constexpr int NST = SPLIT ? 1 : 2;  // stages of K and of V
-    static constexpr int OFF_Q = 0;            // [tile][part]
-    static constexpr int OFF_K = OFF_Q + 2 * PARTS * OP;
-    static constexpr int OFF_V = OFF_K + NST * OP;
-    static constexpr int OFF_RAW = OFF_V + NST * OP;
+    static constexpr int OP = 128 * HD * 2;  // bytes of an operand
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + 2 * OP;
+    static constexpr int OFF_V = OFF_K + 2 * OP;
+    static constexpr int OFF_RAW = OFF_V + 2 * OP;
     static constexpr int OFF_BARS = OFF_RAW + PP_RAW * 4 * TILE;
-    static constexpr int SMEM = OFF_BARS + 512 + 1024;  // + alignment of the base
+    static constexpr int OFF_ROWS = OFF_BARS + 512;       // fp32: factors of two blocks, then m and l [2][128]
+    static constexpr int SMEM = OFF_ROWS + 2048 + 1024;  // + alignment of the base
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -58,7 +64,7 @@ struct PpArgs {
 };
 
 struct PpBars {
-    uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2];
+    uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], oempty[2], c[2], cempty[2];
     uint32_t tmem;
     int item[4];  // sequence, first query row, KV head, found
 };
@@ -192,19 +198,16 @@ __host__ __device__ constexpr int pp_place(int r) {
     return (r & ~31) + ((r >> 1) & 3) * 8 + ((r >> 4) & 1) * 4 + ((r >> 3) & 1) * 2 + (r & 1);
 }
 
-template <class T, int HD>
-__global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArgs P) {
-    constexpr bool SPLIT = sizeof(T) == 4;
-    using C = PpCfg<HD, SPLIT>;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // swizzle atoms: 1024-aligned
-    PpBars &B = *reinterpret_cast<PpBars *>(smem + C::OFF_BARS);
+// What a CTA works on: query rows f0 .. f0 + nf - 1 of sequence b, KV head h, against rows any_lo .. any_hi (those that
+// any of them attends) in nblk blocks from row base on; all of them attend rows all_lo .. all_hi.
+struct PpItem {
+    int b, h, f0, nf, q0, past, any_lo, any_hi, all_lo, all_hi, base, nblk;
+};
+// The item of this CTA: (sequence, ROWS query rows, KV head), heads fastest, a sequence's last rows first.  False: none.
+template <int ROWS>
+ER_DEV bool pp_find(const PpArgs &P, PpBars &B, int warp, int lane, PpItem &I) {
     const er_pages_attention_args &a = P.a;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // so that the compiler knows it is the same in the whole warp
     const int KV = P.p.KV, G = a.n_heads / KV, R = P.p.page_rows;
-
-    // ---- which item this CTA is: (sequence, pair of tiles, KV head), heads fastest, a sequence's last tiles first
     if (warp == 0) {
         const int x = blockIdx.x / KV;
         int found = 0, base = 0;
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 if (q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 || (long long)len > (long long)a.table_stride * R) {
                     if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
                 } else if ((long long)(q1 - q0) * G >= P.min_rows) {
-                    n = (int)(((long long)(q1 - q0) * G + 255) / 256);
+                    n = (int)(((long long)(q1 - q0) * G + ROWS - 1) / ROWS);
                 }
             }
             int inc = n;
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
             const bool mine = x >= first && x < first + n;
             if (mine) {
                 B.item[0] = b;
-                B.item[1] = (n - 1 - (x - first)) * 256;
+                B.item[1] = (n - 1 - (x - first)) * ROWS;
                 B.item[2] = blockIdx.x % KV;
             }
             found = __any_sync(0xffffffffu, mine);
@@ -238,20 +241,266 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
         if (lane == 0) B.item[3] = found;
     }
     __syncthreads();
-    if (!B.item[3]) return;
-    const int b = B.item[0], f0 = B.item[1], h = B.item[2];
-    const int q0 = a.q_start_dev[b], qn = a.q_start_dev[b + 1] - q0, len = a.lens_dev[b], past = len - qn;
-    const int nf = (int)min((long long)qn * G - f0, 256ll);  // query rows of this CTA
-    const int nx = nf > 128 ? 2 : 1;                         // tiles
-    // rows that any of them attends, and the blocks of 128 from a 16-row boundary on
-    const int any_hi = past + (f0 + nf - 1) / G;
-    const int any_lo = a.window ? max(0, past + f0 / G - a.window + 1) : 0;
-    const int base = any_lo & ~15;
-    const int nblk = any_hi < 0 ? 0 : (any_hi - base) / PP_BLOCK + 1;
-    // blocks whose rows all of them attend: rows all_lo .. all_hi
-    const int all_hi = past + f0 / G;
-    const int all_lo = a.window ? max(0, any_hi - a.window + 1) : 0;
+    if (!B.item[3]) return false;
+    I.b = B.item[0];
+    I.f0 = B.item[1];
+    I.h = B.item[2];
+    I.q0 = a.q_start_dev[I.b];
+    const int qn = a.q_start_dev[I.b + 1] - I.q0;
+    I.past = a.lens_dev[I.b] - qn;
+    I.nf = (int)min((long long)qn * G - I.f0, (long long)ROWS);
+    I.any_hi = I.past + (I.f0 + I.nf - 1) / G;
+    I.any_lo = a.window ? max(0, I.past + I.f0 / G - a.window + 1) : 0;
+    I.base = I.any_lo & ~15;
+    I.nblk = I.any_hi < 0 ? 0 : (I.any_hi - I.base) / PP_BLOCK + 1;
+    I.all_hi = I.past + I.f0 / G;
+    I.all_lo = a.window ? max(0, I.any_hi - a.window + 1) : 0;
+    return true;
+}
 
+// Whole warp: false once a wait gave up.  What depends on a warp that gave up waits in vain and gives up too, so every
+// wait ends.
+ER_DEV bool pp_wait(const PpArgs &P, uint64_t *bar, uint32_t par, int lane) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, par));
+    if (!ok && lane == 0) atomicOr(P.p.flags, ER_FLAG_WAIT);
+    return ok;
+}
+
+// A query row as a K-major operand: row r of the one at dst, times a power of two that brings its largest value to [2^14,
+// 2^15) (and the scale's sign); LO: the lo halves go to dst + OP.  Returns the factor that takes scores to log2 units.
+template <class T, int HD, bool LO>
+ER_DEV float pp_query(const er_pages_attention_args &a, uint8_t *dst, const T *src, bool real, int r) {
+    using C = PpCfg<HD>;
+    const bool vec = ((uintptr_t)a.q_dev & 15) == 0 && (a.q_stride * sizeof(T)) % 16 == 0;
+    auto load8 = [&](int c, float (&x)[8]) {
+        __align__(16) T v[8];
+        if (!real) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = pg_cvt<T>(0.f);
+        } else if (vec) {
+#pragma unroll
+            for (int k = 0; k < (int)(8 * sizeof(T)) / 16; ++k)
+                reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(src + 8 * c)[k];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = src[8 * c + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = pg_ld<T>(v + e);
+    };
+    float top = 0.f;
+    bool odd = false;
+#pragma unroll 4
+    for (int c = 0; c < HD / 8; ++c) {
+        float x[8];
+        load8(c, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            top = fmaxf(top, fabsf(x[e]));
+            odd |= !(fabsf(x[e]) <= 3.4028235e38f);
+        }
+    }
+    // an infinite or NaN query: the row is NaN, and so are its scores
+    const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 253);
+    const float scale = a.scale != 0.f ? a.scale : 1.f / sqrtf((float)HD);
+    const float up = odd ? NAN : copysignf(__uint_as_float((uint32_t)(268 - ex) << 23), scale);
+    // (a factor too small for fp32 still has to leave -infinity as it is)
+    const float down = fmaxf(__uint_as_float((uint32_t)(ex - 14) << 23) * (fabsf(scale) * 1.4426950408889634f), 1.2e-38f);
+    dst += r * 128;
+#pragma unroll 4
+    for (int c = 0; c < HD / 8; ++c) {
+        float x[8];
+        load8(c, x);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float y0 = x[2 * k] * up, y1 = x[2 * k + 1] * up;
+            hi[k] = pp_pack(y0, y1);
+            const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
+            lo[k] = pp_pack(y0 - z.x, y1 - z.y);
+        }
+        uint8_t *d = dst + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if constexpr (LO) *reinterpret_cast<uint4 *>(d + C::OP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    return down;
+}
+
+// ---- operands (warps 8-11).  Half block i of the walk (block i / 2) lies in ring slot i % PP_RAW; warps 8, 9 use the first
+// halves, 10 and 11 the second
+template <int HD>
+ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem &I, int warp, int lane) {
+    using C = PpCfg<HD>;
+    const int any_lo = I.any_lo, any_hi = I.any_hi, all_lo = I.all_lo, all_hi = I.all_hi, base = I.base, nblk = I.nblk;
+    auto wait = [&](uint64_t *bar, uint32_t par) { return pp_wait(P, bar, par, lane); };
+    const int pw = warp - 8, g = lane >> 2, t = lane & 3, half = pw >> 1;
+    const uint8_t *ring = smem + C::OFF_RAW;
+    bool ok = true;
+    int slot = half, par = 0;  // of half block 2 j + half
+    for (int j = 0; j < nblk; ++j) {
+        const int st = j & 1, ph = (j >> 1) & 1;
+        ok = wait(B.raw + slot, par);
+        if (!ok) break;
+        const uint8_t *raw = ring + slot * (4 * C::TILE);
+        const int r0 = base + PP_BLOCK * j;
+        const bool edge = r0 < all_lo || r0 + PP_BLOCK - 1 > all_hi;
+        // ---- K: a job is 8 rows, a lane one row's words of quad lane t
+        if (j >= 2) ok = wait(B.kempty + st, ph ^ 1);
+        if (!ok) break;
+        uint8_t *kd = smem + C::OFF_K + st * C::OP;
+#pragma unroll 2
+        for (int job = 0; job < 4; ++job) {
+            const int rr = 8 * (4 * pw + job) + g, in = rr & 15;
+            const uint8_t *src = raw + ((rr >> 4) & 3) * C::TILE;
+            uint32_t w[C::NB], ds[C::NB / 2];
+            if constexpr (HD == 128) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + in * 64 + t * 16);
+                w[0] = x.x; w[1] = x.y; w[2] = x.z; w[C::NB - 1] = x.w;
+                const uint2 y = *reinterpret_cast<const uint2 *>(src + pg_off_ks(HD) + in * 8);
+                ds[0] = y.x; ds[C::NB / 2 - 1] = y.y;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(src + in * 32 + t * 8);
+                w[0] = x.x; w[1] = x.y;
+                ds[0] = *reinterpret_cast<const uint32_t *>(src + pg_off_ks(HD) + in * 4);
+            }
+            if (edge) {  // a row with a NaN value: its K carries it
+                const unsigned short *vs = reinterpret_cast<const unsigned short *>(src + pg_off_vs(HD));
+                bool nan = false;
+#pragma unroll
+                for (int bb = 0; bb < C::NB; ++bb) nan |= (vs[pg_vs_half(in, bb, HD)] & 0x7FFF) > 0x7C00;
+                if (nan)
+#pragma unroll
+                    for (int k = 0; k < C::NB / 2; ++k) ds[k] = 0x7FFF7FFFu;
+            }
+            const int n = pp_place(rr);
+            uint8_t *dst = kd + n * 128;
+            // an odd row writes its blocks in the other order: 8 lanes then cover all the bank groups
+#pragma unroll
+            for (int k = 0; k < C::NB; ++k) {
+                const uint32_t ww = (g & 1) ? w[k ^ 1] : w[k];
+                const int bb = (g & 1) ? k ^ 1 : k;
+                const uint32_t dd = ds[k >> 1], d = prmt(dd, dd, (bb & 1) ? 0x3232u : 0x1010u), z = pp_m24(d);
+                *reinterpret_cast<uint4 *>(dst + (k >> 1) * 16384 + (((4 * (bb & 1) + t) ^ (n & 7)) << 4)) =
+                    make_uint4(pp_val<0>(ww, d, z), pp_val<1>(ww, d, z), pp_val<2>(ww, d, z), pp_val<3>(ww, d, z));
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) pp_arrive(B.kfull + st);
+        // ---- V: a lane holds 4 rows of one dim of two tiles: 16 bytes of the operand
+        if (j >= 2) ok = wait(B.vempty + st, ph ^ 1);
+        if (!ok) break;
+        uint8_t *vd = smem + C::OFF_V + st * C::OP;
+        const int q = HD == 128 ? pw & 1 : 0;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const int pair = 2 * half + (k ^ (g & 1));  // odd g takes the pairs in the other order (bank groups again)
+            const uint8_t *sa = raw + (2 * pair & 3) * C::TILE, *sb = sa + C::TILE;
+            constexpr int NU = HD == 128 ? 4 : 2;  // words of a lane (HD = 64: a warp takes half of them)
+            const int u0 = HD == 128 ? 0 : 2 * (pw & 1);
+            uint32_t wa[NU], wb[NU], da[NU / 2][2], db[NU / 2][2];
+            if constexpr (HD == 128) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(sa + pg_off_v(HD) + q * 512 + lane * 16);
+                const uint4 y = *reinterpret_cast<const uint4 *>(sb + pg_off_v(HD) + q * 512 + lane * 16);
+                wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[NU - 1] = x.w;
+                wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[NU - 1] = y.w;
+                const uint4 v = *reinterpret_cast<const uint4 *>(sa + pg_off_vs(HD) + t * 32 + 16 * q);
+                const uint4 z = *reinterpret_cast<const uint4 *>(sb + pg_off_vs(HD) + t * 32 + 16 * q);
+                da[0][0] = v.x; da[0][1] = v.y; da[NU / 2 - 1][0] = v.z; da[NU / 2 - 1][1] = v.w;
+                db[0][0] = z.x; db[0][1] = z.y; db[NU / 2 - 1][0] = z.z; db[NU / 2 - 1][1] = z.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(sa + pg_off_v(HD) + lane * 16 + 4 * u0);
+                const uint2 y = *reinterpret_cast<const uint2 *>(sb + pg_off_v(HD) + lane * 16 + 4 * u0);
+                wa[0] = x.x; wa[1] = x.y;
+                wb[0] = y.x; wb[1] = y.y;
+                const uint2 v = *reinterpret_cast<const uint2 *>(sa + pg_off_vs(HD) + t * 16 + 4 * u0);
+                const uint2 z = *reinterpret_cast<const uint2 *>(sb + pg_off_vs(HD) + t * 16 + 4 * u0);
+                da[0][0] = v.x; da[0][1] = v.y;
+                db[0][0] = z.x; db[0][1] = z.y;
+            }
+            if (edge) {  // scales of rows that nobody attends, or that are NaN: 0
+#pragma unroll
+                for (int x = 0; x < NU / 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t part = e ? 0xFFFF0000u : 0x0000FFFFu, inf = 0x7C007C00u & part;
+                            const int ra = r0 + 32 * pair + 2 * t + e + 8 * i, rb = ra + 16;
+                            if ((da[x][i] & 0x7FFF7FFFu & part) > inf || ra < any_lo || ra > any_hi) da[x][i] &= ~part;
+                            if ((db[x][i] & 0x7FFF7FFFu & part) > inf || rb < any_lo || rb > any_hi) db[x][i] &= ~part;
+                        }
+            }
+            uint8_t *dst = vd + half * (HD * 128) + ((((pair & 1) * 4 + t) ^ g) << 4);
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                const uint32_t a0 = da[u >> 1][0], a1 = da[u >> 1][1], b0 = db[u >> 1][0], b1 = db[u >> 1][1];
+                const uint32_t za0 = pp_m24(a0), za1 = pp_m24(a1), zb0 = pp_m24(b0), zb1 = pp_m24(b1);
+                const int d = 64 * q + 16 * (u0 + u) + g;
+                *reinterpret_cast<uint4 *>(dst + d * 128) =
+                    make_uint4(pp_val<0>(wa[u], a0, za0), pp_val<2>(wa[u], a1, za1), pp_val<0>(wb[u], b0, zb0),
+                               pp_val<2>(wb[u], b1, zb1));
+                *reinterpret_cast<uint4 *>(dst + (d + 8) * 128) =
+                    make_uint4(pp_val<1>(wa[u], a0, za0), pp_val<3>(wa[u], a1, za1), pp_val<1>(wb[u], b0, zb0),
+                               pp_val<3>(wb[u], b1, zb1));
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) pp_arrive(B.vfull + st);
+        if (lane == 0) pp_arrive(B.rawfree + slot);
+        slot += 2;
+        if (slot >= PP_RAW) {
+            slot -= PP_RAW;
+            par ^= 1;
+        }
+    }
+}
+
+// ---- copies (warp 13): lane i < 4 requests tile i of each half block; the pages are looked up one half block ahead
+template <int HD>
+ER_DEV void pp_copies(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem &I, int lane) {
+    using C = PpCfg<HD>;
+    const er_pages_attention_args &a = P.a;
+    const int KV = P.p.KV, R = P.p.page_rows, b = I.b, h = I.h, base = I.base, any_hi = I.any_hi;
+    auto wait = [&](uint64_t *bar, uint32_t par) { return pp_wait(P, bar, par, lane); };
+    const int nhalf = 2 * I.nblk;
+    auto page_of = [&](int i) {  // the table's entry for tile `lane` of half block i; -1: nothing to read there
+        const int row = base + 64 * i + 16 * lane;
+        return lane < 4 && i < nhalf && row <= any_hi ? a.tables_dev[(size_t)b * a.table_stride + row / R] : -1;
+    };
+    int page = page_of(0), slot = 0, par = 1;
+    bool ok = true;
+    int i = 0;
+    for (; i < nhalf; ++i) {
+        if (i >= PP_RAW) ok = wait(B.rawfree + slot, par);
+        if (!ok) break;
+        const int row = base + 64 * i + 16 * lane;
+        const bool there = lane < 4 && row <= any_hi;
+        if (there && (page < 0 || page >= P.p.n_pages)) {
+            atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
+            page = 0;
+        }
+        const int n = __popc(__ballot_sync(0xffffffffu, there));
+        if (lane == 0) mbar_arrive_expect_tx(B.raw + slot, n * C::TILE);
+        __syncwarp();
+        if (there)
+            bulk_g2s(smem + C::OFF_RAW + (slot * 4 + lane) * C::TILE,
+                     P.p.pool + (((size_t)page * KV + h) * (R >> 4) + ((row % R) >> 4)) * C::TILE, C::TILE,
+                     B.raw + slot);
+        page = page_of(i + 1);
+        if (++slot == PP_RAW) {
+            slot = 0;
+            par ^= 1;
+        }
+    }
+    // given up: copies may still be landing
+    if (!ok)
+        for (int k = max(0, i - PP_RAW); k < i; ++k) mbar_wait(B.raw + k % PP_RAW, (k / PP_RAW) & 1);
+}
+
+// barriers (thread 0) and the whole of TMEM (warp 12)
+ER_DEV void pp_setup(PpBars &B, int tid, int warp) {
     if (tid == 0) {
         for (int i = 0; i < PP_RAW; ++i) {
             mbar_init(B.raw + i, 1);
@@ -265,6 +514,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
             mbar_init(B.s + i, 1);
             mbar_init(B.p + i, 4);
             mbar_init(B.o + i, 1);
+            mbar_init(B.oempty + i, 4);
+            mbar_init(B.c + i, 4);
+            mbar_init(B.cempty + i, 4);
         }
         fence_mbar_init();
     }
@@ -273,97 +525,132 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // ---- queries: thread = row, a power of two brings its largest value to [2^14, 2^15)
-    const int X = warp >> 2;             // softmax warps: their tile
-    const int r = tid & 127;             // and row of it
-    const bool soft = warp < 8 && X < nx;
-    int row = 0, head = 0, tok = 0;
+}
+ER_DEV void pp_close(PpBars &B, int warp) {
+    __syncwarp();
+    pp_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        pp_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(B.tmem), "r"(512) : "memory");
+    }
+}
+// the whole of TMEM is allocated: it starts at 0, which keeps its addresses constants
+constexpr uint32_t PP_TMEM = 0;
+
+// S = Q K^T, D (+)= P V, issued by the lane with `one` set
+template <int HD>
+ER_DEV void pp_score(uint32_t d, uint32_t q, uint32_t k, bool more, uint32_t one) {
+#pragma unroll
+    for (int i = 0; i < HD / 16; ++i) {
+        const uint32_t at = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32);
+        pp_mma_ss(d, pp_desc(q) + (at >> 4), pp_desc(k) + (at >> 4), pp_idesc(128), more || i > 0, one);
+    }
+}
+template <int HD>
+ER_DEV void pp_value(uint32_t d, uint32_t p, uint32_t v, bool more, uint32_t one) {
+#pragma unroll
+    for (int i = 0; i < PP_BLOCK / 16; ++i)
+        pp_mma_ts(d, p + i * 8, pp_desc(v) + (((i >> 2) * (HD * 128) + (i & 3) * 32) >> 4), pp_idesc(HD), more || i > 0, one);
+}
+
+// One block's scores of a row in registers: masked, their largest, and the probabilities written over them.
+ER_DEV void pp_mask(float (&s)[128], int lo, int hi) {
+#pragma unroll
+    for (int k = 0; k < 128; ++k)
+        if (pp_row(k) < lo || pp_row(k) > hi) s[k] = -INFINITY;
+}
+ER_DEV float pp_largest(const float (&s)[128]) {
+    float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int k = 4; k < 124; k += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = pp_max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
+    return pp_max3(pp_max3(mx[0], mx[1], fmaxf(s[124], s[125])), pp_max3(mx[2], mx[3], s[126]), s[127]);
+}
+// p = 2^(s down - m + PP_UP) as fp16 over S's first 64 columns (LO: the lo halves over the others); returns their sum
+template <bool LO>
+ER_DEV float pp_probabilities(const float (&s)[128], uint32_t tS, float down, float m) {
+    const float2 nb = make_float2(PP_UP - m, PP_UP - m), dn = make_float2(down, down);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {  // 32 columns of S become 16 of P: few registers beside S itself
+        uint32_t ph[16];
+        [[maybe_unused]] uint32_t pl[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            float2 x = pp_fma2(make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), dn, nb);
+            x.x = pp_ex2(x.x);
+            x.y = pp_ex2(x.y);
+            sum[k & 1] = pp_add2(sum[k & 1], x);
+            ph[k] = pp_pack(x.x, x.y);
+            if constexpr (LO) {
+                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&ph[k]));
+                pl[k] = pp_pack(x.x - z.x, x.y - z.y);
+            }
+        }
+        pp_st16(tS + 16 * q, ph);
+        if constexpr (LO) pp_st16(tS + 64 + 16 * q, pl);
+    }
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+// 32 values of an output row
+template <class T>
+ER_DEV void pp_store(const er_pages_attention_args &a, T *out, const float *o, float l, float inv) {
+    const bool vec = ((uintptr_t)a.out_dev & 15) == 0 && (a.out_stride * sizeof(T)) % 16 == 0;
+    __align__(16) T v[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = pg_cvt<T>(l == 0.f ? 0.f : o[e] * inv);
+    if (vec) {
+#pragma unroll
+        for (int e = 0; e < (int)(32 * sizeof(T)) / 16; ++e) reinterpret_cast<uint4 *>(out)[e] = reinterpret_cast<uint4 *>(v)[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) out[e] = v[e];
+    }
+}
+ER_DEV float pp_lse(float m, float l) { return l == 0.f ? -INFINITY : (m - PP_UP + log2f(l)) * 0.6931471805599453f; }
+
+// ---------------------------------------------------------------------------
+template <class T, int HD>
+__global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArgs P) {
+    using C = PpCfg<HD>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // swizzle atoms: 1024-aligned
+    PpBars &B = *reinterpret_cast<PpBars *>(smem + C::OFF_BARS);
+    const er_pages_attention_args &a = P.a;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // so that the compiler knows it is the same in the whole warp
+    const int G = a.n_heads / P.p.KV;
+    PpItem I;
+    if (!pp_find<256>(P, B, warp, lane, I)) return;
+    const int nx = I.nf > 128 ? 2 : 1;  // tiles
+    pp_setup(B, tid, warp);
+    // a softmax thread's tile and row
+    const int X = warp >> 2, r = tid & 127, f = I.f0 + X * 128 + r, tok = f / G;
+    const int row = I.q0 + tok, head = I.h * G + (f - tok * G);
+    const bool soft = warp < 8 && X < nx, real = X * 128 + r < I.nf;
     float down = 0.f;
     if (soft) {
-        const int f = f0 + X * 128 + r;
-        const bool real = X * 128 + r < nf;
-        tok = f / G;
-        row = q0 + tok;
-        head = h * G + (f - tok * G);
-        const T *src = (const T *)a.q_dev + row * a.q_stride + (size_t)head * HD;
-        const bool vec = ((uintptr_t)a.q_dev & 15) == 0 && (a.q_stride * sizeof(T)) % 16 == 0;
-        auto load8 = [&](int c, float (&x)[8]) {
-            __align__(16) T v[8];
-            if (!real) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = pg_cvt<T>(0.f);
-            } else if (vec) {
-#pragma unroll
-                for (int k = 0; k < (int)(8 * sizeof(T)) / 16; ++k)
-                    reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(src + 8 * c)[k];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = src[8 * c + e];
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = pg_ld<T>(v + e);
-        };
-        float top = 0.f;
-        bool odd = false;
-#pragma unroll 4
-        for (int c = 0; c < HD / 8; ++c) {
-            float x[8];
-            load8(c, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                top = fmaxf(top, fabsf(x[e]));
-                odd |= !(fabsf(x[e]) <= 3.4028235e38f);
-            }
-        }
-        // an infinite or NaN query: the row is NaN, and so are its scores
-        const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 253);
-        const float scale = a.scale != 0.f ? a.scale : 1.f / sqrtf((float)HD);
-        const float up = odd ? NAN : copysignf(__uint_as_float((uint32_t)(268 - ex) << 23), scale);
-        // (a factor too small for fp32 still has to leave -infinity as it is)
-        down = fmaxf(__uint_as_float((uint32_t)(ex - 14) << 23) * (fabsf(scale) * 1.4426950408889634f), 1.2e-38f);
-        uint8_t *dst = smem + C::OFF_Q + X * C::PARTS * C::OP + r * 128;
-#pragma unroll 4
-        for (int c = 0; c < HD / 8; ++c) {
-            float x[8];
-            load8(c, x);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float y0 = x[2 * k] * up, y1 = x[2 * k + 1] * up;
-                hi[k] = pp_pack(y0, y1);
-                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
-                lo[k] = pp_pack(y0 - z.x, y1 - z.y);
-            }
-            uint8_t *d = dst + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if constexpr (SPLIT) *reinterpret_cast<uint4 *>(d + C::OP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+        down = pp_query<T, HD, false>(a, smem + C::OFF_Q + X * C::OP,
+                                      (const T *)a.q_dev + row * a.q_stride + (size_t)head * HD, real, r);
         fence_proxy_async_smem();
     }
     pp_fence_before();
     __syncthreads();
     pp_fence_after();
-    // the whole of TMEM is allocated: it starts at 0, which keeps its addresses constants
-    constexpr uint32_t tmem = 0;
-    // Whole warp: false once a wait gave up.  What depends on a warp that gave up waits in vain and gives up too, so
-    // every wait ends.
-    auto wait = [&](uint64_t *bar, uint32_t par) {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, par));
-        if (!ok && lane == 0) atomicOr(P.p.flags, ER_FLAG_WAIT);
-        return ok;
-    };
+    auto wait = [&](uint64_t *bar, uint32_t par) { return pp_wait(P, bar, par, lane); };
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        if (X < nx) {
-            const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
+        if (soft) {
+            const uint32_t tl = PP_TMEM + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
             const uint32_t tS = tl + X * 128, tO = tl + 256 + X * HD;
-            const bool real = X * 128 + r < nf;
-            const int pos = real ? past + tok : -1;
+            const int pos = real ? I.past + tok : -1;
             const int first = a.window ? max(0, pos - a.window + 1) : 0;
             float m = PP_NONE, l = 0.f;
             bool ok = true;
-            for (int j = 0; j < nblk; ++j) {
+            for (int j = 0; j < I.nblk; ++j) {
                 ok = wait(B.s + X, j & 1);
                 if (!ok) break;
                 pp_fence_after();
@@ -372,19 +659,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 for (int k = 0; k < 4; ++k) pp_ld32(tS + 32 * k, s + 32 * k);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) pp_wait_ld(s + 32 * k);
-                const int r0 = base + PP_BLOCK * j;
-                if (__any_sync(0xffffffffu, r0 < first || r0 + PP_BLOCK - 1 > pos)) {
-                    const int lo = first - r0, hi = pos - r0;
-#pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (pp_row(k) < lo || pp_row(k) > hi) s[k] = -INFINITY;
-                }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int k = 4; k < 124; k += 8)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = pp_max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
-                const float mt = pp_max3(pp_max3(mx[0], mx[1], fmaxf(s[124], s[125])), pp_max3(mx[2], mx[3], s[126]), s[127]) * down;
+                const int r0 = I.base + PP_BLOCK * j;
+                if (__any_sync(0xffffffffu, r0 < first || r0 + PP_BLOCK - 1 > pos)) pp_mask(s, first - r0, pos - r0);
+                const float mt = pp_largest(s) * down;
                 if (__any_sync(0xffffffffu, mt > m + PP_SLACK)) {
                     const float mn = mt > m + PP_SLACK ? mt : m;
                     const float corr = mn == m ? 1.f : pp_ex2(m - mn);
@@ -402,242 +679,62 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                         }
                     }
                 }
-                const float2 nb = make_float2(PP_UP - m, PP_UP - m), dn = make_float2(down, down);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {  // 32 columns of S become 16 of P: few registers beside S itself
-                    uint32_t ph[16];
-                    [[maybe_unused]] uint32_t pl[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float2 x = pp_fma2(make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), dn, nb);
-                        x.x = pp_ex2(x.x);
-                        x.y = pp_ex2(x.y);
-                        sum[k & 1] = pp_add2(sum[k & 1], x);
-                        ph[k] = pp_pack(x.x, x.y);
-                        if constexpr (SPLIT) {
-                            const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&ph[k]));
-                            pl[k] = pp_pack(x.x - z.x, x.y - z.y);
-                        }
-                    }
-                    pp_st16(tS + 16 * q, ph);
-                    if constexpr (SPLIT) pp_st16(tS + 64 + 16 * q, pl);
-                }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                l += pp_probabilities<false>(s, tS, down, m);
                 pp_wait_st();
                 pp_fence_before();
                 __syncwarp();
                 if (lane == 0) pp_arrive(B.p + X);
             }
-            if (ok && nblk > 0) ok = wait(B.o + X, 0);
+            if (ok && I.nblk > 0) ok = wait(B.o + X, 0);
             if (ok) {
                 pp_fence_after();
                 T *out = (T *)a.out_dev + row * a.out_stride + (size_t)head * HD;
-                const bool vec = ((uintptr_t)a.out_dev & 15) == 0 && (a.out_stride * sizeof(T)) % 16 == 0;
                 const float inv = 1.f / l;
 #pragma unroll 1
                 for (int k = 0; k < HD / 32; ++k) {
                     float o[32];
-                    if (nblk > 0) {
+                    if (I.nblk > 0) {
                         pp_ld32(tO + 32 * k, o);
                         pp_wait_ld(o);
                     }
-                    if (!real) continue;
-                    __align__(16) T v[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = pg_cvt<T>(l == 0.f ? 0.f : o[e] * inv);
-                    if (vec) {
-#pragma unroll
-                        for (int e = 0; e < (int)(32 * sizeof(T)) / 16; ++e)
-                            reinterpret_cast<uint4 *>(out + 32 * k)[e] = reinterpret_cast<uint4 *>(v)[e];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) out[32 * k + e] = v[e];
-                    }
+                    if (real) pp_store<T>(a, out + 32 * k, o, l, inv);
                 }
-                if (real && a.lse_dev)
-                    a.lse_dev[(size_t)row * a.n_heads + head] =
-                        l == 0.f ? -INFINITY : (m - PP_UP + log2f(l)) * 0.6931471805599453f;
+                if (real && a.lse_dev) a.lse_dev[(size_t)row * a.n_heads + head] = pp_lse(m, l);
             }
         }
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        // ---- operands.  Half block i of the walk (block i / 2) lies in ring slot i % PP_RAW; warps 8, 9 use the first
-        // halves, 10 and 11 the second
-        const int pw = warp - 8, g = lane >> 2, t = lane & 3, half = pw >> 1;
-        const uint8_t *ring = smem + C::OFF_RAW;
-        bool ok = true;
-        int slot = half, par = 0;  // of half block 2 j + half
-        for (int j = 0; j < nblk; ++j) {
-            const int st = C::NST == 2 ? j & 1 : 0, ph = C::NST == 2 ? (j >> 1) & 1 : j & 1;
-            ok = wait(B.raw + slot, par);
-            if (!ok) break;
-            const uint8_t *raw = ring + slot * (4 * C::TILE);
-            const int r0 = base + PP_BLOCK * j;
-            const bool edge = r0 < all_lo || r0 + PP_BLOCK - 1 > all_hi;
-            // ---- K: a job is 8 rows, a lane one row's words of quad lane t
-            if (j >= C::NST) ok = wait(B.kempty + st, ph ^ 1);
-            if (!ok) break;
-            uint8_t *kd = smem + C::OFF_K + st * C::OP;
-#pragma unroll 2
-            for (int job = 0; job < 4; ++job) {
-                const int rr = 8 * (4 * pw + job) + g, in = rr & 15;
-                const uint8_t *src = raw + ((rr >> 4) & 3) * C::TILE;
-                uint32_t w[C::NB], ds[C::NB / 2];
-                if constexpr (HD == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + in * 64 + t * 16);
-                    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[C::NB - 1] = x.w;
-                    const uint2 y = *reinterpret_cast<const uint2 *>(src + pg_off_ks(HD) + in * 8);
-                    ds[0] = y.x; ds[C::NB / 2 - 1] = y.y;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(src + in * 32 + t * 8);
-                    w[0] = x.x; w[1] = x.y;
-                    ds[0] = *reinterpret_cast<const uint32_t *>(src + pg_off_ks(HD) + in * 4);
-                }
-                if (edge) {  // a row with a NaN value: its K carries it
-                    const unsigned short *vs = reinterpret_cast<const unsigned short *>(src + pg_off_vs(HD));
-                    bool nan = false;
-#pragma unroll
-                    for (int bb = 0; bb < C::NB; ++bb) nan |= (vs[pg_vs_half(in, bb, HD)] & 0x7FFF) > 0x7C00;
-                    if (nan)
-#pragma unroll
-                        for (int k = 0; k < C::NB / 2; ++k) ds[k] = 0x7FFF7FFFu;
-                }
-                const int n = pp_place(rr);
-                uint8_t *dst = kd + n * 128;
-                // an odd row writes its blocks in the other order: 8 lanes then cover all the bank groups
-#pragma unroll
-                for (int k = 0; k < C::NB; ++k) {
-                    const uint32_t ww = (g & 1) ? w[k ^ 1] : w[k];
-                    const int bb = (g & 1) ? k ^ 1 : k;
-                    const uint32_t dd = ds[k >> 1], d = prmt(dd, dd, (bb & 1) ? 0x3232u : 0x1010u), z = pp_m24(d);
-                    *reinterpret_cast<uint4 *>(dst + (k >> 1) * 16384 + (((4 * (bb & 1) + t) ^ (n & 7)) << 4)) =
-                        make_uint4(pp_val<0>(ww, d, z), pp_val<1>(ww, d, z), pp_val<2>(ww, d, z), pp_val<3>(ww, d, z));
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) pp_arrive(B.kfull + st);
-            // ---- V: a lane holds 4 rows of one dim of two tiles: 16 bytes of the operand
-            if (j >= C::NST) ok = wait(B.vempty + st, ph ^ 1);
-            if (!ok) break;
-            uint8_t *vd = smem + C::OFF_V + st * C::OP;
-            const int q = HD == 128 ? pw & 1 : 0;
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-                const int pair = 2 * half + (k ^ (g & 1));  // odd g takes the pairs in the other order (bank groups again)
-                const uint8_t *sa = raw + (2 * pair & 3) * C::TILE, *sb = sa + C::TILE;
-                constexpr int NU = HD == 128 ? 4 : 2;  // words of a lane (HD = 64: a warp takes half of them)
-                const int u0 = HD == 128 ? 0 : 2 * (pw & 1);
-                uint32_t wa[NU], wb[NU], da[NU / 2][2], db[NU / 2][2];
-                if constexpr (HD == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(sa + pg_off_v(HD) + q * 512 + lane * 16);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(sb + pg_off_v(HD) + q * 512 + lane * 16);
-                    wa[0] = x.x; wa[1] = x.y; wa[2] = x.z; wa[NU - 1] = x.w;
-                    wb[0] = y.x; wb[1] = y.y; wb[2] = y.z; wb[NU - 1] = y.w;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(sa + pg_off_vs(HD) + t * 32 + 16 * q);
-                    const uint4 z = *reinterpret_cast<const uint4 *>(sb + pg_off_vs(HD) + t * 32 + 16 * q);
-                    da[0][0] = v.x; da[0][1] = v.y; da[NU / 2 - 1][0] = v.z; da[NU / 2 - 1][1] = v.w;
-                    db[0][0] = z.x; db[0][1] = z.y; db[NU / 2 - 1][0] = z.z; db[NU / 2 - 1][1] = z.w;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(sa + pg_off_v(HD) + lane * 16 + 4 * u0);
-                    const uint2 y = *reinterpret_cast<const uint2 *>(sb + pg_off_v(HD) + lane * 16 + 4 * u0);
-                    wa[0] = x.x; wa[1] = x.y;
-                    wb[0] = y.x; wb[1] = y.y;
-                    const uint2 v = *reinterpret_cast<const uint2 *>(sa + pg_off_vs(HD) + t * 16 + 4 * u0);
-                    const uint2 z = *reinterpret_cast<const uint2 *>(sb + pg_off_vs(HD) + t * 16 + 4 * u0);
-                    da[0][0] = v.x; da[0][1] = v.y;
-                    db[0][0] = z.x; db[0][1] = z.y;
-                }
-                if (edge) {  // scales of rows that nobody attends, or that are NaN: 0
-#pragma unroll
-                    for (int x = 0; x < NU / 2; ++x)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t part = e ? 0xFFFF0000u : 0x0000FFFFu, inf = 0x7C007C00u & part;
-                                const int ra = r0 + 32 * pair + 2 * t + e + 8 * i, rb = ra + 16;
-                                if ((da[x][i] & 0x7FFF7FFFu & part) > inf || ra < any_lo || ra > any_hi) da[x][i] &= ~part;
-                                if ((db[x][i] & 0x7FFF7FFFu & part) > inf || rb < any_lo || rb > any_hi) db[x][i] &= ~part;
-                            }
-                }
-                uint8_t *dst = vd + half * (HD * 128) + ((((pair & 1) * 4 + t) ^ g) << 4);
-#pragma unroll
-                for (int u = 0; u < NU; ++u) {
-                    const uint32_t a0 = da[u >> 1][0], a1 = da[u >> 1][1], b0 = db[u >> 1][0], b1 = db[u >> 1][1];
-                    const uint32_t za0 = pp_m24(a0), za1 = pp_m24(a1), zb0 = pp_m24(b0), zb1 = pp_m24(b1);
-                    const int d = 64 * q + 16 * (u0 + u) + g;
-                    *reinterpret_cast<uint4 *>(dst + d * 128) =
-                        make_uint4(pp_val<0>(wa[u], a0, za0), pp_val<2>(wa[u], a1, za1), pp_val<0>(wb[u], b0, zb0),
-                                   pp_val<2>(wb[u], b1, zb1));
-                    *reinterpret_cast<uint4 *>(dst + (d + 8) * 128) =
-                        make_uint4(pp_val<1>(wa[u], a0, za0), pp_val<3>(wa[u], a1, za1), pp_val<1>(wb[u], b0, zb0),
-                                   pp_val<3>(wb[u], b1, zb1));
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) pp_arrive(B.vfull + st);
-            if (lane == 0) pp_arrive(B.rawfree + slot);
-            slot += 2;
-            if (slot >= PP_RAW) {
-                slot -= PP_RAW;
-                par ^= 1;
-            }
-        }
+        pp_operands<HD>(P, B, smem, I, warp, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-        if (warp == 12 && nblk > 0) {
-            // ---- products, issued by one thread; the whole warp waits
+        if (warp == 12 && I.nblk > 0) {
             const uint32_t qb = smem_u32(smem + C::OFF_Q), kb = smem_u32(smem + C::OFF_K), vb = smem_u32(smem + C::OFF_V);
-            constexpr uint32_t ID_S = pp_idesc(128), ID_O = pp_idesc(HD);
             const uint32_t one = pp_elect();
-            auto score = [&](int x, int st) {  // S_x = Q_x K^T
-#pragma unroll
-                for (int part = 0; part < C::PARTS; ++part)
-#pragma unroll
-                    for (int k = 0; k < HD / 16; ++k) {
-                        const uint32_t at = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
-                        pp_mma_ss(tmem + x * 128, pp_desc(qb + (x * C::PARTS + part) * C::OP) + (at >> 4),
-                                  pp_desc(kb + st * C::OP) + (at >> 4), ID_S, part + k > 0, one);
-                    }
-            };
-            auto value = [&](int x, int st, bool more) {  // O_x (+)= P_x V
-#pragma unroll
-                for (int part = 0; part < C::PARTS; ++part)
-#pragma unroll
-                    for (int k = 0; k < PP_BLOCK / 16; ++k)
-                        pp_mma_ts(tmem + 256 + x * HD, tmem + x * 128 + part * 64 + k * 8,
-                                  pp_desc(vb + st * C::OP) + (((k >> 2) * (HD * 128) + (k & 3) * 32) >> 4), ID_O,
-                                  more || part + k > 0, one);
-            };
             bool ok = wait(B.kfull + 0, 0);
             if (ok) {
                 pp_fence_after();
                 for (int x = 0; x < nx; ++x) {
-                    score(x, 0);
+                    pp_score<HD>(PP_TMEM + x * 128, qb + x * C::OP, kb, false, one);
                     pp_commit(B.s + x, one);
                 }
                 pp_commit(B.kempty + 0, one);
             }
-            for (int j = 0; ok && j < nblk; ++j) {
-                const int st = C::NST == 2 ? j & 1 : 0, ph = C::NST == 2 ? (j >> 1) & 1 : j & 1;
-                const int j1 = j + 1, st1 = C::NST == 2 ? j1 & 1 : 0, ph1 = C::NST == 2 ? (j1 >> 1) & 1 : j1 & 1;
-                ok = wait(B.vfull + st, ph);
+            for (int j = 0; ok && j < I.nblk; ++j) {
+                const int st = j & 1, j1 = j + 1, st1 = j1 & 1;
+                ok = wait(B.vfull + st, (j >> 1) & 1);
                 for (int x = 0; ok && x < nx; ++x) {
                     ok = wait(B.p + x, j & 1);
                     if (!ok) break;
                     pp_fence_after();
-                    value(x, st, j > 0);
+                    pp_value<HD>(PP_TMEM + 256 + x * HD, PP_TMEM + x * 128, vb + st * C::OP, j > 0, one);
                     if (x == nx - 1) pp_commit(B.vempty + st, one);
-                    if (j1 == nblk) {
+                    if (j1 == I.nblk) {
                         pp_commit(B.o + x, one);
                     } else {
-                        if (x == 0) ok = wait(B.kfull + st1, ph1);
+                        if (x == 0) ok = wait(B.kfull + st1, (j1 >> 1) & 1);
                         if (!ok) break;
                         pp_fence_after();
-                        score(x, st1);
+                        pp_score<HD>(PP_TMEM + x * 128, qb + x * C::OP, kb + st1 * C::OP, false, one);
                         pp_commit(B.s + x, one);
                         if (x == nx - 1) pp_commit(B.kempty + st1, one);
                     }
@@ -647,56 +744,182 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 pp_commit(B.o, one);
                 for (int k = 0; k < 2; ++k) mbar_wait(B.o, k);
             }
-        } else if (warp == 13 && nblk > 0) {
-            // ---- copies: lane i < 4 requests tile i of each half block; the pages are looked up one half block ahead
-            const int nhalf = 2 * nblk;
-            auto page_of = [&](int i) {  // the table's entry for tile `lane` of half block i; -1: nothing to read there
-                const int row = base + 64 * i + 16 * lane;
-                return lane < 4 && i < nhalf && row <= any_hi ? a.tables_dev[(size_t)b * a.table_stride + row / R] : -1;
-            };
-            int page = page_of(0), slot = 0, par = 1;
-            bool ok = true;
-            int i = 0;
-            for (; i < nhalf; ++i) {
-                if (i >= PP_RAW) ok = wait(B.rawfree + slot, par);
-                if (!ok) break;
-                const int row = base + 64 * i + 16 * lane;
-                const bool there = lane < 4 && row <= any_hi;
-                if (there && (page < 0 || page >= P.p.n_pages)) {
-                    atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
-                    page = 0;
-                }
-                const int n = __popc(__ballot_sync(0xffffffffu, there));
-                if (lane == 0) mbar_arrive_expect_tx(B.raw + slot, n * C::TILE);
-                __syncwarp();
-                if (there)
-                    bulk_g2s(smem + C::OFF_RAW + (slot * 4 + lane) * C::TILE,
-                             P.p.pool + (((size_t)page * KV + h) * (R >> 4) + ((row % R) >> 4)) * C::TILE, C::TILE,
-                             B.raw + slot);
-                page = page_of(i + 1);
-                if (++slot == PP_RAW) {
-                    slot = 0;
-                    par ^= 1;
-                }
-            }
-            // given up: copies may still be landing
-            if (!ok)
-                for (int k = max(0, i - PP_RAW); k < i; ++k) mbar_wait(B.raw + k % PP_RAW, (k / PP_RAW) & 1);
+        } else if (warp == 13) {
+            pp_copies<HD>(P, B, smem, I, lane);
         }
     }
-    __syncwarp();
+    pp_close(B, warp);
+}
+
+// ---------------------------------------------------------------------------
+template <int HD>
+__global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpArgs P) {
+    using C = PpCfg<HD>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // swizzle atoms: 1024-aligned
+    PpBars &B = *reinterpret_cast<PpBars *>(smem + C::OFF_BARS);
+    const er_pages_attention_args &a = P.a;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // so that the compiler knows it is the same in the whole warp
+    const int G = a.n_heads / P.p.KV;
+    PpItem I;
+    if (!pp_find<128>(P, B, warp, lane, I)) return;
+    pp_setup(B, tid, warp);
+    // warps 0-3 and 4-7: thread = query row
+    const int r = tid & 127, f = I.f0 + r, tok = f / G;
+    const int row = I.q0 + tok, head = I.h * G + (f - tok * G);
+    const bool real = r < I.nf;
+    float *factor = reinterpret_cast<float *>(smem + C::OFF_ROWS);  // [2][128]; [2][128] m, l at the end
+    float down = 0.f;
+    if (warp < 4) {
+        down = pp_query<float, HD, true>(a, smem + C::OFF_Q,
+                                         (const float *)a.q_dev + row * a.q_stride + (size_t)head * HD, real, r);
+        fence_proxy_async_smem();
+    }
     pp_fence_before();
     __syncthreads();
-    if (warp == 12) {
-        pp_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    pp_fence_after();
+    auto wait = [&](uint64_t *bar, uint32_t par) { return pp_wait(P, bar, par, lane); };
+    const uint32_t tl = PP_TMEM + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int pos = real ? I.past + tok : -1;
+        const int first = a.window ? max(0, pos - a.window + 1) : 0;
+        float m = PP_NONE, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < I.nblk; ++j) {
+            const int buf = j & 1, ph = (j >> 1) & 1;
+            ok = wait(B.s + buf, ph);
+            if (!ok) break;
+            pp_fence_after();
+            const uint32_t tS = tl + buf * 128;
+            float s[128];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pp_ld32(tS + 32 * k, s + 32 * k);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pp_wait_ld(s + 32 * k);
+            const int r0 = I.base + PP_BLOCK * j;
+            if (__any_sync(0xffffffffu, r0 < first || r0 + PP_BLOCK - 1 > pos)) pp_mask(s, first - r0, pos - r0);
+            const float mt = pp_largest(s) * down;
+            const float mn = mt > m + PP_SLACK ? mt : m;
+            const float corr = mn == m ? 1.f : pp_ex2(m - mn);
+            l *= corr;
+            m = mn;
+            if (j >= 2) ok = wait(B.cempty + buf, ph ^ 1);
+            if (!ok) break;
+            factor[buf * 128 + r] = corr;
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.c + buf);
+            l += pp_probabilities<true>(s, tS, down, m);
+            pp_wait_st();
+            pp_fence_before();
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.p + buf);
+        }
+        // m and l follow as if they were one more block's factor
+        if (ok && I.nblk >= 2) ok = wait(B.cempty + (I.nblk & 1), ((I.nblk >> 1) & 1) ^ 1);
+        if (ok) {
+            factor[256 + r] = m;
+            factor[384 + r] = l;
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.c + (I.nblk & 1));
+        }
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        float o[HD];
+#pragma unroll
+        for (int e = 0; e < HD; ++e) o[e] = 0.f;
+        bool ok = true;
+        for (int j = 0; j < I.nblk; ++j) {
+            const int buf = j & 1, ph = (j >> 1) & 1;
+            ok = wait(B.c + buf, ph);
+            if (!ok) break;
+            const float corr = factor[buf * 128 + r];
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.cempty + buf);
+            ok = wait(B.o + buf, ph);
+            if (!ok) break;
+            pp_fence_after();
+#pragma unroll
+            for (int k = 0; k < HD / 32; ++k) {
+                float d[32];
+                pp_ld32(tl + 256 + buf * HD + 32 * k, d);
+                pp_wait_ld(d);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[32 * k + e] = fmaf(o[32 * k + e], corr, d[e]);
+            }
+            pp_fence_before();
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.oempty + buf);
+        }
+        if (ok) ok = wait(B.c + (I.nblk & 1), (I.nblk >> 1) & 1);
+        if (ok && real) {
+            const float m = factor[256 + r], l = factor[384 + r], inv = 1.f / l;
+            float *out = (float *)a.out_dev + row * a.out_stride + (size_t)head * HD;
+#pragma unroll
+            for (int k = 0; k < HD / 32; ++k) pp_store<float>(a, out + 32 * k, o + 32 * k, l, inv);
+            if (a.lse_dev) a.lse_dev[(size_t)row * a.n_heads + head] = pp_lse(m, l);
+        }
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        pp_operands<HD>(P, B, smem, I, warp, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        if (warp == 12 && I.nblk > 0) {
+            const uint32_t qb = smem_u32(smem + C::OFF_Q), kb = smem_u32(smem + C::OFF_K), vb = smem_u32(smem + C::OFF_V);
+            const uint32_t one = pp_elect();
+            auto score = [&](int j) {  // S of block j, hi then lo halves of the queries
+                const int st = j & 1;
+                pp_score<HD>(PP_TMEM + st * 128, qb, kb + st * C::OP, false, one);
+                pp_score<HD>(PP_TMEM + st * 128, qb + C::OP, kb + st * C::OP, true, one);
+                pp_commit(B.s + st, one);
+                pp_commit(B.kempty + st, one);
+            };
+            bool ok = true;
+            for (int j = 0; ok && j < min(2, I.nblk); ++j) {
+                ok = wait(B.kfull + j, 0);
+                if (!ok) break;
+                pp_fence_after();
+                score(j);
+            }
+            for (int j = 0; ok && j < I.nblk; ++j) {
+                const int st = j & 1, ph = (j >> 1) & 1;
+                ok = wait(B.vfull + st, ph);
+                if (ok && j >= 2) ok = wait(B.oempty + st, ph ^ 1);
+                if (ok) ok = wait(B.p + st, ph);
+                if (!ok) break;
+                pp_fence_after();
+                pp_value<HD>(PP_TMEM + 256 + st * HD, PP_TMEM + st * 128, vb + st * C::OP, false, one);
+                pp_value<HD>(PP_TMEM + 256 + st * HD, PP_TMEM + st * 128 + 64, vb + st * C::OP, true, one);
+                pp_commit(B.o + st, one);
+                pp_commit(B.vempty + st, one);
+                if (j + 2 < I.nblk) {
+                    ok = wait(B.kfull + st, ph ^ 1);
+                    if (!ok) break;
+                    pp_fence_after();
+                    score(j + 2);
+                }
+            }
+            if (!ok) {  // given up: products in flight read shared memory and TMEM until they end
+                pp_commit(B.vempty, one);
+                for (int k = 0; k < 2; ++k) mbar_wait(B.vempty, k);
+            }
+        } else if (warp == 13) {
+            pp_copies<HD>(P, B, smem, I, lane);
+        }
     }
+    pp_close(B, warp);
 }
 
 template <class T, int HD>
+static auto prompt_kernel() {
+    if constexpr (sizeof(T) == 4) return pages_prompt32_kernel<HD>;
+    else return pages_prompt_kernel<T, HD>;
+}
+template <class T, int HD>
 static cudaError_t prompt_prepare() {
-    return cudaFuncSetAttribute(pages_prompt_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                PpCfg<HD, sizeof(T) == 4>::SMEM);
+    return cudaFuncSetAttribute(prompt_kernel<T, HD>(), cudaFuncAttributeMaxDynamicSharedMemorySize, PpCfg<HD>::SMEM);
 }
 cudaError_t pages_prompt_prepare() {
     cudaError_t e[6] = {prompt_prepare<float, 64>(), prompt_prepare<float, 128>(), prompt_prepare<__half, 64>(),
@@ -709,16 +932,15 @@ cudaError_t pages_prompt_prepare() {
 
 template <class T>
 static cudaError_t prompt_t(const PpArgs &P, unsigned grid, cudaStream_t st) {
-    constexpr bool S = sizeof(T) == 4;
-    if (P.p.hd == 128) pages_prompt_kernel<T, 128><<<grid, PP_THREADS, PpCfg<128, S>::SMEM, st>>>(P);
-    else pages_prompt_kernel<T, 64><<<grid, PP_THREADS, PpCfg<64, S>::SMEM, st>>>(P);
+    if (P.p.hd == 128) prompt_kernel<T, 128>()<<<grid, PP_THREADS, PpCfg<128>::SMEM, st>>>(P);
+    else prompt_kernel<T, 64>()<<<grid, PP_THREADS, PpCfg<64>::SMEM, st>>>(P);
     return cudaGetLastError();
 }
 
 cudaError_t launch_pages_prompt(const PagesView &p, const er_pages_attention_args &a, int min_rows, cudaStream_t st) {
     const PpArgs P = {p, a, min_rows};
-    const long long G = a.n_heads / p.KV;
-    const long long items = ((long long)a.n_tokens * G + 255) / 256 + (a.n_seqs < a.n_tokens ? a.n_seqs : a.n_tokens);
+    const long long G = a.n_heads / p.KV, rows = a.type == ER_F32 ? 128 : 256;  // query rows of a CTA
+    const long long items = ((long long)a.n_tokens * G + rows - 1) / rows + (a.n_seqs < a.n_tokens ? a.n_seqs : a.n_tokens);
     if (items * p.KV > 2147483647ll) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(items * p.KV);
     return a.type == ER_F32   ? prompt_t<float>(P, grid, st)
