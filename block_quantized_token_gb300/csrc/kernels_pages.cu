@@ -379,8 +379,8 @@ ER_DEV void st_row(T *row, int c, bool vec, const float (&x)[8]) {
 // the pair's larger value, hence by E = 2 AP_ERR max |m| over the blocks that hold the lane's pairs (that block and,
 // for halves, its counterpart in the other half, which the same lanes hold).  Returns whether some code or scale is
 // not certain within E.
-// AP_ERR: the sum of HD squares takes at most 10 float32 steps (half of that in its root), the reciprocal root 3, two
-// products 2, the rotation 3: below 14 steps of 2^-24.
+// AP_ERR: the sum of HD squares takes at most 10 float32 steps (half of that in its root), the reciprocal root and its
+// argument 4, gain times cosine 1, the rotation 2, the last product 1: below 14 steps of 2^-24.
 constexpr float AP_ERR = 14.f * 5.9604645e-8f;
 
 template <bool HALVES, bool CHECK>
@@ -489,7 +489,6 @@ ER_DEV void append_qk(const AppendArgs &A) {
     const PagesView &p = A.p;
     const int lane = threadIdx.x & 31, c = lane % LG;
     const long long grp = ((long long)blockIdx.x * AP_WARPS + (threadIdx.x >> 5)) * GPW + lane / LG;
-    const int rows = a.n_heads + p.KV;
     const int t = (int)(grp / A.parts), part = (int)(grp - (long long)t * A.parts);
     const bool in = t < a.n_tokens;
     const int slot = in ? a.slots_dev[t] : -1;
@@ -498,108 +497,121 @@ ER_DEV void append_qk(const AppendArgs &A) {
     if (!__any_sync(0xffffffffu, there)) return;
     auto aligned = [](const void *x, int64_t stride) { return ((uintptr_t)x & 15) == 0 && (stride * sizeof(T)) % 16 == 0; };
     const bool vq = aligned(a.q_dev, a.q_stride), vk = aligned(a.k_dev, a.k_stride), vo = aligned(a.q_out_dev, a.q_out_stride);
-    // the lane's pairs i: values (2 i, 2 i + 1), or (i, i + 4) for halves; their (cos, sin) and the two gains
+    // The lane's pair i is values (2 i, 2 i + 1), or (i, i + 4) for halves.  Gain, cosine and sine go together once a token:
+    //   (a, b) -> rs (a ga c - b gb s, b gb c + a ga s)
     const bool turn = a.rope_dev != nullptr;
-    float2 cs[4];
-    float gain[2][8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        cs[i] = turn && there ? __ldg(reinterpret_cast<const float2 *>(a.rope_dev) + (size_t)pos * (HD / 2) + 4 * c + i)
-                              : make_float2(1.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float *gp = k ? a.k_gain_dev : a.q_gain_dev;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            gain[k][e] = gp ? __ldg(gp + (HALVES ? (e >> 2) * (HD / 2) + 4 * c + (e & 3) : 8 * c + e)) : 1.f;
-    }
-    auto source = [&](int r, bool &vec) {
-        const bool key = r >= a.n_heads;
-        vec = key ? vk : vq;
-        return key ? (const T *)a.k_dev + t * a.k_stride + (size_t)(r - a.n_heads) * HD
-                   : (const T *)a.q_dev + t * a.q_stride + (size_t)r * HD;
+    auto dim = [&](int e) { return HALVES ? (e >> 2) * (HD / 2) + 4 * c + (e & 3) : 8 * c + e; };
+    auto table = [&](int i) {
+        return turn && there ? __ldg(reinterpret_cast<const float2 *>(a.rope_dev) + (size_t)pos * (HD / 2) + 4 * c + i)
+                             : make_float2(1.f, 0.f);
     };
-    float nx[8];
+    float co[8], si[8];  // ga c, gb c of each pair; ga s, gb s
+    auto factors = [&](const float *gain) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) nx[e] = 0.f;
-    if (there && part < rows) {
-        bool vec;
-        const T *src = source(part, vec);
-        ld_row<T, HD, HALVES>(src, c, vec, nx);
-    }
-    // whole warps go round together (its groups' tokens and parts may differ by one row)
-    for (int r0 = 0; r0 < rows; r0 += A.parts) {
-        const int r = r0 + part;
-        const bool live = there && r < rows;
-        float x[8], y[8];
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = table(i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = nx[e];
-            y[e] = nx[e];
-        }
-        if (there && r + A.parts < rows) {
-            bool vec;
-            const T *src = source(r + A.parts, vec);
-            ld_row<T, HD, HALVES>(src, c, vec, nx);
-        }
-        const bool key = r >= a.n_heads;
-        const bool norm = key ? a.k_gain_dev != nullptr : a.q_gain_dev != nullptr;
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = 1; o < LG; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (norm) {
-            const float rs = rsqrtf(ss * (1.f / HD) + a.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e] * rs * (key ? gain[1][e] : gain[0][e]);
-        }
-        if (turn) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e0 = HALVES ? i : 2 * i, e1 = HALVES ? i + 4 : 2 * i + 1;
-                const float ya = y[e0], yb = y[e1];
-                y[e0] = ya * cs[i].x - yb * cs[i].y;
-                y[e1] = yb * cs[i].x + ya * cs[i].y;
+            for (int k = 0; k < 2; ++k) {
+                const int e = HALVES ? i + 4 * k : 2 * i + k;
+                const float g = gain ? __ldg(gain + dim(e)) : 1.f;
+                co[e] = g * t.x;
+                si[e] = g * t.y;
             }
         }
-        if (live && !key) st_row<T, HD, HALVES>((T *)a.q_out_dev + t * a.q_out_stride + (size_t)r * HD, c, vo, y);
-        if (!__any_sync(0xffffffffu, live && key)) continue;
+    };
+    auto row_of = [&](const float (&x)[8], bool norm, float (&y)[8]) {
+        float rs = 1.f;
+        if (norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = 1; o < LG; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            rs = rsqrtf(ss * (1.f / HD) + a.eps);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e0 = HALVES ? i : 2 * i, e1 = HALVES ? i + 4 : 2 * i + 1;
+            y[e0] = (x[e0] * co[e0] - x[e1] * si[e1]) * rs;
+            y[e1] = (x[e1] * co[e1] + x[e0] * si[e0]) * rs;
+        }
+    };
+    // Whole warps go round together (its groups' tokens and parts may differ); a row's values are on their way while the one
+    // before is worked.
+    auto rows_of = [&](const T *base, int64_t stride, bool vec, int n, auto work) {
+        const T *src = base + t * stride + (size_t)part * HD;
+        float nx[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) nx[e] = 0.f;
+        if (there && part < n) ld_row<T, HD, HALVES>(src, c, vec, nx);
+        for (int r = part; r - part < n; r += A.parts) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = nx[e];
+            src += (size_t)A.parts * HD;
+            if (there && r + A.parts < n) ld_row<T, HD, HALVES>(src, c, vec, nx);
+            work(r, there && r < n, x);
+        }
+    };
+    if (a.n_heads) {
+        factors(a.q_gain_dev);
+        T *dst = (T *)a.q_out_dev + t * a.q_out_stride;
+        rows_of((const T *)a.q_dev, a.q_stride, vq, a.n_heads, [&](int r, bool live, const float (&x)[8]) {
+            float y[8];
+            row_of(x, a.q_gain_dev != nullptr, y);
+            if (live) st_row<T, HD, HALVES>(dst + (size_t)r * HD, c, vo, y);
+        });
+    }
+    const bool norm = a.k_gain_dev != nullptr;
+    factors(a.k_gain_dev);
+    rows_of((const T *)a.k_dev, a.k_stride, vk, p.KV, [&](int r, bool live, const float (&x)[8]) {
         uint32_t codes;
         float d[2];
-        if (!a.k_gain_dev && !turn) {
-            ap_quant<HALVES, false>(y, codes, d, lane);  // keys as they are
-        } else if (__any_sync(0xffffffffu, ap_quant<HALVES, true>(y, codes, d, lane) && live && key)) {
-            // those rows again in float64: their codes are those of the formula whatever the float32 steps were
-            double z[8], zs = 0.0;
+        if (!norm && !turn) {
+            ap_quant<HALVES, false>(x, codes, d, lane);  // keys as they are
+        } else {
+            float y[8];
+            row_of(x, norm, y);
+            if (__any_sync(0xffffffffu, ap_quant<HALVES, true>(y, codes, d, lane) && live)) {
+                // those rows again in float64: their codes are those of the formula whatever the float32 steps were
+                double zs = 0.0, rs = 1.0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                z[e] = (double)x[e];
-                zs += z[e] * z[e];
-            }
+                for (int e = 0; e < 8; ++e) zs += (double)x[e] * (double)x[e];
 #pragma unroll
-            for (int o = 1; o < LG; o <<= 1) zs += __shfl_xor_sync(0xffffffffu, zs, o);
-            if (norm) {
-                const double rs = 1.0 / sqrt(zs / HD + (double)a.eps);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = z[e] * rs * (double)gain[1][e];
-            }
-            if (turn) {
-#pragma unroll
+                for (int o = 1; o < LG; o <<= 1) zs += __shfl_xor_sync(0xffffffffu, zs, o);
+                if (norm) rs = 1.0 / sqrt(zs / HD + (double)a.eps);
+#pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
-                    const int e0 = HALVES ? i : 2 * i, e1 = HALVES ? i + 4 : 2 * i + 1;
-                    const double za = z[e0], zb = z[e1], co = (double)cs[i].x, sn = (double)cs[i].y;
-                    z[e0] = za * co - zb * sn;
-                    z[e1] = zb * co + za * sn;
-                }
-            }
+                    const float2 cs = table(i);
+                    double z[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = (float)z[e];
-            ap_quant<HALVES, false>(y, codes, d, lane);
+                    for (int k = 0; k < 2; ++k) {
+                        float v = 0.f;
+                        int dm = 0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (q == i) {
+                                const int e = HALVES ? q + 4 * k : 2 * q + k;
+                                v = x[e];
+                                dm = dim(e);
+                            }
+                        z[k] = (double)v * rs * (norm ? (double)__ldg(a.k_gain_dev + dm) : 1.0);
+                    }
+                    const float ya = (float)(z[0] * (double)cs.x - z[1] * (double)cs.y);
+                    const float yb = (float)(z[1] * (double)cs.x + z[0] * (double)cs.y);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (q == i) {
+                            y[HALVES ? q : 2 * q] = ya;
+                            y[HALVES ? q + 4 : 2 * q + 1] = yb;
+                        }
+                }
+                ap_quant<HALVES, false>(y, codes, d, lane);
+            }
         }
         const uint32_t mate = __shfl_xor_sync(0xffffffffu, codes, 1);
-        if (!live || !key) continue;
-        uint8_t *tile = pg_tile(p.pool, p.page_rows, p.KV, HD, slot, r - a.n_heads);
+        if (!live) return;
+        uint8_t *tile = pg_tile(p.pool, p.page_rows, p.KV, HD, slot, r);
         const int in16 = (slot % p.page_rows) & 15;
         __half *ks = reinterpret_cast<__half *>(tile + pg_off_ks(HD)) + in16 * (HD / 32);
         if constexpr (HALVES) {
@@ -617,7 +629,7 @@ ER_DEV void append_qk(const AppendArgs &A) {
             *reinterpret_cast<uint32_t *>(tile + pg_k_word(in16, (c & 3) * (HD / 32) + (c >> 2), HD)) = ap_kword(codes);
             if ((c & 3) == 0) ks[c >> 2] = __float2half_rn(d[0]);
         }
-    }
+    });
 }
 
 template <class T, int HD>
@@ -715,7 +727,7 @@ __global__ void __launch_bounds__(AP_WARPS * 32, AP_BLOCKS) pages_append_kernel(
 template <class T>
 static cudaError_t append_t(const PagesView &p, const er_pages_append_args &a, int num_sms, cudaStream_t st) {
     AppendArgs A = {p, a, 1, 0, 16};
-    const int rows = a.n_heads + p.KV;
+    const int rows = a.n_heads > p.KV ? a.n_heads : p.KV;
     // Groups (of HD / 8 lanes) enough for twice the GPU's threads, and no more than one a row: a step's few tokens are
     // spread row by row, a prompt's groups keep their token's table row and gains for several heads.
     const long long want = 2ll * num_sms * 2048 / (p.hd / 8);

@@ -36,10 +36,7 @@
 
 namespace er {
 
-// 8 warps of up to 255 registers: 12 of 168 spill (fp32: 93 us against 72 for 16 x 8192, bf16 55 against 54)
-constexpr int PD_WARPS = 8;
-constexpr int PD_THREADS = PD_WARPS * 32;
-constexpr int PD_SLOTS = 4;    // steps in a warp's ring
+constexpr int PD_MAX_WARPS = 12;
 constexpr int PD_STEP = 32;      // rows of a step: two tiles
 constexpr int PD_ROWS = 8;       // query rows of a unit
 constexpr int PD_SEQS = 512;     // sequences of a launch (more: several launches)
@@ -48,20 +45,41 @@ constexpr float PD_UP = 7.f;     // p = 2^(s - m + PD_UP)
 constexpr float PD_SLACK = 8.f;  // scores may pass m by this much
 constexpr float PD_NONE = -3e38f;  // m before any score
 
+template <class T>
+struct PdType;  // RAW: K enters as codes (bf16); QLO: queries have a lo half; PLO: probabilities have one
+template <>
+struct PdType<float> {
+    static constexpr bool RAW = false, QLO = true, PLO = true;
+};
+template <>
+struct PdType<__half> {
+    static constexpr bool RAW = false, QLO = false, PLO = true;
+};
+template <>
+struct PdType<__nv_bfloat16> {
+    static constexpr bool RAW = true, QLO = false, PLO = false;
+};
+
 struct PdSeq {  // a sequence: its rows of q, its length, its steps (-1: rows with nothing to attend)
     int q0, qn, len, ns;
 };
-template <int HD>
+// 12 warps hide more latency than 8 where 168 registers a thread hold a warp's state, which they do for HD = 64 and for
+// bf16 queries (ragged 61 x 0..4001, bf16: 45 us against 50; 1 x 2048, 64 dims, fp32: 12.7 against 14.7); fp32 and fp16
+// queries at 128 dims spill then (16 x 8192 fp32: 69 us against 62).
+template <class T, int HD>
 struct PdCfg {
+    static constexpr int WARPS = HD == 64 || sizeof(T) == 2 && PdType<T>::RAW ? PD_MAX_WARPS : 8;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int SLOTS = WARPS == 8 ? 4 : 3;  // steps in a warp's ring
     static constexpr int TILE = pg_tile_bytes(HD);
     static constexpr int NB = HD / 32;               // 32-dim blocks
     static constexpr int STATE = PD_ROWS * HD + 16;  // floats of a state: o [8][HD], m [8], l [8]
-    static constexpr int RING = PD_SLOTS * 2 * TILE; // a warp's; later its last segment's state
-    static constexpr int OFF_FIRST = PD_WARPS * RING;
-    static constexpr int OFF_W = OFF_FIRST + PD_WARPS * STATE * 4;
+    static constexpr int RING = SLOTS * 2 * TILE; // a warp's; later its last segment's state
+    static constexpr int OFF_FIRST = WARPS * RING;
+    static constexpr int OFF_W = OFF_FIRST + WARPS * STATE * 4;
     static constexpr int OFF_SEQ = OFF_W + (PD_SEQS + 2) * 8;
     static constexpr int OFF_BARS = OFF_SEQ + PD_SEQS * (int)sizeof(PdSeq);
-    static constexpr int OFF_MISC = OFF_BARS + PD_WARPS * PD_SLOTS * 8;
+    static constexpr int OFF_MISC = OFF_BARS + WARPS * SLOTS * 8;
     static constexpr int SMEM = OFF_MISC + 2048;
     static_assert(RING >= STATE * 4 && OFF_W % 8 == 0 && OFF_BARS % 8 == 0 && SMEM <= 232448, "shared memory layout");
 };
@@ -73,10 +91,10 @@ struct PdSeg {
     int off;  // byte offset of the state in shared memory, -1: none
 };
 struct PdMisc {
-    PdSeg seg[2 * PD_WARPS];
-    long long wsum[PD_WARPS];
-    int run[2 * PD_WARPS + 1];  // first of each run in ent
-    short ent[2 * PD_WARPS];    // the states that there are, in list order
+    PdSeg seg[2 * PD_MAX_WARPS];
+    long long wsum[PD_MAX_WARPS];
+    int run[2 * PD_MAX_WARPS + 1];  // first of each run in ent
+    short ent[2 * PD_MAX_WARPS];    // the states that there are, in list order
     int n_runs;
     int wait_bad;
     int last[2];
@@ -125,21 +143,6 @@ ER_DEV uint32_t pd_trans(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-template <class T>
-struct PdType;  // RAW: K enters as codes (bf16); QLO: queries have a lo half; PLO: probabilities have one
-template <>
-struct PdType<float> {
-    static constexpr bool RAW = false, QLO = true, PLO = true;
-};
-template <>
-struct PdType<__half> {
-    static constexpr bool RAW = false, QLO = false, PLO = true;
-};
-template <>
-struct PdType<__nv_bfloat16> {
-    static constexpr bool RAW = true, QLO = false, PLO = false;
-};
-
 struct PdArgs {
     PagesView p;
     er_pages_attention_args a;
@@ -167,8 +170,9 @@ ER_DEV void pd_row(int r, int rg, int G, int q0, int h, int &row, int &head, int
 }
 
 template <class T, int HD>
-__global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArgs P) {
-    using C = PdCfg<HD>;
+__global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kernel(const PdArgs P) {
+    using C = PdCfg<T, HD>;
+    constexpr int PD_WARPS = C::WARPS, PD_THREADS = C::THREADS, PD_SLOTS = C::SLOTS;
     using Y = PdType<T>;
     extern __shared__ __align__(128) uint8_t smem[];
     long long *W = reinterpret_cast<long long *>(smem + C::OFF_W);
@@ -636,13 +640,8 @@ __global__ void __launch_bounds__(PD_THREADS, 1) pages_decode_kernel(const PdArg
                 reference(x);
                 probabilities(x);
                 if (more && plain(r0) && plain(r0 + PD_STEP)) {
-                    float y[2][4];
-                    scores(std::false_type{}, sl, r0 + PD_STEP, y);
                     values(std::false_type{}, here, r0);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[n][e] = y[n][e];
+                    scores(std::false_type{}, sl, r0 + PD_STEP, x);
                 } else {
                     values(std::true_type{}, here, r0);
                     if (more) scores(std::true_type{}, sl, r0 + PD_STEP, x);
@@ -860,7 +859,7 @@ size_t pages_attn_part_floats(int num_sms) { return (size_t)num_sms * 2 * (PD_RO
 
 template <class T, int HD>
 static cudaError_t decode_prepare() {
-    return cudaFuncSetAttribute(pages_decode_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, PdCfg<HD>::SMEM);
+    return cudaFuncSetAttribute(pages_decode_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, PdCfg<T, HD>::SMEM);
 }
 cudaError_t pages_attn_prepare() {
     if (cudaError_t e = pages_prompt_prepare(); e != cudaSuccess) return e;
@@ -874,8 +873,8 @@ cudaError_t pages_attn_prepare() {
 
 template <class T>
 static cudaError_t decode_t(const PdArgs &P, int num_sms, cudaStream_t st) {
-    if (P.p.hd == 128) pages_decode_kernel<T, 128><<<num_sms, PD_THREADS, PdCfg<128>::SMEM, st>>>(P);
-    else pages_decode_kernel<T, 64><<<num_sms, PD_THREADS, PdCfg<64>::SMEM, st>>>(P);
+    if (P.p.hd == 128) pages_decode_kernel<T, 128><<<num_sms, PdCfg<T, 128>::THREADS, PdCfg<T, 128>::SMEM, st>>>(P);
+    else pages_decode_kernel<T, 64><<<num_sms, PdCfg<T, 64>::THREADS, PdCfg<T, 64>::SMEM, st>>>(P);
     return cudaGetLastError();
 }
 

@@ -12,9 +12,10 @@
 //     TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x HD).
 //   fp32 rows (pages_prompt32_kernel): one tile; queries and probabilities enter as hi + lo fp16 halves (2^-22), two
 //   products each.  The tensor cores' sums truncate (over thousands of rows 2^-18 of the output and growing), so a block's
-//   O starts from 0 and warps 4-7 add it to sums in registers, rounded to nearest.
-//     warps 0-3       softmax, as above; leaves each block's rescale factor in shared memory
-//     warps 4-7       o = o * factor + the block's O; writes the output
+//   O starts from 0 and is added to sums in registers, rounded to nearest.
+//     warps 0-3, 4-7  two threads a row, one for either half of the columns of S and of O: softmax, as above, with the
+//                     row's largest score exchanged through shared memory; then o = o * factor + the last block's O.
+//                     (One thread a row is bound by its own latency: 212 us against 167 for 4 x 500 tokens.)
 //     warp 12         S of the block after next goes to the buffer whose P is used up, so the softmax never waits for it
 //     TMEM: two buffers of S/P, two of a block's O.
 //   Both: warps 8-11 turn codes into fp16 operands in shared memory, exactly (pages.cuh), K and V K-major with the
@@ -30,6 +31,8 @@
 //
 // Masks.  Blocks that some row attends only in part mask S; there, rows of V that no row of the CTA attends are
 // zeroed (they may hold anything), and a NaN value of V is carried by K instead, so only rows that attend it see it.
+#include <type_traits>
+
 #include "pages.cuh"
 #include "pages.h"
 
@@ -52,7 +55,7 @@ struct PpCfg {
     static constexpr int OFF_V = OFF_K + 2 * OP;
     static constexpr int OFF_RAW = OFF_V + 2 * OP;
     static constexpr int OFF_BARS = OFF_RAW + PP_RAW * 4 * TILE;
-    static constexpr int OFF_ROWS = OFF_BARS + 512;       // fp32: factors of two blocks, then m and l [2][128]
+    static constexpr int OFF_ROWS = OFF_BARS + 512;      // fp32: [2 blocks][2 halves][128] values of the rows
     static constexpr int SMEM = OFF_ROWS + 2048 + 1024;  // + alignment of the base
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -64,7 +67,7 @@ struct PpArgs {
 };
 
 struct PpBars {
-    uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], oempty[2], c[2], cempty[2];
+    uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], oempty[2], x[2];
     uint32_t tmem;
     int item[4];  // sequence, first query row, KV head, found
 };
@@ -203,7 +206,8 @@ __host__ __device__ constexpr int pp_place(int r) {
 struct PpItem {
     int b, h, f0, nf, q0, past, any_lo, any_hi, all_lo, all_hi, base, nblk;
 };
-// The item of this CTA: (sequence, ROWS query rows, KV head), heads fastest, a sequence's last rows first.  False: none.
+// The item of this CTA: (sequence, ROWS query rows, KV head), heads fastest, long sequences first and a sequence's
+// last rows first.  False: none.
 template <int ROWS>
 ER_DEV bool pp_find(const PpArgs &P, PpBars &B, int warp, int lane, PpItem &I) {
     const er_pages_attention_args &a = P.a;
@@ -213,22 +217,23 @@ ER_DEV bool pp_find(const PpArgs &P, PpBars &B, int warp, int lane, PpItem &I) {
         int found = 0, base = 0;
         for (int b0 = 0; b0 < a.n_seqs && !found; b0 += 32) {
             const int b = b0 + lane;
-            int n = 0;
+            int n = 0, len = -1;
             if (b < a.n_seqs) {
-                const int q0 = a.q_start_dev[b], q1 = a.q_start_dev[b + 1], len = a.lens_dev[b];
+                const int q0 = a.q_start_dev[b], q1 = a.q_start_dev[b + 1];
+                len = a.lens_dev[b];
                 if (q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 || (long long)len > (long long)a.table_stride * R) {
                     if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
                 } else if ((long long)(q1 - q0) * G >= P.min_rows) {
                     n = (int)(((long long)(q1 - q0) * G + ROWS - 1) / ROWS);
                 }
             }
-            int inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
+            // the items before this sequence's: of 32 sequences the longest come first, so that the last items are short
+            int first = base, all = 0;
+            for (int o = 0; o < 32; ++o) {
+                const int len_o = __shfl_sync(0xffffffffu, len, o), n_o = __shfl_sync(0xffffffffu, n, o);
+                if (len_o > len || (len_o == len && o < lane)) first += n_o;
+                all += n_o;
             }
-            const int first = base + inc - n;
             const bool mine = x >= first && x < first + n;
             if (mine) {
                 B.item[0] = b;
@@ -236,7 +241,7 @@ ER_DEV bool pp_find(const PpArgs &P, PpBars &B, int warp, int lane, PpItem &I) {
                 B.item[2] = blockIdx.x % KV;
             }
             found = __any_sync(0xffffffffu, mine);
-            base += __shfl_sync(0xffffffffu, inc, 31);
+            base += all;
         }
         if (lane == 0) B.item[3] = found;
     }
@@ -335,35 +340,29 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
     auto wait = [&](uint64_t *bar, uint32_t par) { return pp_wait(P, bar, par, lane); };
     const int pw = warp - 8, g = lane >> 2, t = lane & 3, half = pw >> 1;
     const uint8_t *ring = smem + C::OFF_RAW;
-    bool ok = true;
-    int slot = half, par = 0;  // of half block 2 j + half
-    for (int j = 0; j < nblk; ++j) {
-        const int st = j & 1, ph = (j >> 1) & 1;
-        ok = wait(B.raw + slot, par);
-        if (!ok) break;
-        const uint8_t *raw = ring + slot * (4 * C::TILE);
-        const int r0 = base + PP_BLOCK * j;
-        const bool edge = r0 < all_lo || r0 + PP_BLOCK - 1 > all_hi;
-        // ---- K: a job is 8 rows, a lane one row's words of quad lane t
-        if (j >= 2) ok = wait(B.kempty + st, ph ^ 1);
-        if (!ok) break;
-        uint8_t *kd = smem + C::OFF_K + st * C::OP;
-#pragma unroll 2
+    // K: a job is 8 rows, a lane one row's words of quad lane t.  An odd row writes its blocks in the other order: 8 lanes
+    // then cover all the bank groups.  Row 32 pw + 8 job + g goes to place 32 pw + 8 (g / 2) + 4 (job / 2) + 2 (job % 2) + g % 2.
+    const int odd = g & 1;
+    const uint32_t kat = (uint32_t)((32 * pw + 8 * (g >> 1) + odd) * 128), kch = (uint32_t)(((4 * odd + t) ^ odd) << 4);
+    const uint32_t sel0 = odd ? 0x3232u : 0x1010u, sel1 = odd ? 0x1010u : 0x3232u;
+    auto keys = [&](auto edge_tag, const uint8_t *raw, uint8_t *kd) {
+        constexpr bool EDGE = decltype(edge_tag)::value;
+#pragma unroll 1
         for (int job = 0; job < 4; ++job) {
-            const int rr = 8 * (4 * pw + job) + g, in = rr & 15;
-            const uint8_t *src = raw + ((rr >> 4) & 3) * C::TILE;
+            const int in = 8 * (job & 1) + g;
+            const uint8_t *src = raw + (2 * pw + (job >> 1) & 3) * C::TILE;
             uint32_t w[C::NB], ds[C::NB / 2];
             if constexpr (HD == 128) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(src + in * 64 + t * 16);
-                w[0] = x.x; w[1] = x.y; w[2] = x.z; w[C::NB - 1] = x.w;
+                w[0] = odd ? x.y : x.x; w[1] = odd ? x.x : x.y; w[2] = odd ? x.w : x.z; w[C::NB - 1] = odd ? x.z : x.w;
                 const uint2 y = *reinterpret_cast<const uint2 *>(src + pg_off_ks(HD) + in * 8);
                 ds[0] = y.x; ds[C::NB / 2 - 1] = y.y;
             } else {
                 const uint2 x = *reinterpret_cast<const uint2 *>(src + in * 32 + t * 8);
-                w[0] = x.x; w[1] = x.y;
+                w[0] = odd ? x.y : x.x; w[1] = odd ? x.x : x.y;
                 ds[0] = *reinterpret_cast<const uint32_t *>(src + pg_off_ks(HD) + in * 4);
             }
-            if (edge) {  // a row with a NaN value: its K carries it
+            if constexpr (EDGE) {  // a row with a NaN value: its K carries it
                 const unsigned short *vs = reinterpret_cast<const unsigned short *>(src + pg_off_vs(HD));
                 bool nan = false;
 #pragma unroll
@@ -372,32 +371,27 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
 #pragma unroll
                     for (int k = 0; k < C::NB / 2; ++k) ds[k] = 0x7FFF7FFFu;
             }
-            const int n = pp_place(rr);
-            uint8_t *dst = kd + n * 128;
-            // an odd row writes its blocks in the other order: 8 lanes then cover all the bank groups
+            const int at = 2 * (job & 1) + 4 * (job >> 1);
+            uint8_t *dst = kd + kat + at * 128;
+            const uint32_t ch = kch ^ (uint32_t)(at << 4);
 #pragma unroll
             for (int k = 0; k < C::NB; ++k) {
-                const uint32_t ww = (g & 1) ? w[k ^ 1] : w[k];
-                const int bb = (g & 1) ? k ^ 1 : k;
-                const uint32_t dd = ds[k >> 1], d = prmt(dd, dd, (bb & 1) ? 0x3232u : 0x1010u), z = pp_m24(d);
-                *reinterpret_cast<uint4 *>(dst + (k >> 1) * 16384 + (((4 * (bb & 1) + t) ^ (n & 7)) << 4)) =
-                    make_uint4(pp_val<0>(ww, d, z), pp_val<1>(ww, d, z), pp_val<2>(ww, d, z), pp_val<3>(ww, d, z));
+                const uint32_t d = prmt(ds[k >> 1], 0u, (k & 1) ? sel1 : sel0), z = pp_m24(d);
+                *reinterpret_cast<uint4 *>(dst + (k >> 1) * 16384 + (ch ^ ((k & 1) * 64u))) =
+                    make_uint4(pp_val<0>(w[k], d, z), pp_val<1>(w[k], d, z), pp_val<2>(w[k], d, z), pp_val<3>(w[k], d, z));
             }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) pp_arrive(B.kfull + st);
-        // ---- V: a lane holds 4 rows of one dim of two tiles: 16 bytes of the operand
-        if (j >= 2) ok = wait(B.vempty + st, ph ^ 1);
-        if (!ok) break;
-        uint8_t *vd = smem + C::OFF_V + st * C::OP;
-        const int q = HD == 128 ? pw & 1 : 0;
+    };
+    // V: a lane holds 4 rows of one dim of two tiles: 16 bytes of the operand.  Odd g takes the half block's two pairs of
+    // tiles in the other order (bank groups again).  HD = 64: a warp takes half the words of a lane.
+    constexpr int NU = HD == 128 ? 4 : 2;
+    const int q = HD == 128 ? pw & 1 : 0, u0 = HD == 128 ? 0 : 2 * (pw & 1);
+    auto vals = [&](auto edge_tag, const uint8_t *raw, uint8_t *vd, int r0) {
+        constexpr bool EDGE = decltype(edge_tag)::value;
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
-            const int pair = 2 * half + (k ^ (g & 1));  // odd g takes the pairs in the other order (bank groups again)
-            const uint8_t *sa = raw + (2 * pair & 3) * C::TILE, *sb = sa + C::TILE;
-            constexpr int NU = HD == 128 ? 4 : 2;  // words of a lane (HD = 64: a warp takes half of them)
-            const int u0 = HD == 128 ? 0 : 2 * (pw & 1);
+            const int pair = k ^ odd;  // of the half block
+            const uint8_t *sa = raw + 2 * pair * C::TILE, *sb = sa + C::TILE;
             uint32_t wa[NU], wb[NU], da[NU / 2][2], db[NU / 2][2];
             if constexpr (HD == 128) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(sa + pg_off_v(HD) + q * 512 + lane * 16);
@@ -418,7 +412,7 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
                 da[0][0] = v.x; da[0][1] = v.y;
                 db[0][0] = z.x; db[0][1] = z.y;
             }
-            if (edge) {  // scales of rows that nobody attends, or that are NaN: 0
+            if constexpr (EDGE) {  // scales of rows that nobody attends, or that are NaN: 0
 #pragma unroll
                 for (int x = 0; x < NU / 2; ++x)
 #pragma unroll
@@ -426,12 +420,12 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const uint32_t part = e ? 0xFFFF0000u : 0x0000FFFFu, inf = 0x7C007C00u & part;
-                            const int ra = r0 + 32 * pair + 2 * t + e + 8 * i, rb = ra + 16;
+                            const int ra = r0 + 64 * half + 32 * pair + 2 * t + e + 8 * i, rb = ra + 16;
                             if ((da[x][i] & 0x7FFF7FFFu & part) > inf || ra < any_lo || ra > any_hi) da[x][i] &= ~part;
                             if ((db[x][i] & 0x7FFF7FFFu & part) > inf || rb < any_lo || rb > any_hi) db[x][i] &= ~part;
                         }
             }
-            uint8_t *dst = vd + half * (HD * 128) + ((((pair & 1) * 4 + t) ^ g) << 4);
+            uint8_t *dst = vd + half * (HD * 128) + (((pair * 4 + t) ^ g) << 4);
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 const uint32_t a0 = da[u >> 1][0], a1 = da[u >> 1][1], b0 = db[u >> 1][0], b1 = db[u >> 1][1];
@@ -445,6 +439,28 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
                                pp_val<3>(wb[u], b1, zb1));
             }
         }
+    };
+    bool ok = true;
+    int slot = half, par = 0;  // of half block 2 j + half
+    for (int j = 0; j < nblk; ++j) {
+        const int st = j & 1, ph = (j >> 1) & 1;
+        ok = wait(B.raw + slot, par);
+        if (!ok) break;
+        const uint8_t *raw = ring + slot * (4 * C::TILE);
+        const int r0 = base + PP_BLOCK * j;
+        const bool edge = r0 < all_lo || r0 + PP_BLOCK - 1 > all_hi;
+        if (j >= 2) ok = wait(B.kempty + st, ph ^ 1);
+        if (!ok) break;
+        uint8_t *kd = smem + C::OFF_K + st * C::OP, *vd = smem + C::OFF_V + st * C::OP;
+        if (edge) keys(std::true_type{}, raw, kd);
+        else keys(std::false_type{}, raw, kd);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) pp_arrive(B.kfull + st);
+        if (j >= 2) ok = wait(B.vempty + st, ph ^ 1);
+        if (!ok) break;
+        if (edge) vals(std::true_type{}, raw, vd, r0);
+        else vals(std::false_type{}, raw, vd, r0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) pp_arrive(B.vfull + st);
@@ -500,7 +516,7 @@ ER_DEV void pp_copies(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem &I
 }
 
 // barriers (thread 0) and the whole of TMEM (warp 12)
-ER_DEV void pp_setup(PpBars &B, int tid, int warp) {
+ER_DEV void pp_setup(PpBars &B, int tid, int warp, int softmax_warps) {
     if (tid == 0) {
         for (int i = 0; i < PP_RAW; ++i) {
             mbar_init(B.raw + i, 1);
@@ -512,11 +528,10 @@ ER_DEV void pp_setup(PpBars &B, int tid, int warp) {
             mbar_init(B.vfull + i, 4);
             mbar_init(B.vempty + i, 1);
             mbar_init(B.s + i, 1);
-            mbar_init(B.p + i, 4);
+            mbar_init(B.p + i, softmax_warps);
             mbar_init(B.o + i, 1);
-            mbar_init(B.oempty + i, 4);
-            mbar_init(B.c + i, 4);
-            mbar_init(B.cempty + i, 4);
+            mbar_init(B.oempty + i, 8);
+            mbar_init(B.x + i, 8);
         }
         fence_mbar_init();
     }
@@ -555,26 +570,28 @@ ER_DEV void pp_value(uint32_t d, uint32_t p, uint32_t v, bool more, uint32_t one
 }
 
 // One block's scores of a row in registers: masked, their largest, and the probabilities written over them.
-ER_DEV void pp_mask(float (&s)[128], int lo, int hi) {
+template <int N>
+ER_DEV void pp_mask(float (&s)[N], int lo, int hi) {  // (places 64 on are 64 rows on: pp_row)
 #pragma unroll
-    for (int k = 0; k < 128; ++k)
+    for (int k = 0; k < N; ++k)
         if (pp_row(k) < lo || pp_row(k) > hi) s[k] = -INFINITY;
 }
-ER_DEV float pp_largest(const float (&s)[128]) {
+template <int N>
+ER_DEV float pp_largest(const float (&s)[N]) {
     float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-    for (int k = 4; k < 124; k += 8)
+    for (int k = 4; k < N - 4; k += 8)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = pp_max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
-    return pp_max3(pp_max3(mx[0], mx[1], fmaxf(s[124], s[125])), pp_max3(mx[2], mx[3], s[126]), s[127]);
+    return pp_max3(pp_max3(mx[0], mx[1], fmaxf(s[N - 4], s[N - 3])), pp_max3(mx[2], mx[3], s[N - 2]), s[N - 1]);
 }
-// p = 2^(s down - m + PP_UP) as fp16 over S's first 64 columns (LO: the lo halves over the others); returns their sum
-template <bool LO>
-ER_DEV float pp_probabilities(const float (&s)[128], uint32_t tS, float down, float m) {
+// p = 2^(s down - m + PP_UP) as fp16 to N / 2 columns at tP (LO: the lo halves 64 columns on); returns their sum
+template <bool LO, int N>
+ER_DEV float pp_probabilities(const float (&s)[N], uint32_t tP, float down, float m) {
     const float2 nb = make_float2(PP_UP - m, PP_UP - m), dn = make_float2(down, down);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {  // 32 columns of S become 16 of P: few registers beside S itself
+    for (int q = 0; q < N / 32; ++q) {  // 32 columns of S become 16 of P: few registers beside S itself
         uint32_t ph[16];
         [[maybe_unused]] uint32_t pl[16];
 #pragma unroll
@@ -585,12 +602,12 @@ ER_DEV float pp_probabilities(const float (&s)[128], uint32_t tS, float down, fl
             sum[k & 1] = pp_add2(sum[k & 1], x);
             ph[k] = pp_pack(x.x, x.y);
             if constexpr (LO) {
-                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&ph[k]));
-                pl[k] = pp_pack(x.x - z.x, x.y - z.y);
+                const float2 z = pp_fma2(__half22float2(*reinterpret_cast<const __half2 *>(&ph[k])), make_float2(-1.f, -1.f), x);
+                pl[k] = pp_pack(z.x, z.y);
             }
         }
-        pp_st16(tS + 16 * q, ph);
-        if constexpr (LO) pp_st16(tS + 64 + 16 * q, pl);
+        pp_st16(tP + 16 * q, ph);
+        if constexpr (LO) pp_st16(tP + 64 + 16 * q, pl);
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -625,7 +642,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
     PpItem I;
     if (!pp_find<256>(P, B, warp, lane, I)) return;
     const int nx = I.nf > 128 ? 2 : 1;  // tiles
-    pp_setup(B, tid, warp);
+    pp_setup(B, tid, warp, 4);
     // a softmax thread's tile and row
     const int X = warp >> 2, r = tid & 127, f = I.f0 + X * 128 + r, tok = f / G;
     const int row = I.q0 + tok, head = I.h * G + (f - tok * G);
@@ -646,8 +663,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
         if (soft) {
             const uint32_t tl = PP_TMEM + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
             const uint32_t tS = tl + X * 128, tO = tl + 256 + X * HD;
-            const int pos = real ? I.past + tok : -1;
-            const int first = a.window ? max(0, pos - a.window + 1) : 0;
+            const int pos = real ? I.past + tok : 2147483647;  // rows past the last are computed (from zeros) and dropped
+            const int first = a.window && real ? max(0, pos - a.window + 1) : 0;
             float m = PP_NONE, l = 0.f;
             bool ok = true;
             for (int j = 0; j < I.nblk; ++j) {
@@ -660,7 +677,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
 #pragma unroll
                 for (int k = 0; k < 4; ++k) pp_wait_ld(s + 32 * k);
                 const int r0 = I.base + PP_BLOCK * j;
-                if (__any_sync(0xffffffffu, r0 < first || r0 + PP_BLOCK - 1 > pos)) pp_mask(s, first - r0, pos - r0);
+                if (__any_sync(0xffffffffu, r0 < first || r0 + PP_BLOCK - 1 > pos)) pp_mask(s, first - r0, min(pos, r0 + PP_BLOCK) - r0);
                 const float mt = pp_largest(s) * down;
                 if (__any_sync(0xffffffffu, mt > m + PP_SLACK)) {
                     const float mn = mt > m + PP_SLACK ? mt : m;
@@ -764,102 +781,111 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
     const int G = a.n_heads / P.p.KV;
     PpItem I;
     if (!pp_find<128>(P, B, warp, lane, I)) return;
-    pp_setup(B, tid, warp);
-    // warps 0-3 and 4-7: thread = query row
-    const int r = tid & 127, f = I.f0 + r, tok = f / G;
+    pp_setup(B, tid, warp, 8);
+    // warps 0-3 and 4-7: thread = query row, W = which half of its columns
+    const int r = tid & 127, W = warp >> 2, f = I.f0 + r, tok = f / G;
     const int row = I.q0 + tok, head = I.h * G + (f - tok * G);
     const bool real = r < I.nf;
-    float *factor = reinterpret_cast<float *>(smem + C::OFF_ROWS);  // [2][128]; [2][128] m, l at the end
+    float *xch = reinterpret_cast<float *>(smem + C::OFF_ROWS);  // [2 blocks][2 halves][128]
     float down = 0.f;
     if (warp < 4) {
         down = pp_query<float, HD, true>(a, smem + C::OFF_Q,
                                          (const float *)a.q_dev + row * a.q_stride + (size_t)head * HD, real, r);
+        xch[r] = down;
         fence_proxy_async_smem();
     }
     pp_fence_before();
     __syncthreads();
     pp_fence_after();
+    if (warp >= 4 && warp < 8) down = xch[r];
+    __syncthreads();
     auto wait = [&](uint64_t *bar, uint32_t par) { return pp_wait(P, bar, par, lane); };
     const uint32_t tl = PP_TMEM + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
 
-    if (warp < 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int pos = real ? I.past + tok : -1;
-        const int first = a.window ? max(0, pos - a.window + 1) : 0;
-        float m = PP_NONE, l = 0.f;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        constexpr int HO = HD / 2;  // columns of O of a thread
+        const int pos = real ? I.past + tok : 2147483647;  // rows past the last are computed (from zeros) and dropped
+        const int first = a.window && real ? max(0, pos - a.window + 1) : 0;
+        float m = PP_NONE, l = 0.f, last = 1.f;  // last: the factor of the block whose O is still to come
+        float o[HO];
+#pragma unroll
+        for (int e = 0; e < HO; ++e) o[e] = 0.f;
         bool ok = true;
+        auto gather = [&](int j) {  // o = o * factor + O of block j
+            const int buf = j & 1;
+            if (!wait(B.o + buf, (j >> 1) & 1)) return false;
+            pp_fence_after();
+            float d[HO];
+#pragma unroll
+            for (int k = 0; k < HO / 32; ++k) pp_ld32(tl + 256 + buf * HD + W * HO + 32 * k, d + 32 * k);
+#pragma unroll
+            for (int k = 0; k < HO / 32; ++k) pp_wait_ld(d + 32 * k);
+            const float2 c = make_float2(last, last);
+#pragma unroll
+            for (int e = 0; e < HO; e += 2) {
+                const float2 y = pp_fma2(make_float2(o[e], o[e + 1]), c, make_float2(d[e], d[e + 1]));
+                o[e] = y.x;
+                o[e + 1] = y.y;
+            }
+            pp_fence_before();
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.oempty + buf);
+            return true;
+        };
         for (int j = 0; j < I.nblk; ++j) {
             const int buf = j & 1, ph = (j >> 1) & 1;
             ok = wait(B.s + buf, ph);
             if (!ok) break;
             pp_fence_after();
             const uint32_t tS = tl + buf * 128;
-            float s[128];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) pp_ld32(tS + 32 * k, s + 32 * k);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) pp_wait_ld(s + 32 * k);
-            const int r0 = I.base + PP_BLOCK * j;
-            if (__any_sync(0xffffffffu, r0 < first || r0 + PP_BLOCK - 1 > pos)) pp_mask(s, first - r0, pos - r0);
-            const float mt = pp_largest(s) * down;
+            float s[64];
+            pp_ld32(tS + 64 * W, s);
+            pp_ld32(tS + 64 * W + 32, s + 32);
+            pp_wait_ld(s);
+            pp_wait_ld(s + 32);
+            const int r0 = I.base + PP_BLOCK * j + 64 * W;
+            if (__any_sync(0xffffffffu, r0 < first || r0 + 63 > pos)) pp_mask(s, first - r0, min(pos, r0 + PP_BLOCK) - r0);
+            const float mine = pp_largest(s) * down;
+            // the other half's largest; past this wait both halves of S are in registers, and P may go over them
+            xch[buf * 256 + W * 128 + r] = mine;
+            pp_fence_before();
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.x + buf);
+            ok = wait(B.x + buf, ph);
+            if (!ok) break;
+            pp_fence_after();
+            const float mt = fmaxf(mine, xch[buf * 256 + (W ^ 1) * 128 + r]);
             const float mn = mt > m + PP_SLACK ? mt : m;
             const float corr = mn == m ? 1.f : pp_ex2(m - mn);
             l *= corr;
             m = mn;
-            if (j >= 2) ok = wait(B.cempty + buf, ph ^ 1);
-            if (!ok) break;
-            factor[buf * 128 + r] = corr;
-            __syncwarp();
-            if (lane == 0) pp_arrive(B.c + buf);
-            l += pp_probabilities<true>(s, tS, down, m);
+            l += pp_probabilities<true>(s, tS + 32 * W, down, m);
             pp_wait_st();
             pp_fence_before();
             __syncwarp();
             if (lane == 0) pp_arrive(B.p + buf);
-        }
-        // m and l follow as if they were one more block's factor
-        if (ok && I.nblk >= 2) ok = wait(B.cempty + (I.nblk & 1), ((I.nblk >> 1) & 1) ^ 1);
-        if (ok) {
-            factor[256 + r] = m;
-            factor[384 + r] = l;
-            __syncwarp();
-            if (lane == 0) pp_arrive(B.c + (I.nblk & 1));
-        }
-    } else if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-        float o[HD];
-#pragma unroll
-        for (int e = 0; e < HD; ++e) o[e] = 0.f;
-        bool ok = true;
-        for (int j = 0; j < I.nblk; ++j) {
-            const int buf = j & 1, ph = (j >> 1) & 1;
-            ok = wait(B.c + buf, ph);
-            if (!ok) break;
-            const float corr = factor[buf * 128 + r];
-            __syncwarp();
-            if (lane == 0) pp_arrive(B.cempty + buf);
-            ok = wait(B.o + buf, ph);
-            if (!ok) break;
-            pp_fence_after();
-#pragma unroll
-            for (int k = 0; k < HD / 32; ++k) {
-                float d[32];
-                pp_ld32(tl + 256 + buf * HD + 32 * k, d);
-                pp_wait_ld(d);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[32 * k + e] = fmaf(o[32 * k + e], corr, d[e]);
+            if (j > 0) {
+                ok = gather(j - 1);
+                if (!ok) break;
             }
-            pp_fence_before();
-            __syncwarp();
-            if (lane == 0) pp_arrive(B.oempty + buf);
+            last = corr;
         }
-        if (ok) ok = wait(B.c + (I.nblk & 1), (I.nblk >> 1) & 1);
+        if (ok && I.nblk > 0) ok = gather(I.nblk - 1);
+        if (ok) {  // the two halves' sums, exchanged as one more block's largest would be
+            const int buf = I.nblk & 1;
+            xch[buf * 256 + W * 128 + r] = l;
+            __syncwarp();
+            if (lane == 0) pp_arrive(B.x + buf);
+            ok = wait(B.x + buf, (I.nblk >> 1) & 1);
+        }
         if (ok && real) {
-            const float m = factor[256 + r], l = factor[384 + r], inv = 1.f / l;
-            float *out = (float *)a.out_dev + row * a.out_stride + (size_t)head * HD;
+            l += xch[(I.nblk & 1) * 256 + (W ^ 1) * 128 + r];
+            const float inv = 1.f / l;
+            float *out = (float *)a.out_dev + row * a.out_stride + (size_t)head * HD + W * HO;
 #pragma unroll
-            for (int k = 0; k < HD / 32; ++k) pp_store<float>(a, out + 32 * k, o + 32 * k, l, inv);
-            if (a.lse_dev) a.lse_dev[(size_t)row * a.n_heads + head] = pp_lse(m, l);
+            for (int k = 0; k < HO / 32; ++k) pp_store<float>(a, out + 32 * k, o + 32 * k, l, inv);
+            if (a.lse_dev && W == 0) a.lse_dev[(size_t)row * a.n_heads + head] = pp_lse(m, l);
         }
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
