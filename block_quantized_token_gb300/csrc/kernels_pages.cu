@@ -4,6 +4,8 @@
 #include "pages.cuh"
 #include "pages.h"
 
+#include <type_traits>
+
 namespace er {
 
 // ---------------------------------------------------------------------------
@@ -290,26 +292,57 @@ cudaError_t launch_rope_table(int hd, double base, int n, float *out, cudaStream
 // for the "halves" rotation, 4 c .. + 3 of each half of the head, so that a pair is in one lane.
 //
 // What bounds append: the bytes of the rows (a token's queries are read and written once, keys and values read
-// once and leave in 18 / 32 byte a value).  Queries and keys: a group keeps its token's (cos, sin) and both gains in
-// registers over several heads, the next head's values on their way.  Values: a warp takes a run of tokens whose
+// once and leave in 18 / 32 byte a value).  Queries and keys: a group keeps its token's gain times (cos, sin) in
+// registers over several heads, four heads' loads in flight; a key row is quantised from float32 steps, and again from
+// float64 ones where those leave a code in doubt (about one warp in a hundred).  Values: a warp takes a run of tokens whose
 // slots follow one another inside a tile, so that a prompt's tiles leave as whole 16-byte words although a V word
 // mixes four rows; a lone row leaves as bytes.
 // ---------------------------------------------------------------------------
-constexpr int AP_WARPS = 8;
-constexpr int AP_BLOCKS = 4;  // blocks an SM: latency, not registers, costs (2: 139 us, 3: 104, 4: 97 for 8192 bf16 tokens, append + read)
+// append + read of 8192 bf16 tokens, 32 query and 8 K/V heads of 128: 71 us (33.6 for the bytes alone at the copy rate).
+// What costs is instructions and latency, so warps count before registers: blocks of 8 warps 2 an SM 139 us, 3 104, 4 97;
+// then with the factors joined, 16-bit values kept as words and the unsure rows done after the others (few spills) 73,
+// and 71 in blocks of 4 warps.
+constexpr int AP_WARPS = 4;
+constexpr int AP_BLOCKS = 8;  // an SM
 
-template <class T>
-ER_DEV void ld8(const T *p, bool vec, float (&x)[8]) {
-    __align__(16) T v[8];
-    if (vec) {
+// N consecutive values as they are, in 32-bit words (kept as words: 16-bit values alone would take a register each)
+template <class T, int N>
+ER_DEV void ld_raw(const T *p, bool vec, uint32_t *w) {
+    constexpr int W = N * sizeof(T) / 4;
+    if (!vec) {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int k = 0; k < (int)(8 * sizeof(T)) / 16; ++k) reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(p)[k];
+            for (int e = 0; e < N; ++e) w[e] = reinterpret_cast<const uint32_t *>(p)[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                w[e] = (uint32_t) reinterpret_cast<const unsigned short *>(p)[2 * e] |
+                       (uint32_t) reinterpret_cast<const unsigned short *>(p)[2 * e + 1] << 16;
+        }
+    } else if constexpr (W % 4 == 0) {
+#pragma unroll
+        for (int k = 0; k < W / 4; ++k) {
+            const uint4 x = reinterpret_cast<const uint4 *>(p)[k];
+            w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+        }
     } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = p[e];
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
     }
+}
+// those words' 8 values
+template <class T>
+ER_DEV void raw_f32(const uint32_t (&w)[2 * sizeof(T)], float (&x)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = pg_ld<T>(v + e);
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (std::is_same<T, float>::value) {
+            x[e] = __uint_as_float(w[e]);
+        } else if constexpr (std::is_same<T, __half>::value) {
+            x[e] = __half2float(__ushort_as_half((unsigned short)(w[e >> 1] >> (16 * (e & 1)))));
+        } else {
+            x[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+        }
+    }
 }
 template <class T>
 ER_DEV void st8(T *p, bool vec, const float (&x)[8]) {
@@ -326,19 +359,6 @@ ER_DEV void st8(T *p, bool vec, const float (&x)[8]) {
 }
 // 4 consecutive values (8 or 16 bytes)
 template <class T>
-ER_DEV void ld4(const T *p, bool vec, float *x) {
-    __align__(16) T v[4];
-    if (vec) {
-        if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
-        else *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = p[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = pg_ld<T>(v + e);
-}
-template <class T>
 ER_DEV void st4(T *p, bool vec, const float *x) {
     __align__(16) T v[4];
 #pragma unroll
@@ -353,12 +373,12 @@ ER_DEV void st4(T *p, bool vec, const float *x) {
 }
 // a row in lane c's order (see above)
 template <class T, int HD, bool HALVES>
-ER_DEV void ld_row(const T *row, int c, bool vec, float (&x)[8]) {
+ER_DEV void ld_row(const T *row, int c, bool vec, uint32_t (&v)[2 * sizeof(T)]) {
     if constexpr (HALVES) {
-        ld4<T>(row + 4 * c, vec, x);
-        ld4<T>(row + HD / 2 + 4 * c, vec, x + 4);
+        ld_raw<T, 4>(row + 4 * c, vec, v);
+        ld_raw<T, 4>(row + HD / 2 + 4 * c, vec, v + sizeof(T));
     } else {
-        ld8<T>(row + 8 * c, vec, x);
+        ld_raw<T, 8>(row + 8 * c, vec, v);
     }
 }
 template <class T, int HD, bool HALVES>
@@ -425,33 +445,46 @@ ER_DEV bool ap_quant(const float (&y)[8], uint32_t &codes, float (&d)[2], int la
             m[s] = __uint_as_float(big | (key << 31));
         }
     }
-    codes = 0;
     float E = 0.f;
     if (CHECK) {
 #pragma unroll
         for (int s = 0; s < S; ++s) E = fmaxf(E, fabsf(m[s]));
         E *= 2.f * AP_ERR;
     }
+    // 1.5 * 2^23 + 8: adding it to a quotient leaves the code in the sum's last bits, rounded to nearest
+    constexpr float MAGIC = 12582920.f;
+    constexpr uint32_t BITS = 0x4B400000u;  // of 1.5 * 2^23
+    codes = 0;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const float dd = pg_scale(m[s]), inv = 1.f / dd;
         d[s] = dd;
-        // within this of a border between codes the quotient is taken again: the reciprocal's and the product's rounding of at
-        // most 8.5 (1 + 2^-8), and the row's own error
-        const float near = 3e-6f + (CHECK ? E * fabsf(inv) : 0.f);
+        // within this of a border between codes the quotient is in doubt: the reciprocal's and the product's rounding of at most
+        // 8.1, and the row's own error
+        const float sure = 0.5f - 3e-6f - (CHECK ? E * fabsf(inv) : 0.f);
         if (CHECK) unsure |= pg_scale(fabsf(m[s]) + E) != pg_scale(fabsf(m[s]) - E) || fabsf(mx[s] + mn[s]) <= 2.f * E;
         const bool none = dd == 0.f || isnan(dd);
+        float off = 0.f;  // the largest distance of a quotient from its code
+        uint32_t acc = 0;
 #pragma unroll
         for (int e = 0; e < EP; ++e) {
-            const float r = y[s * EP + e] * inv + 8.5f, f = floorf(r);
-            int c = min(max((int)f, 0), 15);
-            if (r - f < near || r - f > 1.f - near) {
-                if (CHECK) unsure = true;
-                else c = (int)fminf(fmaxf(roundf(y[s * EP + e] / dd) + 8.f, 0.f), 15.f);
-            }
-            codes |= (uint32_t)(none ? 8 : c) << (4 * (s * EP + e));
+            const float u = fmaf(y[s * EP + e], inv, MAGIC);
+            off = fmaxf(off, fabsf(fmaf(y[s * EP + e], inv, MAGIC - u)));
+            acc += (__float_as_uint(fminf(u, MAGIC + 7.f)) - BITS) << (4 * (s * EP + e));
         }
-        if (CHECK && none) unsure = true;
+        // (a limited or subnormal scale lets quotients pass 8 (1 + 2^-8); then the fields below would spill over)
+        const bool doubt = !none && !(off < sure && fabsf(m[s]) < 21600.f && fabsf(dd) >= 6.2e-5f);
+        if (CHECK) {
+            unsure |= doubt || none;
+        } else if (__any_sync(0xffffffffu, doubt)) {
+            if (doubt) {
+                acc = 0;
+#pragma unroll
+                for (int e = 0; e < EP; ++e)
+                    acc |= (uint32_t)fminf(fmaxf(roundf(y[s * EP + e] / dd) + 8.f, 0.f), 15.f) << (4 * (s * EP + e));
+            }
+        }
+        codes |= none ? (S == 1 ? 0x88888888u : s ? 0x88880000u : 0x8888u) : acc;
     }
     return unsure;
 }
@@ -468,7 +501,7 @@ struct AppendArgs {
     PagesView p;
     er_pages_append_args a;
     int parts;      // groups that share a token's queries and keys
-    int qk_blocks;  // blocks of queries and keys; those after them take the values
+    int v_blocks;   // blocks that take the values, first because a run takes longest; those after them take the others
     int chunk;      // tokens of a value warp's chunk (1 or 16)
 };
 
@@ -488,7 +521,7 @@ ER_DEV void append_qk(const AppendArgs &A) {
     const er_pages_append_args &a = A.a;
     const PagesView &p = A.p;
     const int lane = threadIdx.x & 31, c = lane % LG;
-    const long long grp = ((long long)blockIdx.x * AP_WARPS + (threadIdx.x >> 5)) * GPW + lane / LG;
+    const long long grp = ((long long)(blockIdx.x - A.v_blocks) * AP_WARPS + (threadIdx.x >> 5)) * GPW + lane / LG;
     const int t = (int)(grp / A.parts), part = (int)(grp - (long long)t * A.parts);
     const bool in = t < a.n_tokens;
     const int slot = in ? a.slots_dev[t] : -1;
@@ -536,23 +569,40 @@ ER_DEV void append_qk(const AppendArgs &A) {
             y[e1] = (x[e1] * co[e1] + x[e0] * si[e0]) * rs;
         }
     };
-    // Whole warps go round together (its groups' tokens and parts may differ); a row's values are on their way while the one
-    // before is worked.
-    auto rows_of = [&](const T *base, int64_t stride, bool vec, int n, auto work) {
+    // Whole warps go round together (its groups' tokens and parts may differ), U rows of a group at a time: their loads are
+    // in flight together.  work returns whether the row is to be done again by the exact steps, after the others of its U.
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;  // (8 with 3 / 4 of the warps: 78 us for 73; 2: 79 for 75)
+    auto rows_of = [&](const T *base, int64_t stride, bool vec, int n, auto work, auto again) {
         const T *src = base + t * stride + (size_t)part * HD;
-        float nx[8];
+        for (int r = part; r - part < n; r += U * A.parts) {
+            uint32_t v[U][2 * sizeof(T)];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) nx[e] = 0.f;
-        if (there && part < n) ld_row<T, HD, HALVES>(src, c, vec, nx);
-        for (int r = part; r - part < n; r += A.parts) {
-            float x[8];
+            for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = nx[e];
-            src += (size_t)A.parts * HD;
-            if (there && r + A.parts < n) ld_row<T, HD, HALVES>(src, c, vec, nx);
-            work(r, there && r < n, x);
+                for (int e = 0; e < (int)(2 * sizeof(T)); ++e) v[u][e] = 0;
+                if (there && r + u * A.parts < n) ld_row<T, HD, HALVES>(src + (size_t)u * A.parts * HD, c, vec, v[u]);
+            }
+            unsigned redo = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r - part + u * A.parts >= n) break;  // (the same in the whole warp)
+                float x[8];
+                raw_f32<T>(v[u], x);
+                redo |= (work(r + u * A.parts, there && r + u * A.parts < n, x) ? 1u : 0u) << u;
+            }
+            for (redo = __reduce_or_sync(0xffffffffu, redo); redo; redo &= redo - 1) {
+                const int u = __ffs(redo) - 1;
+                const bool live = there && r + u * A.parts < n;
+                uint32_t w[2 * sizeof(T)] = {};
+                if (live) ld_row<T, HD, HALVES>(src + (size_t)u * A.parts * HD, c, vec, w);
+                float x[8];
+                raw_f32<T>(w, x);
+                again(r + u * A.parts, live, x);
+            }
+            src += (size_t)U * A.parts * HD;
         }
     };
+    auto never = [](int, bool, const float (&)[8]) {};
     if (a.n_heads) {
         factors(a.q_gain_dev);
         T *dst = (T *)a.q_out_dev + t * a.q_out_stride;
@@ -560,55 +610,12 @@ ER_DEV void append_qk(const AppendArgs &A) {
             float y[8];
             row_of(x, a.q_gain_dev != nullptr, y);
             if (live) st_row<T, HD, HALVES>(dst + (size_t)r * HD, c, vo, y);
-        });
+            return false;
+        }, never);
     }
     const bool norm = a.k_gain_dev != nullptr;
     factors(a.k_gain_dev);
-    rows_of((const T *)a.k_dev, a.k_stride, vk, p.KV, [&](int r, bool live, const float (&x)[8]) {
-        uint32_t codes;
-        float d[2];
-        if (!norm && !turn) {
-            ap_quant<HALVES, false>(x, codes, d, lane);  // keys as they are
-        } else {
-            float y[8];
-            row_of(x, norm, y);
-            if (__any_sync(0xffffffffu, ap_quant<HALVES, true>(y, codes, d, lane) && live)) {
-                // those rows again in float64: their codes are those of the formula whatever the float32 steps were
-                double zs = 0.0, rs = 1.0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) zs += (double)x[e] * (double)x[e];
-#pragma unroll
-                for (int o = 1; o < LG; o <<= 1) zs += __shfl_xor_sync(0xffffffffu, zs, o);
-                if (norm) rs = 1.0 / sqrt(zs / HD + (double)a.eps);
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const float2 cs = table(i);
-                    double z[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float v = 0.f;
-                        int dm = 0;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (q == i) {
-                                const int e = HALVES ? q + 4 * k : 2 * q + k;
-                                v = x[e];
-                                dm = dim(e);
-                            }
-                        z[k] = (double)v * rs * (norm ? (double)__ldg(a.k_gain_dev + dm) : 1.0);
-                    }
-                    const float ya = (float)(z[0] * (double)cs.x - z[1] * (double)cs.y);
-                    const float yb = (float)(z[1] * (double)cs.x + z[0] * (double)cs.y);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (q == i) {
-                            y[HALVES ? q : 2 * q] = ya;
-                            y[HALVES ? q + 4 : 2 * q + 1] = yb;
-                        }
-                }
-                ap_quant<HALVES, false>(y, codes, d, lane);
-            }
-        }
+    auto store = [&](int r, bool live, uint32_t codes, const float (&d)[2]) {
         const uint32_t mate = __shfl_xor_sync(0xffffffffu, codes, 1);
         if (!live) return;
         uint8_t *tile = pg_tile(p.pool, p.page_rows, p.KV, HD, slot, r);
@@ -629,7 +636,48 @@ ER_DEV void append_qk(const AppendArgs &A) {
             *reinterpret_cast<uint32_t *>(tile + pg_k_word(in16, (c & 3) * (HD / 32) + (c >> 2), HD)) = ap_kword(codes);
             if ((c & 3) == 0) ks[c >> 2] = __float2half_rn(d[0]);
         }
-    });
+    };
+    auto exact = [&](int r, bool live, const float (&x)[8]) {
+        // in float64: the codes are those of the formula whatever the float32 steps were
+        double zs = 0.0, rs = 1.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) zs += (double)x[e] * (double)x[e];
+#pragma unroll
+        for (int o = 1; o < LG; o <<= 1) zs += __shfl_xor_sync(0xffffffffu, zs, o);
+        if (norm) rs = 1.0 / sqrt(zs / HD + (double)a.eps);
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 cs = table(i);
+            const int e0 = HALVES ? i : 2 * i, e1 = HALVES ? i + 4 : 2 * i + 1;
+            const double za = (double)x[e0] * rs * (norm ? (double)__ldg(a.k_gain_dev + dim(e0)) : 1.0);
+            const double zb = (double)x[e1] * rs * (norm ? (double)__ldg(a.k_gain_dev + dim(e1)) : 1.0);
+            y[e0] = (float)(za * (double)cs.x - zb * (double)cs.y);
+            y[e1] = (float)(zb * (double)cs.x + za * (double)cs.y);
+        }
+        uint32_t codes;
+        float d[2];
+        ap_quant<HALVES, false>(y, codes, d, lane);
+        store(r, live, codes, d);
+    };
+    if (!norm && !turn) {  // keys as they are
+        rows_of((const T *)a.k_dev, a.k_stride, vk, p.KV, [&](int r, bool live, const float (&x)[8]) {
+            uint32_t codes;
+            float d[2];
+            ap_quant<HALVES, false>(x, codes, d, lane);
+            store(r, live, codes, d);
+            return false;
+        }, never);
+    } else {
+        rows_of((const T *)a.k_dev, a.k_stride, vk, p.KV, [&](int r, bool live, const float (&x)[8]) {
+            uint32_t codes;
+            float d[2], y[8];
+            row_of(x, norm, y);
+            const bool unsure = ap_quant<HALVES, true>(y, codes, d, lane);
+            store(r, live, codes, d);
+            return unsure && live;
+        }, exact);
+    }
 }
 
 template <class T, int HD>
@@ -638,7 +686,7 @@ ER_DEV void append_v(const AppendArgs &A, uint32_t (&cw)[16][HD / 8 + 2], unsign
     const er_pages_append_args &a = A.a;
     const PagesView &p = A.p;
     const int lane = threadIdx.x & 31, c = lane % LG, gi = lane / LG;
-    const long long item = (long long)(blockIdx.x - A.qk_blocks) * AP_WARPS + (threadIdx.x >> 5);
+    const long long item = (long long)blockIdx.x * AP_WARPS + (threadIdx.x >> 5);
     const int chunk = (int)(item / p.KV), h = (int)(item - (long long)chunk * p.KV);
     const int t0 = chunk * A.chunk;
     if (t0 >= a.n_tokens) return;
@@ -666,10 +714,10 @@ ER_DEV void append_v(const AppendArgs &A, uint32_t (&cw)[16][HD / 8 + 2], unsign
 #pragma unroll 4
         for (int k0 = 0; k0 < n; k0 += GPW) {
             const int k = k0 + gi;
+            uint32_t v[2 * sizeof(T)] = {};
+            if (k < n) ld_raw<T, 8>(src + k * a.v_stride, vec, v);
             float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            if (k < n) ld8<T>(src + k * a.v_stride, vec, x);
+            raw_f32<T>(v, x);
             uint32_t codes;
             float d[2];
             ap_quant<false, false>(x, codes, d, lane);
@@ -720,17 +768,18 @@ template <class T, int HD, bool HALVES>
 __global__ void __launch_bounds__(AP_WARPS * 32, AP_BLOCKS) pages_append_kernel(const AppendArgs A) {
     __shared__ __align__(16) uint32_t cw[AP_WARPS][16][HD / 8 + 2];
     __shared__ unsigned short sc[AP_WARPS][16][HD / 32];
-    if ((int)blockIdx.x < A.qk_blocks) append_qk<T, HD, HALVES>(A);
-    else append_v<T, HD>(A, cw[threadIdx.x >> 5], sc[threadIdx.x >> 5]);
+    if ((int)blockIdx.x < A.v_blocks) append_v<T, HD>(A, cw[threadIdx.x >> 5], sc[threadIdx.x >> 5]);
+    else append_qk<T, HD, HALVES>(A);
 }
 
 template <class T>
 static cudaError_t append_t(const PagesView &p, const er_pages_append_args &a, int num_sms, cudaStream_t st) {
     AppendArgs A = {p, a, 1, 0, 16};
     const int rows = a.n_heads > p.KV ? a.n_heads : p.KV;
-    // Groups (of HD / 8 lanes) enough for twice the GPU's threads, and no more than one a row: a step's few tokens are
-    // spread row by row, a prompt's groups keep their token's table row and gains for several heads.
-    const long long want = 2ll * num_sms * 2048 / (p.hd / 8);
+    // Groups (of HD / 8 lanes) enough for the threads that the GPU holds at once, and no more than one a row: a step's few
+    // tokens are spread row by row, a prompt's groups keep their token's factors for several heads (8192 tokens: two
+    // groups a token 71 us, three 75, five 78, nine 88).
+    const long long want = (long long)num_sms * AP_BLOCKS * AP_WARPS * 32 / (p.hd / 8);
     const long long parts = (want + a.n_tokens - 1) / a.n_tokens;
     A.parts = (int)(parts < 1 ? 1 : parts > rows ? rows : parts);
     const long long per = AP_WARPS * 32 / (p.hd / 8);
@@ -740,7 +789,7 @@ static cudaError_t append_t(const PagesView &p, const er_pages_append_args &a, i
     const long long chunks = ((long long)a.n_tokens + A.chunk - 1) / A.chunk;
     const long long v = (chunks * p.KV + AP_WARPS - 1) / AP_WARPS;
     if (qk + v > 2147483647ll) return cudaErrorInvalidValue;
-    A.qk_blocks = (int)qk;
+    A.v_blocks = (int)v;
     const unsigned blocks = (unsigned)(qk + v);
     const bool halves = a.rope_style == ER_ROPE_HALVES;
     if (p.hd == 128)
