@@ -51,7 +51,7 @@ ER_DEV void plan_scan(long long &a, long long &b, long long (&ws)[2][PL_THREADS 
 __global__ void __launch_bounds__(PL_THREADS) pages_plan_kernel(PagesView p, er_pages_plan_args a, int *ticket) {
     __shared__ PlanShared s;
     const int tid = threadIdx.x, R = p.page_rows;
-    const long long rows_max = (long long)a.table_stride * R;
+    const long long rows_max = pg_max_len(a.table_stride, R);
     const int free_count = min(max(*a.free_count_dev, 0), p.n_pages);
     constexpr int PER = ER_PAGES_MAX_SEQS / PL_THREADS;
     int flag = 0;

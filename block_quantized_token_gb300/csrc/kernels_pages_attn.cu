@@ -152,7 +152,7 @@ struct PdArgs {
 };
 
 // the first row that any of a sequence's qn new tokens attends
-ER_DEV int pd_row0(int len, int qn, int window) { return window ? max(0, len - qn - window + 1) : 0; }
+ER_DEV int pd_row0(int len, int qn, int window) { return pg_first(len - qn, window); }
 // x / d for x >= 0, mostly below 2^32
 ER_DEV long long pd_div(long long x, int d) {
     return (x >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)d) : x / d;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                 const int q0 = a.q_start_dev[b], q1 = a.q_start_dev[b + 1], len = a.lens_dev[b];
                 int ns = 0;
                 const bool bad = q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 ||
-                                 (long long)len > (long long)a.table_stride * R;
+                                 len > pg_max_len(a.table_stride, R);
                 if (bad) {
                     if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
                 } else if ((long long)(q1 - q0) * G >= P.max_rows) {
@@ -372,10 +372,10 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
         for (int c = 0; c < 2; ++c) {
             const int tok = (U.rg * PD_ROWS + 2 * t + c) / G;
             pos[c] = tok < U.qn ? past + tok : -1;
-            first[c] = a.window ? max(0, pos[c] - a.window + 1) : 0;
+            first[c] = pg_first(pos[c], a.window);
         }
-        const int any_lo = a.window ? max(0, past + tok0 - a.window + 1) : 0, any_hi = past + tok1;
-        const int all_lo = a.window ? max(0, past + tok1 - a.window + 1) : 0, all_hi = past + tok0;
+        const int any_lo = pg_first(past + tok0, a.window), any_hi = past + tok1;
+        const int all_lo = pg_first(past + tok1, a.window), all_hi = past + tok0;
 
         // the queries as B: k16 steps 2 bb + i, the lane's dims 32 bb + 8 t + 4 i .. + 3 of column g
         uint32_t qh[2 * C::NB][2];

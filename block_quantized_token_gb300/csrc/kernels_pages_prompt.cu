@@ -221,7 +221,7 @@ ER_DEV bool pp_find(const PpArgs &P, PpBars &B, int warp, int lane, PpItem &I) {
             if (b < a.n_seqs) {
                 const int q0 = a.q_start_dev[b], q1 = a.q_start_dev[b + 1];
                 len = a.lens_dev[b];
-                if (q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 || (long long)len > (long long)a.table_stride * R) {
+                if (q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 || len > pg_max_len(a.table_stride, R)) {
                     if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
                 } else if ((long long)(q1 - q0) * G >= P.min_rows) {
                     n = (int)(((long long)(q1 - q0) * G + ROWS - 1) / ROWS);
@@ -255,11 +255,11 @@ ER_DEV bool pp_find(const PpArgs &P, PpBars &B, int warp, int lane, PpItem &I) {
     I.past = a.lens_dev[I.b] - qn;
     I.nf = (int)min((long long)qn * G - I.f0, (long long)ROWS);
     I.any_hi = I.past + (I.f0 + I.nf - 1) / G;
-    I.any_lo = a.window ? max(0, I.past + I.f0 / G - a.window + 1) : 0;
+    I.any_lo = pg_first(I.past + I.f0 / G, a.window);
     I.base = I.any_lo & ~15;
     I.nblk = I.any_hi < 0 ? 0 : (I.any_hi - I.base) / PP_BLOCK + 1;
     I.all_hi = I.past + I.f0 / G;
-    I.all_lo = a.window ? max(0, I.any_hi - a.window + 1) : 0;
+    I.all_lo = pg_first(I.any_hi, a.window);
     return true;
 }
 
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
         if (soft) {
             const uint32_t tl = PP_TMEM + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
             const uint32_t tS = tl + X * 128, tO = tl + 256 + X * HD;
-            const int pos = real ? I.past + tok : 2147483647;  // rows past the last are computed (from zeros) and dropped
+            const int pos = real ? max(I.past + tok, -1) : 2147483647;  // rows past the last are computed (from zeros) and dropped
             const int first = a.window && real ? max(0, pos - a.window + 1) : 0;
             float m = PP_NONE, l = 0.f;
             bool ok = true;
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         constexpr int HO = HD / 2;  // columns of O of a thread
-        const int pos = real ? I.past + tok : 2147483647;  // rows past the last are computed (from zeros) and dropped
+        const int pos = real ? max(I.past + tok, -1) : 2147483647;  // rows past the last are computed (from zeros) and dropped
         const int first = a.window && real ? max(0, pos - a.window + 1) : 0;
         float m = PP_NONE, l = 0.f, last = 1.f;  // last: the factor of the block whose O is still to come
         float o[HO];

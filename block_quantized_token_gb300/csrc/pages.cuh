@@ -75,4 +75,12 @@ ER_DEV __half pg_cvt<__half>(float v) { return __float2half_rn(v); }
 template <>
 ER_DEV __nv_bfloat16 pg_cvt<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+constexpr int PG_MAX_LEN = 2147483647 - 1024;
+// a sequence's rows at most: what its table holds, and fewer than 2^31 by so much that sums with a block or a page stay ints
+ER_DEV int pg_max_len(int table_stride, int page_rows) {
+    return (int)min((long long)table_stride * page_rows, (long long)PG_MAX_LEN);
+}
+// the first row that the token at position p attends (p < 0: none, whatever this says)
+ER_DEV int pg_first(int p, int window) { return window ? max(0, max(p, 0) - (window - 1)) : 0; }
+
 }  // namespace er

@@ -24,6 +24,9 @@ er_status check_config(const er_pages_config *c) {
     if ((long long)c->n_pages * c->page_rows > 2147483647ll)
         return er_fail_status(ER_EINVAL, "n_pages * page_rows must be below 2^31");
     if (c->n_kv_heads > 1024 || c->n_layers > 65536) return er_fail_status(ER_EINVAL, "n_kv_heads or n_layers too large");
+    // a layer's tiles have 32-bit numbers in the kernels
+    if ((long long)c->n_pages * (c->page_rows / 16) * c->n_kv_heads > 2147483647ll)
+        return er_fail_status(ER_EINVAL, "n_pages * page_rows * n_kv_heads must be below 2^35");
     return ER_OK;
 }
 
@@ -34,6 +37,11 @@ size_t layer_bytes(const er_pages_config *c) {
 bool row_type(int t) { return t == ER_F32 || t == ER_F16 || t == ER_BF16; }
 int type_bytes(int t) { return t == ER_F32 ? 4 : 2; }
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+template <class... P>
+bool words(const P *...p) {  // int32 and float arrays (NULL is)
+    return (((uintptr_t)p | ...) & 3) == 0;
+}
 
 er_status check_handle(const er_pages *p) {
     if (!p) return er_fail_status(ER_EINVAL, "handle is NULL");
@@ -111,6 +119,9 @@ er_status er_pages_plan(er_pages *p, const er_pages_plan_args *a, void *stream) 
         !a->free_count_out_dev || !a->q_start_dev ||
         (a->max_tokens && (!a->positions_dev || !a->slots_dev || !a->seqs_dev)))
         return er_fail_status(ER_EINVAL, "NULL argument");
+    if (!words(a->lens_dev, a->new_dev, a->free_dev, a->free_count_dev, a->tables_dev, a->lens_out_dev, a->free_count_out_dev,
+               a->q_start_dev, a->positions_dev, a->slots_dev, a->seqs_dev))
+        return er_fail_status(ER_EINVAL, "int arrays must be 4-byte aligned");
     if (er_status s = check_handle(p); s != ER_OK) return s;
     return done(launch_pages_plan(view_of(p, 0), *a, p->ticket, p->num_sms, (cudaStream_t)stream), "er_pages_plan");
 }
@@ -120,6 +131,7 @@ er_status er_pages_release(er_pages *p, int32_t n_seqs, const int32_t *done_dev,
     if (!p || !done_dev || !lens || !tables || !free_list || !free_count) return er_fail_status(ER_EINVAL, "NULL argument");
     if (n_seqs < 1 || n_seqs > ER_PAGES_MAX_SEQS) return er_fail_status(ER_EINVAL, "n_seqs must be in 1..1024");
     if (table_stride < 1) return er_fail_status(ER_EINVAL, "table_stride must be positive");
+    if (!words(done_dev, lens, tables, free_list, free_count)) return er_fail_status(ER_EINVAL, "int arrays must be 4-byte aligned");
     if (er_status s = check_handle(p); s != ER_OK) return s;
     return done(launch_pages_release(view_of(p, 0), n_seqs, done_dev, lens, tables, table_stride, free_list, free_count,
                                      (cudaStream_t)stream),
@@ -148,6 +160,8 @@ er_status er_pages_append(er_pages *p, int32_t layer, const er_pages_append_args
     if (a->rope_dev && (!a->positions_dev || a->rope_positions < 1))
         return er_fail_status(ER_EINVAL, "a rope table needs positions and rope_positions >= 1");
     if (a->rope_dev && !aligned(a->rope_dev, 8)) return er_fail_status(ER_EINVAL, "the rope table must be 8-byte aligned");
+    if (!words(a->q_gain_dev, a->k_gain_dev, a->positions_dev, a->slots_dev))
+        return er_fail_status(ER_EINVAL, "gains, positions and slots must be 4-byte aligned");
     if (!(a->eps >= 0.f) || isinf(a->eps)) return er_fail_status(ER_EINVAL, "eps must be finite and >= 0");
     const int64_t row = (int64_t)a->n_heads * p->cfg.head_dim, kvd = (int64_t)p->cfg.n_kv_heads * p->cfg.head_dim;
     if (a->q_stride < row || a->q_out_stride < row || a->k_stride < kvd || a->v_stride < kvd)
@@ -165,6 +179,7 @@ er_status er_pages_read(er_pages *p, int32_t layer, int32_t n, const int32_t *sl
     if (er_status s = check_layer(p, layer); s != ER_OK) return s;
     if (!row_type(type)) return er_fail_status(ER_EINVAL, "type must be ER_F32, ER_F16 or ER_BF16");
     if (n < 0 || (n && !slots)) return er_fail_status(ER_EINVAL, "n negative or slots NULL");
+    if (!words(slots)) return er_fail_status(ER_EINVAL, "slots must be 4-byte aligned");
     if (!aligned(k, type_bytes(type)) || !aligned(v, type_bytes(type)))
         return er_fail_status(ER_EINVAL, "rows must be aligned to their type");
     if (!n || (!k && !v)) return ER_OK;
@@ -180,7 +195,10 @@ er_status er_pages_attention(er_pages *p, int32_t layer, const er_pages_attentio
         return er_fail_status(ER_EINVAL, "n_tokens, table_stride or window out of range");
     if (a->n_heads < 1 || a->n_heads % p->cfg.n_kv_heads || a->n_heads / p->cfg.n_kv_heads > 64)
         return er_fail_status(ER_EINVAL, "n_heads must be a multiple of n_kv_heads, at most 64 times it");
+    if ((int64_t)a->n_tokens * (a->n_heads / p->cfg.n_kv_heads) > 2147483647ll - 1024)
+        return er_fail_status(ER_EINVAL, "n_tokens * n_heads / n_kv_heads must be below 2^31 - 1024");
     if (!a->n_tokens) return ER_OK;
+    if (!words(a->q_start_dev, a->lens_dev, a->tables_dev)) return er_fail_status(ER_EINVAL, "int arrays must be 4-byte aligned");
     if (!a->q_dev || !a->out_dev || !a->q_start_dev || !a->lens_dev || !a->tables_dev)
         return er_fail_status(ER_EINVAL, "NULL argument");
     const int64_t row = (int64_t)a->n_heads * p->cfg.head_dim;

@@ -46,7 +46,7 @@ enum { ER_BF16 = 30 };
  *
  * Configuration.  page_rows: a multiple of 16 up to 1024; head_dim 64 or 128
  * (else ER_EUNSUPPORTED); kv_type ER_Q4_0 (another er_dtype: ER_EUNSUPPORTED);
- * n_pages * page_rows < 2^31.  The handle owns scratch only; it belongs to the
+ * n_pages * page_rows < 2^31 and that times n_kv_heads < 2^35.  The handle owns scratch only; it belongs to the
  * device it was created on (a call with another device current is ER_EINVAL).
  * The calls of one handle share its scratch: order them (one stream, or
  * events), captured graphs of them included.  Work that overlaps takes a handle
@@ -68,7 +68,7 @@ ER_API void er_pages_destroy(er_pages *p);
  * need are at most *free_count_dev and their new tokens at most max_tokens; the
  * first that does not fit and every one after it get nothing (flag bit 0).  A
  * request with a negative length or count, or whose rows pass its table
- * (table_stride pages), gets nothing either, by itself (flag bit 1).  Written:
+ * (table_stride pages) or 2^31 - 1025, gets nothing either, by itself (flag bit 1).  Written:
  *   tables_dev           [n_seqs][table_stride]: the new pages' entries only; the
  *                        i-th page given out is free_dev[*free_count_dev - 1 - i]
  *   lens_out_dev         [n_seqs] lens + admitted tokens (may be lens_dev)
@@ -149,10 +149,11 @@ ER_API er_status er_pages_read(er_pages *p, int32_t layer, int32_t n, const int3
  * no sequence are left alone.  Scores, softmax and sums are fp32; fp32 queries
  * and probabilities enter the tensor cores as two fp16 halves, 16-bit queries'
  * probabilities in long prompts as one.  Results do not depend on timing.
- *   - A q_start_dev that falls or passes n_tokens, a length below 0 or past the
- *     table, and a table entry outside the pool set flag bit 1 and leave that
+ *   - A q_start_dev that falls or passes n_tokens, a length below 0, past the
+ *     table or past 2^31 - 1025, and a table entry outside the pool set flag bit 1 and leave that
  *     sequence's outputs unspecified; nothing outside the pool is read.
- *   - n_heads must be a multiple of n_kv_heads, at most 64 times it. */
+ *   - n_heads must be a multiple of n_kv_heads, at most 64 times it, and n_tokens
+ *     times that ratio below 2^31 - 1024. */
 typedef struct {
     int32_t n_seqs, n_tokens, n_heads, type, table_stride, window;
     const void *q_dev;

@@ -798,3 +798,156 @@ def test_handles_free_what_they_allocate():
         c.close()
         break
     assert i >= 1 and er.er_debug_live_allocations() == n
+
+
+# ------------------------------------------------------------------------------------------------------------------
+# sizes and contents at the edges of what the header allows
+# ------------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,new", [("f32", 1), ("bf16", 9), ("f32", 70), ("f16", 140)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 20])
+def test_window_past_every_length(dtype, new, window):
+    """The widest windows, with tokens before row 0: position - window must not wrap."""
+    b = Batch([new // 2, 300, new], [new] * 3, 4, 2, 64, 16, dtype, seed=31, window=window)
+    b.check(*b.run())
+    fine(b.cache)
+
+
+def test_lengths_next_to_2_31_are_flagged():
+    from block_quantized_token_gb300 import er
+    cache = paged(4, 16, 1, 64, fill=noise(32))
+    stride = 1 << 28  # (the table has one entry; nothing may look further)
+    one, out = ints([0]), torch.full((2, 1, 64), 7.0, device="cuda")
+    for n in (2 ** 31 - 1, 2 ** 31 - 1024):
+        lens, start, new = ints([n]), ints([0, 2]), ints([0])
+        er.er_pages_attention(cache.handle, 0, er.er_pages_attention_args(
+            1, 2, 1, er.ER_F32, stride, 0, out.data_ptr(), out.data_ptr(), None, 64, 64, start.data_ptr(),
+            lens.data_ptr(), one.data_ptr(), 0.0))
+        fine(cache, 2)
+        lo, co, q, t = ints([-7]), ints([-7]), ints([-7, -7]), [ints([-7] * 4) for _ in range(3)]
+        er.er_pages_plan(cache.handle, er.er_pages_plan_args(
+            1, 4, stride, lens.data_ptr(), new.data_ptr(), one.data_ptr(), ints([1]).data_ptr(), one.data_ptr(),
+            lo.data_ptr(), co.data_ptr(), q.data_ptr(), *(x.data_ptr() for x in t)))
+        fine(cache, 2)
+        assert lo.item() == n and co.item() == 1 and q.tolist() == [0, 0] and t[1].tolist() == [-1] * 4
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv,hd,page", [(64, 1, 128, 16), (64, 1, 64, 1024), (34, 2, 64, 112), (63, 1, 128, 32)])
+@pytest.mark.parametrize("new", [[1], [1, 1, 0, 1], [3, 0, 1, 40]])
+def test_wide_groups_and_large_pages(dtype, heads, kv, hd, page, new):
+    b = Batch([1 + 700 * i for i in range(1, len(new) + 1)], new, heads, kv, hd, page, dtype, seed=34, tail=2)
+    b.check(*b.run())
+    fine(b.cache)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_many_sequences(dtype, mixed):
+    """More sequences than one launch lists, single tokens alone and among prompts."""
+    rng = np.random.default_rng(35)
+    lens, new = rng.integers(0, 60, 700), np.ones(700, int)
+    new[::7] = 0
+    if mixed:
+        for i in (0, 31, 32, 511, 512, 690):
+            lens[i], new[i] = 150 + i % 90, 40 + i % 70
+    b = Batch(lens.tolist(), new.tolist(), 4, 2, 64, 16, dtype, seed=36, tail=3)
+    b.check(*b.run())
+    fine(b.cache)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("new", [1, 100])
+def test_rows_at_odd_addresses(dtype, new):
+    """Queries and outputs one value past an aligned address, and a stride of an odd number of values."""
+    b = Batch([333, 40 + new], [new, new], 4, 2, 64, 16, dtype, seed=37)
+    out, lse = b.run()
+    n = b.q.shape[0]
+    def odd(fill):
+        flat = torch.full((n * 261 + 1,), fill, dtype=b.q.dtype, device="cuda")
+        return flat, flat[1:].view(n, 261)[:, :256].view(n, 4, 64)
+    (_, q), (flat, o) = odd(0.0), odd(7.0)
+    q.copy_(b.q)
+    o2, l2 = b.run(out=o, q=q)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+    assert flat[0] == 7 and (flat[1:].view(n, 261)[:, 256:] == 7).all()
+    o3, l3 = b.run(out=q, q=q)  # over the queries themselves
+    assert torch.equal(o3, out) and torch.equal(l3, lse)
+
+
+@pytest.mark.parametrize("dtype,new", [("f32", 1), ("bf16", 1), ("f32", 50), ("bf16", 100)])
+def test_window_leaves_earlier_pages_unread(dtype, new):
+    """Pages before every token's window may be given back: their entries are not looked at.  Another layer's rows."""
+    b = Batch([700, 900], [new, new], 4, 2, 64, 16, dtype, seed=38, window=100)
+    first = b.run()
+    b.check(*first)
+    for i, n in enumerate(b.lens):
+        b.tables[i, :(n - new - 100 + 1) // 16] = -1
+    again = b.run()
+    fine(b.cache)
+    three = paged(b.pages, 16, 2, 64, layers=3, fill=noise(39))
+    three.pool.view(3, -1)[2].copy_(b.cache.pool)
+    out, lse = torch.empty_like(first[0]), torch.empty_like(first[1])
+    three.attention(2, b.q, out, *b.args(), window=100, lse=lse)
+    for o, z in (again, (out, lse)):
+        assert torch.equal(o, first[0]) and torch.equal(z, first[1])
+    with pytest.raises(Exception):
+        three.attention(3, b.q, out, *b.args())
+
+
+def test_two_graphs_of_one_handle_in_turn():
+    """A decode step and a prompt captured apart; replayed one after the other they share the handle's scratch."""
+    small, large = (Batch(l, n, 8, 2, 128, 16, "bf16", seed=40) for l, n in (([5000, 90], [1, 1]), ([700, 300], [200, 1])))
+    want, graphs = [small.run(), large.run()], []
+    pool = torch.cat([small.cache.pool, large.cache.pool])
+    cache = paged(small.pages + large.pages, 16, 2, 128, pool=pool)
+    large.tables = np.where(large.tables >= 0, large.tables + small.pages, large.tables)
+    side = torch.cuda.Stream()
+    for b in (small, large):
+        args = b.args()
+        out, lse = torch.zeros_like(b.q), torch.zeros(tuple(b.q.shape[:2]), device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            cache.attention(0, b.q, out, *args, lse=lse)
+        graphs.append((g, out, lse, args))
+    for _ in range(4):
+        for (g, out, lse, _), w in zip(graphs, want):
+            out.zero_()
+            g.replay()
+            assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+    fine(cache)
+
+
+def test_more_refusals():
+    from block_quantized_token_gb300 import er
+    cache = paged(4, 16, 2, 64, fill=noise(41))
+    x, i = torch.zeros((4, 2, 64), device="cuda"), ints([0] * 8)
+    p, ip = x.data_ptr(), i.data_ptr()
+    base = dict(n_seqs=1, n_tokens=4, n_heads=2, type=er.ER_F32, table_stride=4, window=0, q=p, out=p, lse=None,
+                q_stride=128, out_stride=128, q_start=ip, lens=ip, tables=ip, scale=0.0)
+    calls = [lambda kw=kw: er.er_pages_attention(cache.handle, 0, er.er_pages_attention_args(**{**base, **kw}))
+             for kw in (dict(q_start=ip + 1), dict(lens=ip + 2), dict(tables=ip + 3), dict(n_tokens=2 ** 31 - 1),
+                        dict(n_tokens=1 << 26, n_heads=128, q_stride=8192, out_stride=8192))]
+    base_p = dict(n_seqs=1, max_tokens=4, table_stride=4, lens=ip, new_=ip, free=ip, free_count=ip, tables=ip, lens_out=ip,
+                  free_count_out=ip, q_start=ip, positions=ip, slots=ip, seqs=ip)
+    calls += [lambda n=n: er.er_pages_plan(cache.handle, er.er_pages_plan_args(**{**base_p, n: ip + 2}))
+              for n in ("lens", "new_", "free", "free_count", "tables", "lens_out", "free_count_out", "q_start", "positions",
+                        "slots", "seqs")]
+    base_a = dict(n_tokens=4, n_heads=2, type=er.ER_F32, rope_style=0, rope_positions=0, q=p, k=p, v=p, q_out=p,
+                  q_stride=128, k_stride=128, v_stride=128, q_out_stride=128, q_gain=None, k_gain=None, rope=None,
+                  positions=None, slots=ip, eps=1e-5)
+    calls += [lambda kw=kw: er.er_pages_append(cache.handle, 0, er.er_pages_append_args(**{**base_a, **kw}))
+              for kw in (dict(slots=ip + 1), dict(q_gain=p + 2), dict(k_gain=p + 1),
+                         dict(rope=p, rope_positions=1, positions=ip + 2))]
+    calls += [lambda: er.er_pages_read(cache.handle, 0, 1, ip + 2, er.ER_F32, p, p),
+              lambda: er.er_pages_release(cache.handle, 1, ip + 1, ip, ip, 1, ip, ip),
+              lambda: er.er_pages_release(cache.handle, 1, ip, ip, ip + 2, 1, ip, ip),
+              lambda: er.er_pages_release(cache.handle, 0, ip, ip, ip, 1, ip, ip),
+              lambda: er.er_pages_release(cache.handle, 1, ip, ip, ip, 0, ip, ip)]
+    for call in calls:
+        with pytest.raises(er.ErError) as e:
+            call()
+        assert e.value.status == er.ER_EINVAL
+    torch.cuda.synchronize()
+    assert (x == 0).all() and (i == 0).all()
+    fine(cache)

@@ -36,7 +36,7 @@ def test_pool_bytes(er):
     ("page_rows", 0, "ER_EINVAL"), ("page_rows", 24, "ER_EINVAL"), ("page_rows", 2048, "ER_EINVAL"),
     ("n_kv_heads", 0, "ER_EINVAL"), ("head_dim", 96, "ER_EUNSUPPORTED"), ("head_dim", 0, "ER_EINVAL"),
     ("kv_type", 8, "ER_EUNSUPPORTED"), ("kv_type", 1, "ER_EUNSUPPORTED"), ("kv_type", 5, "ER_EINVAL"),
-    ("n_pages", 1 << 27, "ER_EINVAL")])
+    ("n_pages", 1 << 27, "ER_EINVAL"), ("n_kv_heads", 1025, "ER_EINVAL"), ("n_layers", 65537, "ER_EINVAL")])
 def test_config_refused(er, field, value, status):
     cfg = _cfg(er, **{field: value})
     assert er.er_pages_pool_bytes(cfg) == 0
@@ -44,6 +44,18 @@ def test_config_refused(er, field, value, status):
         er.er_pages_create(cfg, 4096)
     assert e.value.status == getattr(er, status)
     assert er.er_last_error()
+
+
+def test_config_tiles_of_a_layer_fit_32_bits(er):
+    for pages, kv in (((1 << 21) - 1, 17), (1 << 20, 32), (1 << 15, 1024)):
+        cfg = _cfg(er, n_pages=pages, page_rows=1024, n_kv_heads=kv)
+        assert er.er_pages_pool_bytes(cfg) == 0
+        with pytest.raises(er.ErError) as e:
+            er.er_pages_create(cfg, 4096)
+        assert e.value.status == er.ER_EINVAL
+    # the largest of all: past 32 bits everywhere, and inside 64
+    assert er.er_pages_pool_bytes(_cfg(er, n_layers=65536, n_pages=(1 << 21) - 1, page_rows=1024, n_kv_heads=16, head_dim=128)) \
+        == 65536 * ((1 << 21) - 1) * 64 * 16 * 18 * 128
 
 
 def test_null_and_misaligned_refused(er):
