@@ -27,8 +27,8 @@
 //   O^T += V^T P^T.  One code word is a lane's whole A operand, a mask and one FMA a pair, exact.  Probabilities go from
 //         the scores' layout to B's by movmatrix, as hi + lo halves (2^-22; bf16 outputs: hi alone, 2^-11).
 // Masks.  Tiles that some row of the unit attends only in part go through a path that masks scores and zeroes the
-// scales of rows nobody attends (they may hold anything); a NaN value that only some of the unit's tokens attend
-// is carried by their scores instead.
+// scales of rows nobody attends (they may hold anything).  There a NaN value is carried by the scores of the tokens that
+// attend it, where the unit's tokens differ in that (all their dims become NaN).
 #include <type_traits>
 
 #include "pages.cuh"
@@ -374,6 +374,13 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
             pos[c] = tok < U.qn ? past + tok : -1;
             first[c] = pg_first(pos[c], a.window);
         }
+        // Values that are NaN: a step that only some of the unit's rows attend carries them by its scores instead, and its values
+        // with them are 0.  `carry`, `carried`: the largest magnitude of a scale that is left to the values, of the steps
+        // whose scores are next and whose values are (infinity's, or NaN's where nothing is carried: one token, or scores that
+        // were not masked).
+        constexpr uint32_t NEVER = 0x7FFFu;
+        const uint32_t carry = tok0 < tok1 ? 0x7C00u : NEVER;
+        uint32_t carried = carry;
         const int any_lo = pg_first(past + tok0, a.window), any_hi = past + tok1;
         const int all_lo = pg_first(past + tok1, a.window), all_hi = past + tok0;
 
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                     for (int bb = 0; bb < C::NB; ++bb)
 #pragma unroll
                         for (int v = 0; v < 2; ++v)
-                            vnan[v] |= (vs[(((g >> 1) * C::NB + bb) * 2 + v) * 2 + (g & 1)] & 0x7FFF) > 0x7C00;
+                            vnan[v] |= (vs[(((g >> 1) * C::NB + bb) * 2 + v) * 2 + (g & 1)] & 0x7FFF) > carry;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int r = r0 + 16 * n + g + 8 * (k >> 1);
@@ -578,14 +585,15 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                     const uint4 y = *reinterpret_cast<const uint4 *>(sn + pg_off_v(HD) + q * 512 + lane * 16);
                     vw[q][0] = y.x; vw[q][1] = y.y; vw[q][2] = y.z; vw[q][3] = y.w;
                 }
-                if constexpr (EDGE) {  // scales of rows that nobody attends, or that are NaN: 0
+                if constexpr (EDGE) {  // scales of rows that nobody attends, or that are NaN and carried by the scores: 0
 #pragma unroll
                     for (int bb = 0; bb < C::NB; ++bb)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int r = r0 + 16 * n + 2 * t + (k & 1) + 8 * (k >> 1);
                             const uint32_t half = (k & 1) ? 0xFFFF0000u : 0x0000FFFFu;
-                            if (((vd[bb][k >> 1] & half) & 0x7FFF7FFFu) > (0x7C007C00u & half) || r < any_lo || r > any_hi)
+                            const uint32_t above = (k & 1) ? carried << 16 | 0xFFFFu : carried;
+                            if ((vd[bb][k >> 1] & half & 0x7FFF7FFFu) > above || r < any_lo || r > any_hi)
                                 vd[bb][k >> 1] &= ~half;
                         }
                 }
@@ -642,9 +650,11 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                 if (more && plain(r0) && plain(r0 + PD_STEP)) {
                     values(std::false_type{}, here, r0);
                     scores(std::false_type{}, sl, r0 + PD_STEP, x);
+                    carried = NEVER;
                 } else {
                     values(std::true_type{}, here, r0);
                     if (more) scores(std::true_type{}, sl, r0 + PD_STEP, x);
+                    carried = carry;
                 }
                 __syncwarp();  // every lane has read the slot
                 issue();

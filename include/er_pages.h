@@ -152,6 +152,9 @@ ER_API er_status er_pages_read(er_pages *p, int32_t layer, int32_t n, const int3
  *   - A q_start_dev that falls or passes n_tokens, a length below 0, past the
  *     table or past 2^31 - 1025, and a table entry outside the pool set flag bit 1 and leave that
  *     sequence's outputs unspecified; nothing outside the pool is read.
+ *   - A NaN in a cached row makes NaN of at least its 32 dims (of a value) or of
+ *     the whole head (of a key) in every token that attends the row, and of
+ *     nothing in those that do not.
  *   - n_heads must be a multiple of n_kv_heads, at most 64 times it, and n_tokens
  *     times that ratio below 2^31 - 1024. */
 typedef struct {

@@ -831,6 +831,45 @@ def test_lengths_next_to_2_31_are_flagged():
         assert lo.item() == n and co.item() == 1 and q.tolist() == [0, 0] and t[1].tolist() == [-1] * 4
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("new", [1, 5, 100])
+@pytest.mark.parametrize("row", [0, 31, 130, 255, 256, 287, 290, 299])
+def test_nan_values_reach_the_tokens_that_attend_them(dtype, new, row):
+    """A NaN in 32 dims of one cached V row: in those dims of every token that attends it, in no token that does not; a
+    single token's other dims stay as they were."""
+    b = Batch([300], [new], 4, 2, 128, 16, dtype, seed=33)
+    v = torch.tensor(b.v[0][row:row + 1], dtype=torch.float32, device="cuda")
+    v[:, 0, 40] = float("nan")
+    k = torch.tensor(b.k[0][row:row + 1], dtype=torch.float32, device="cuda")
+    clean, zc = b.run()
+    b.cache.append(0, None, k, v, None, ints([b.tables[0, row // 16] * 16 + row % 16]))
+    out, lse = b.run()
+    attends = torch.arange(300 - new, 300, device="cuda") >= row
+    bad = torch.isnan(out)
+    assert bad[attends][:, :2, 32:64].all() and not bad[~attends].any() and not bad[:, 2:].any()
+    assert torch.equal(out[:, 2:], clean[:, 2:]) and torch.equal(lse[:, 2:], zc[:, 2:])
+    if new == 1:
+        assert not bad[..., :32].any() and not bad[..., 64:].any() and torch.isfinite(lse).all()
+        other = [d for d in range(128) if not 32 <= d < 64]
+        assert torch.equal(out[..., other], clean[..., other]) and torch.equal(lse, zc)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("row", [3, 19967, 19968, 19999, 20000, 20007, 20009])
+@pytest.mark.parametrize("new", [1, 5])
+def test_nan_value_in_a_long_sequence(dtype, row, new):
+    """The same where warps walk several blocks of rows, the last of them not whole: before it, in it, far from it."""
+    b = Batch([20010], [new], 8, 8, 128, 16, dtype, seed=42)
+    k, v = (torch.tensor(x[0][row:row + 1], dtype=torch.float32, device="cuda") for x in (b.k, b.v))
+    v[:, :, 100] = float("nan")
+    b.cache.append(0, None, k, v, None, ints([b.tables[0, row // 16] * 16 + row % 16]))
+    bad = torch.isnan(b.run()[0])
+    attends = torch.arange(20010 - new, 20010, device="cuda") >= row
+    assert bad[attends][..., 96:].all() and not bad[~attends].any()
+    if new == 1:
+        assert not bad[..., :96].any()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("heads,kv,hd,page", [(64, 1, 128, 16), (64, 1, 64, 1024), (34, 2, 64, 112), (63, 1, 128, 32)])
 @pytest.mark.parametrize("new", [[1], [1, 1, 0, 1], [3, 0, 1, 40]])
