@@ -67,7 +67,7 @@ struct PpArgs {
 };
 
 struct PpBars {
-    uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], oempty[2], x[2];
+    uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], oempty[2], x[2], q;
     uint32_t tmem;
     int item[4];  // sequence, first query row, KV head, found
 };
@@ -271,64 +271,77 @@ ER_DEV bool pp_wait(const PpArgs &P, uint64_t *bar, uint32_t par, int lane) {
     return ok;
 }
 
-// A query row as a K-major operand: row r of the one at dst, times a power of two that brings its largest value to [2^14,
-// 2^15) (and the scale's sign); LO: the lo halves go to dst + OP.  Returns the factor that takes scores to log2 units.
-template <class T, int HD, bool LO>
-ER_DEV float pp_query(const er_pages_attention_args &a, uint8_t *dst, const T *src, bool real, int r) {
+// NR query rows, row0 .. of the tile that starts at query row f0 (nf of its rows are real, the others zeros), as rows of the
+// K-major operand at dst.  A row is times a power of two that brings its largest value to [2^14, 2^15) (and the scale's
+// sign); LO: the lo halves go to dst + OP.  down[row]: the factor that takes its scores to log2 units.  16 bytes of a row a
+// lane, every row's loads in flight together (a thread a row, four loads at a time, took 20,000 cycles of a CTA; this
+// takes less than the first block's way through the ring).
+template <class T, int HD, bool LO, int NR>
+ER_DEV void pp_queries(const er_pages_attention_args &a, const PpItem &I, int G, uint8_t *dst, float *down, int f0, int nf, int row0,
+                       int lane) {
     using C = PpCfg<HD>;
+    constexpr int LPR = HD * (int)sizeof(T) / 16, RPP = 32 / LPR, PASSES = NR / RPP, V = 16 / (int)sizeof(T);
     const bool vec = ((uintptr_t)a.q_dev & 15) == 0 && (a.q_stride * sizeof(T)) % 16 == 0;
-    auto load8 = [&](int c, float (&x)[8]) {
-        __align__(16) T v[8];
-        if (!real) {
+    const int c = lane % LPR;  // values V c .. of the row
+    uint4 raw[PASSES];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = pg_cvt<T>(0.f);
-        } else if (vec) {
+    for (int p = 0; p < PASSES; ++p) {
+        const int r = row0 + p * RPP + lane / LPR, f = f0 + r, tok = f / G;
+        raw[p] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < nf) {
+            const T *src = (const T *)a.q_dev + (I.q0 + tok) * a.q_stride + (size_t)(I.h * G + (f - tok * G)) * HD + V * c;
+            if (vec) {
+                raw[p] = *reinterpret_cast<const uint4 *>(src);
+            } else {
+                __align__(16) T v[V];
 #pragma unroll
-            for (int k = 0; k < (int)(8 * sizeof(T)) / 16; ++k)
-                reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(src + 8 * c)[k];
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = src[8 * c + e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = pg_ld<T>(v + e);
-    };
-    float top = 0.f;
-    bool odd = false;
-#pragma unroll 4
-    for (int c = 0; c < HD / 8; ++c) {
-        float x[8];
-        load8(c, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            top = fmaxf(top, fabsf(x[e]));
-            odd |= !(fabsf(x[e]) <= 3.4028235e38f);
+                for (int e = 0; e < V; ++e) v[e] = src[e];
+                raw[p] = *reinterpret_cast<uint4 *>(v);
+            }
         }
     }
-    // an infinite or NaN query: the row is NaN, and so are its scores
-    const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 253);
     const float scale = a.scale != 0.f ? a.scale : 1.f / sqrtf((float)HD);
-    const float up = odd ? NAN : copysignf(__uint_as_float((uint32_t)(268 - ex) << 23), scale);
-    // (a factor too small for fp32 still has to leave -infinity as it is)
-    const float down = fmaxf(__uint_as_float((uint32_t)(ex - 14) << 23) * (fabsf(scale) * 1.4426950408889634f), 1.2e-38f);
-    dst += r * 128;
-#pragma unroll 4
-    for (int c = 0; c < HD / 8; ++c) {
-        float x[8];
-        load8(c, x);
-        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+    for (int p = 0; p < PASSES; ++p) {
+        const int r = row0 + p * RPP + lane / LPR;
+        __align__(16) T v[V];
+        *reinterpret_cast<uint4 *>(v) = raw[p];
+        float x[V];
+        uint32_t top = 0;  // the largest magnitude's bits; an infinity's or a NaN's are above every number's
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            x[e] = pg_ld<T>(v + e);
+            top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+        }
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // an infinite or NaN query: the row is NaN, and so are its scores
+        const int ex = min(max((int)(top >> 23), 15), 253);
+        const float up = top >= 0x7F800000u ? NAN : copysignf(__uint_as_float((uint32_t)(268 - ex) << 23), scale);
+        uint32_t hi[V / 2];
+        [[maybe_unused]] uint32_t lo[V / 2];
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {
             const float y0 = x[2 * k] * up, y1 = x[2 * k + 1] * up;
             hi[k] = pp_pack(y0, y1);
-            const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
-            lo[k] = pp_pack(y0 - z.x, y1 - z.y);
+            if constexpr (LO) {
+                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
+                lo[k] = pp_pack(y0 - z.x, y1 - z.y);
+            }
         }
-        uint8_t *d = dst + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if constexpr (LO) *reinterpret_cast<uint4 *>(d + C::OP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const int ch = V * c / 8;  // 16 bytes of the operand
+        uint8_t *d = dst + r * 128 + (ch >> 3) * 16384 + (((ch & 7) ^ (r & 7)) << 4);
+        if constexpr (V == 8) {
+            *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[V / 2 - 2], hi[V / 2 - 1]);
+        } else {
+            *reinterpret_cast<uint2 *>(d + 8 * (c & 1)) = make_uint2(hi[0], hi[1]);
+            if constexpr (LO) *reinterpret_cast<uint2 *>(d + C::OP + 8 * (c & 1)) = make_uint2(lo[0], lo[1]);
+        }
+        // (a factor too small for fp32 still has to leave -infinity as it is)
+        if (c == 0)
+            down[r] = fmaxf(__uint_as_float((uint32_t)(ex - 14) << 23) * (fabsf(scale) * 1.4426950408889634f), 1.2e-38f);
     }
-    return down;
+    static_assert(!LO || V == 4, "only fp32 rows have lo halves");
 }
 
 // ---- operands (warps 8-11).  Half block i of the walk (block i / 2) lies in ring slot i % PP_RAW; warps 8, 9 use the first
@@ -516,7 +529,8 @@ ER_DEV void pp_copies(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem &I
 }
 
 // barriers (thread 0) and the whole of TMEM (warp 12)
-ER_DEV void pp_setup(PpBars &B, int tid, int warp, int softmax_warps) {
+// query_warps, softmax_warps: warps that make the queries' operands, and that share a tile's P
+ER_DEV void pp_setup(PpBars &B, int tid, int warp, int query_warps, int softmax_warps) {
     if (tid == 0) {
         for (int i = 0; i < PP_RAW; ++i) {
             mbar_init(B.raw + i, 1);
@@ -533,6 +547,7 @@ ER_DEV void pp_setup(PpBars &B, int tid, int warp, int softmax_warps) {
             mbar_init(B.oempty + i, 8);
             mbar_init(B.x + i, 8);
         }
+        mbar_init(&B.q, query_warps);
         fence_mbar_init();
     }
     if (warp == 12) {
@@ -540,6 +555,9 @@ ER_DEV void pp_setup(PpBars &B, int tid, int warp, int softmax_warps) {
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    pp_fence_before();
+    __syncthreads();
+    pp_fence_after();
 }
 ER_DEV void pp_close(PpBars &B, int warp) {
     __syncwarp();
@@ -642,20 +660,11 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
     PpItem I;
     if (!pp_find<256>(P, B, warp, lane, I)) return;
     const int nx = I.nf > 128 ? 2 : 1;  // tiles
-    pp_setup(B, tid, warp, 4);
+    pp_setup(B, tid, warp, 4 * nx, 4);
     // a softmax thread's tile and row
     const int X = warp >> 2, r = tid & 127, f = I.f0 + X * 128 + r, tok = f / G;
     const int row = I.q0 + tok, head = I.h * G + (f - tok * G);
     const bool soft = warp < 8 && X < nx, real = X * 128 + r < I.nf;
-    float down = 0.f;
-    if (soft) {
-        down = pp_query<T, HD, false>(a, smem + C::OFF_Q + X * C::OP,
-                                      (const T *)a.q_dev + row * a.q_stride + (size_t)head * HD, real, r);
-        fence_proxy_async_smem();
-    }
-    pp_fence_before();
-    __syncthreads();
-    pp_fence_after();
     auto wait = [&](uint64_t *bar, uint32_t par) { return pp_wait(P, bar, par, lane); };
 
     if (warp < 8) {
@@ -666,6 +675,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
             const int pos = real ? max(I.past + tok, -1) : 2147483647;  // rows past the last are computed (from zeros) and dropped
             const int first = a.window && real ? max(0, pos - a.window + 1) : 0;
             float m = PP_NONE, l = 0.f;
+            float *rows = reinterpret_cast<float *>(smem + C::OFF_ROWS) + X * 128;
+            pp_queries<T, HD, false, 32>(a, I, G, smem + C::OFF_Q + X * C::OP, rows, I.f0 + X * 128, I.nf - X * 128,
+                                         32 * (warp & 3), lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) pp_arrive(&B.q);
+            const float down = rows[r];
             bool ok = true;
             for (int j = 0; j < I.nblk; ++j) {
                 ok = wait(B.s + X, j & 1);
@@ -727,7 +743,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
         if (warp == 12 && I.nblk > 0) {
             const uint32_t qb = smem_u32(smem + C::OFF_Q), kb = smem_u32(smem + C::OFF_K), vb = smem_u32(smem + C::OFF_V);
             const uint32_t one = pp_elect();
-            bool ok = wait(B.kfull + 0, 0);
+            bool ok = wait(&B.q, 0) && wait(B.kfull + 0, 0);
             if (ok) {
                 pp_fence_after();
                 for (int x = 0; x < nx; ++x) {
@@ -781,24 +797,12 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
     const int G = a.n_heads / P.p.KV;
     PpItem I;
     if (!pp_find<128>(P, B, warp, lane, I)) return;
-    pp_setup(B, tid, warp, 8);
+    pp_setup(B, tid, warp, 8, 8);
     // warps 0-3 and 4-7: thread = query row, W = which half of its columns
     const int r = tid & 127, W = warp >> 2, f = I.f0 + r, tok = f / G;
     const int row = I.q0 + tok, head = I.h * G + (f - tok * G);
     const bool real = r < I.nf;
     float *xch = reinterpret_cast<float *>(smem + C::OFF_ROWS);  // [2 blocks][2 halves][128]
-    float down = 0.f;
-    if (warp < 4) {
-        down = pp_query<float, HD, true>(a, smem + C::OFF_Q,
-                                         (const float *)a.q_dev + row * a.q_stride + (size_t)head * HD, real, r);
-        xch[r] = down;
-        fence_proxy_async_smem();
-    }
-    pp_fence_before();
-    __syncthreads();
-    pp_fence_after();
-    if (warp >= 4 && warp < 8) down = xch[r];
-    __syncthreads();
     auto wait = [&](uint64_t *bar, uint32_t par) { return pp_wait(P, bar, par, lane); };
     const uint32_t tl = PP_TMEM + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
 
@@ -811,7 +815,14 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
         float o[HO];
 #pragma unroll
         for (int e = 0; e < HO; ++e) o[e] = 0.f;
-        bool ok = true;
+        // the queries, 16 rows a warp; the factors lie where block 1's exchange will be (nobody gets there before both of a
+        // row's threads have read them)
+        pp_queries<float, HD, true, 16>(a, I, G, smem + C::OFF_Q, xch + 256, I.f0, I.nf, 32 * (warp & 3) + 16 * W, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) pp_arrive(&B.q);
+        bool ok = wait(&B.q, 0);
+        const float down = xch[256 + r];
         auto gather = [&](int j) {  // o = o * factor + O of block j
             const int buf = j & 1;
             if (!wait(B.o + buf, (j >> 1) & 1)) return false;
@@ -833,7 +844,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             if (lane == 0) pp_arrive(B.oempty + buf);
             return true;
         };
-        for (int j = 0; j < I.nblk; ++j) {
+        for (int j = 0; ok && j < I.nblk; ++j) {
             const int buf = j & 1, ph = (j >> 1) & 1;
             ok = wait(B.s + buf, ph);
             if (!ok) break;
@@ -902,7 +913,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
                 pp_commit(B.s + st, one);
                 pp_commit(B.kempty + st, one);
             };
-            bool ok = true;
+            bool ok = wait(&B.q, 0);
             for (int j = 0; ok && j < min(2, I.nblk); ++j) {
                 ok = wait(B.kfull + j, 0);
                 if (!ok) break;
