@@ -15,12 +15,17 @@
 //   O starts from 0 and is added to sums in registers, rounded to nearest.
 //     warps 0-3, 4-7  two threads a row, one for either half of the columns of S and of O: softmax, as above, with the
 //                     row's largest score exchanged through shared memory; then o = o * factor + the last block's O.
-//                     (One thread a row is bound by its own latency: 212 us against 167 for 4 x 500 tokens.)
+//                     (One thread a row is bound by its own latency: 212 us against 167 for 4 x 500 tokens.  For 16-bit rows, where two
+//                     tiles take turns, two threads a row cost more than they gave: 546 us against 492 for 8192 tokens.)
 //     warp 12         S of the block after next goes to the buffer whose P is used up, so the softmax never waits for it
 //     TMEM: two buffers of S/P, two of a block's O.
 //   Both: warps 8-11 turn codes into fp16 operands in shared memory, exactly (pages.cuh), K and V K-major with the
 //   128-byte swizzle, two stages each; warp 13 requests the cached tiles: bulk copies into a ring of half blocks, each
 //   used by two operand warps.
+//
+// Registers (the launch's 128 a thread, shared out anew: 2 softmax + operands + rest = 512).  16 bits: 208, 48, 48 hold everything;
+// a spill in any role delays the others (8192 bf16 tokens: 433 us; 200, 80, 32: 485; 208, 64, 32: 460; 200, 64, 48: 446).
+// fp32: 200, 64, 48 (4 x 500 tokens: 134 us; 200, 80, 32: 138).
 //
 // The block's rows are put in the order k' = 32 a + 8 t + 4 b + 2 i + e for row 32 a + 16 b + 8 i + 2 t + e, in K's rows,
 // hence S's and P's columns, and in V's K dimension: so a thread that holds a code word of V of two 16-row tiles
@@ -69,7 +74,7 @@ struct PpArgs {
 struct PpBars {
     uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], oempty[2], x[2], q;
     uint32_t tmem;
-    int item[4];  // sequence, first query row, KV head, found
+    int item[6];  // sequence, first query row, KV head, found, first row of q, query rows
 };
 static_assert(sizeof(PpBars) <= 512, "barriers");
 
@@ -254,6 +259,10 @@ ER_DEV bool pp_find(const PpArgs &P, PpBars &B, int warp, int lane, PpItem &I) {
     const int qn = a.q_start_dev[I.b + 1] - I.q0;
     I.past = a.lens_dev[I.b] - qn;
     I.nf = (int)min((long long)qn * G - I.f0, (long long)ROWS);
+    if (threadIdx.x == 0) {
+        B.item[4] = I.q0;
+        B.item[5] = I.nf;
+    }
     I.any_hi = I.past + (I.f0 + I.nf - 1) / G;
     I.any_lo = pg_first(I.past + I.f0 / G, a.window);
     I.base = I.any_lo & ~15;
@@ -271,41 +280,47 @@ ER_DEV bool pp_wait(const PpArgs &P, uint64_t *bar, uint32_t par, int lane) {
     return ok;
 }
 
-// NR query rows, row0 .. of the tile that starts at query row f0 (nf of its rows are real, the others zeros), as rows of the
-// K-major operand at dst.  A row is times a power of two that brings its largest value to [2^14, 2^15) (and the scale's
-// sign); LO: the lo halves go to dst + OP.  down[row]: the factor that takes its scores to log2 units.  16 bytes of a row a
-// lane, every row's loads in flight together (a thread a row, four loads at a time, took 20,000 cycles of a CTA; this
-// takes less than the first block's way through the ring).
+ER_DEV const uint8_t *pp_shfl(const uint8_t *p, int lane) {
+    return reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, (unsigned long long)p, lane));
+}
+
+// NR query rows as rows row0 .. of the K-major operand at dst: lane i < NR knows row row0 + i's address, or NULL (zeros).
+// A row is times a power of two that brings its largest value to [2^14, 2^15) (and the scale's sign); LO: the lo halves go
+// to dst + OP.  down[row]: the factor that takes its scores to log2 units.
+// Neighbouring lanes take 16 bytes each of a row, first as they are to places of its operand (every row on its way at
+// once, in no registers), then from there, row by row, into the operand.  A thread a row and four loads at a time took
+// 20,000 cycles of a CTA.
 template <class T, int HD, bool LO, int NR>
-ER_DEV void pp_queries(const er_pages_attention_args &a, const PpItem &I, int G, uint8_t *dst, float *down, int f0, int nf, int row0,
-                       int lane) {
+ER_DEV void pp_queries(const er_pages_attention_args &a, uint8_t *dst, float *down, const T *mine, int row0, int lane) {
     using C = PpCfg<HD>;
-    constexpr int LPR = HD * (int)sizeof(T) / 16, RPP = 32 / LPR, PASSES = NR / RPP, V = 16 / (int)sizeof(T);
+    constexpr int LPR = HD * (int)sizeof(T) / 16, RPP = 32 / LPR, V = 16 / (int)sizeof(T);
+    constexpr int HALF = HD / 8;  // 16-byte places of a row of one operand
     const bool vec = ((uintptr_t)a.q_dev & 15) == 0 && (a.q_stride * sizeof(T)) % 16 == 0;
     const int c = lane % LPR;  // values V c .. of the row
-    uint4 raw[PASSES];
+    auto place = [&](int r, int ch) { return dst + r * 128 + (ch >> 3) * 16384 + (((ch & 7) ^ (r & 7)) << 4); };
+    auto raw_at = [&](int r) { return place(r, c & (HALF - 1)) + (c / HALF) * C::OP; };
+#pragma unroll 1
+    for (int p = 0; p < NR; p += RPP) {
+        const int i = p + lane / LPR;
+        const uint8_t *src = pp_shfl(reinterpret_cast<const uint8_t *>(mine), i);
+        uint8_t *to = raw_at(row0 + i);
+        if (vec) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)),
+                         "l"(src ? src + 16 * c : (const uint8_t *)a.q_dev), "r"(src ? 16 : 0)
+                         : "memory");
+        } else {
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-        const int r = row0 + p * RPP + lane / LPR, f = f0 + r, tok = f / G;
-        raw[p] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < nf) {
-            const T *src = (const T *)a.q_dev + (I.q0 + tok) * a.q_stride + (size_t)(I.h * G + (f - tok * G)) * HD + V * c;
-            if (vec) {
-                raw[p] = *reinterpret_cast<const uint4 *>(src);
-            } else {
-                __align__(16) T v[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[e] = src[e];
-                raw[p] = *reinterpret_cast<uint4 *>(v);
-            }
+            for (int e = 0; e < V; ++e)
+                reinterpret_cast<T *>(to)[e] = src ? reinterpret_cast<const T *>(src)[V * c + e] : pg_cvt<T>(0.f);
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     const float scale = a.scale != 0.f ? a.scale : 1.f / sqrtf((float)HD);
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-        const int r = row0 + p * RPP + lane / LPR;
+#pragma unroll 2
+    for (int p = 0; p < NR; p += RPP) {
+        const int r = row0 + p + lane / LPR;
         __align__(16) T v[V];
-        *reinterpret_cast<uint4 *>(v) = raw[p];
+        *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(raw_at(r));
         float x[V];
         uint32_t top = 0;  // the largest magnitude's bits; an infinity's or a NaN's are above every number's
 #pragma unroll
@@ -315,6 +330,7 @@ ER_DEV void pp_queries(const er_pages_attention_args &a, const PpItem &I, int G,
         }
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        __syncwarp();  // the row is read: its places may be written
         // an infinite or NaN query: the row is NaN, and so are its scores
         const int ex = min(max((int)(top >> 23), 15), 253);
         const float up = top >= 0x7F800000u ? NAN : copysignf(__uint_as_float((uint32_t)(268 - ex) << 23), scale);
@@ -329,8 +345,7 @@ ER_DEV void pp_queries(const er_pages_attention_args &a, const PpItem &I, int G,
                 lo[k] = pp_pack(y0 - z.x, y1 - z.y);
             }
         }
-        const int ch = V * c / 8;  // 16 bytes of the operand
-        uint8_t *d = dst + r * 128 + (ch >> 3) * 16384 + (((ch & 7) ^ (r & 7)) << 4);
+        uint8_t *d = place(r, V * c / 8);
         if constexpr (V == 8) {
             *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[V / 2 - 2], hi[V / 2 - 1]);
         } else {
@@ -341,7 +356,7 @@ ER_DEV void pp_queries(const er_pages_attention_args &a, const PpItem &I, int G,
         if (c == 0)
             down[r] = fmaxf(__uint_as_float((uint32_t)(ex - 14) << 23) * (fabsf(scale) * 1.4426950408889634f), 1.2e-38f);
     }
-    static_assert(!LO || V == 4, "only fp32 rows have lo halves");
+    static_assert(LO == (V == 4), "fp32 rows have lo halves");
 }
 
 // ---- operands (warps 8-11).  Half block i of the walk (block i / 2) lies in ring slot i % PP_RAW; warps 8, 9 use the first
@@ -629,19 +644,37 @@ ER_DEV float pp_probabilities(const float (&s)[N], uint32_t tP, float down, floa
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
-// 32 values of an output row
-template <class T>
-ER_DEV void pp_store(const er_pages_attention_args &a, T *out, const float *o, float l, float inv) {
+// N = 2 HD / sizeof(T) values of an output row a thread, columns tO .. of TMEM or (tO = NONE) o, times inv, to `mine` (NULL: not
+// a real row).  Through shared memory (`stage`: 2 HD bytes a row, the warp's own place in the queries, which nothing reads any
+// more), so that neighbouring lanes write a row: a thread a row takes a cycle a 16-byte piece.
+template <class T, int HD, class Load>
+ER_DEV void pp_store(const er_pages_attention_args &a, uint8_t *stage, T *mine, int lane, Load load) {
+    constexpr int N = 2 * HD / (int)sizeof(T), ROW = 2 * HD, LPR = ROW / 16, V = 16 / (int)sizeof(T);
     const bool vec = ((uintptr_t)a.out_dev & 15) == 0 && (a.out_stride * sizeof(T)) % 16 == 0;
-    __align__(16) T v[32];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = pg_cvt<T>(l == 0.f ? 0.f : o[e] * inv);
-    if (vec) {
+    for (int k = 0; k < N / 32; ++k) {
+        float o[32];
+        load(k, o);
+        __align__(16) T v[32];
 #pragma unroll
-        for (int e = 0; e < (int)(32 * sizeof(T)) / 16; ++e) reinterpret_cast<uint4 *>(out)[e] = reinterpret_cast<uint4 *>(v)[e];
-    } else {
+        for (int e = 0; e < 32; ++e) v[e] = pg_cvt<T>(o[e]);
+        if (vec) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) out[e] = v[e];
+            for (int e = 0; e < 32 / V; ++e)
+                *reinterpret_cast<uint4 *>(stage + lane * ROW + (((32 / V * k + e) ^ (lane & 7)) << 4)) = reinterpret_cast<uint4 *>(v)[e];
+        } else if (mine) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mine[32 * k + e] = v[e];
+        }
+    }
+    if (!vec) return;
+    __syncwarp();
+    const int c = lane % LPR;
+#pragma unroll 4
+    for (int p = 0; p < 32; p += 32 / LPR) {
+        const int i = p + lane / LPR;
+        const uint8_t *dst = pp_shfl(reinterpret_cast<const uint8_t *>(mine), i);
+        if (dst) const_cast<uint4 *>(reinterpret_cast<const uint4 *>(dst))[c] = *reinterpret_cast<const uint4 *>(stage + i * ROW + ((c ^ (i & 7)) << 4));
     }
 }
 ER_DEV float pp_lse(float m, float l) { return l == 0.f ? -INFINITY : (m - PP_UP + log2f(l)) * 0.6931471805599453f; }
@@ -668,7 +701,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
     auto wait = [&](uint64_t *bar, uint32_t par) { return pp_wait(P, bar, par, lane); };
 
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         if (soft) {
             const uint32_t tl = PP_TMEM + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
             const uint32_t tS = tl + X * 128, tO = tl + 256 + X * HD;
@@ -676,7 +709,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
             const int first = a.window && real ? max(0, pos - a.window + 1) : 0;
             float m = PP_NONE, l = 0.f;
             float *rows = reinterpret_cast<float *>(smem + C::OFF_ROWS) + X * 128;
-            pp_queries<T, HD, false, 32>(a, I, G, smem + C::OFF_Q + X * C::OP, rows, I.f0 + X * 128, I.nf - X * 128,
+            pp_queries<T, HD, false, 32>(a, smem + C::OFF_Q + X * C::OP, rows,
+                                         real ? (const T *)a.q_dev + row * a.q_stride + (size_t)head * HD : nullptr,
                                          32 * (warp & 3), lane);
             fence_proxy_async_smem();
             __syncwarp();
@@ -718,28 +752,31 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 __syncwarp();
                 if (lane == 0) pp_arrive(B.p + X);
             }
-            if (ok && I.nblk > 0) ok = wait(B.o + X, 0);
+            if (ok) ok = I.nblk > 0 ? wait(B.o + X, 0) : wait(&B.q, 0);  // the queries' place is free
             if (ok) {
                 pp_fence_after();
-                T *out = (T *)a.out_dev + row * a.out_stride + (size_t)head * HD;
                 const float inv = 1.f / l;
-#pragma unroll 1
-                for (int k = 0; k < HD / 32; ++k) {
-                    float o[32];
-                    if (I.nblk > 0) {
-                        pp_ld32(tO + 32 * k, o);
-                        pp_wait_ld(o);
-                    }
-                    if (real) pp_store<T>(a, out + 32 * k, o, l, inv);
-                }
+                // the row once more, from shared memory: it would cost registers in the loop
+                const volatile int *item = B.item;
+                const int f = item[1] + X * 128 + r, tok = f / G, row = item[4] + tok, head = item[2] * G + (f - tok * G);
+                const bool real = X * 128 + r < item[5];
+                pp_store<T, HD>(a, smem + C::OFF_Q + warp * (64 * HD), real ? (T *)a.out_dev + row * a.out_stride + (size_t)head * HD : nullptr,
+                                lane, [&](int k, float (&o)[32]) {
+                                    if (I.nblk > 0) {
+                                        pp_ld32(tO + 32 * k, o);
+                                        pp_wait_ld(o);
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+                                });
                 if (real && a.lse_dev) a.lse_dev[(size_t)row * a.n_heads + head] = pp_lse(m, l);
             }
         }
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         pp_operands<HD>(P, B, smem, I, warp, lane);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 12 && I.nblk > 0) {
             const uint32_t qb = smem_u32(smem + C::OFF_Q), kb = smem_u32(smem + C::OFF_K), vb = smem_u32(smem + C::OFF_V);
             const uint32_t one = pp_elect();
@@ -817,7 +854,11 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
         for (int e = 0; e < HO; ++e) o[e] = 0.f;
         // the queries, 16 rows a warp; the factors lie where block 1's exchange will be (nobody gets there before both of a
         // row's threads have read them)
-        pp_queries<float, HD, true, 16>(a, I, G, smem + C::OFF_Q, xch + 256, I.f0, I.nf, 32 * (warp & 3) + 16 * W, lane);
+        const int row0 = 32 * (warp & 3) + 16 * W, fq = I.f0 + row0 + (lane & 15), tq = fq / G;
+        pp_queries<float, HD, true, 16>(a, smem + C::OFF_Q, xch + 256,
+                                        row0 + (lane & 15) < I.nf ? (const float *)a.q_dev + (I.q0 + tq) * a.q_stride +
+                                                                        (size_t)(I.h * G + (fq - tq * G)) * HD : nullptr,
+                                        row0, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) pp_arrive(&B.q);
@@ -890,19 +931,22 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             if (lane == 0) pp_arrive(B.x + buf);
             ok = wait(B.x + buf, (I.nblk >> 1) & 1);
         }
-        if (ok && real) {
+        if (ok) {
             l += xch[(I.nblk & 1) * 256 + (W ^ 1) * 128 + r];
             const float inv = 1.f / l;
-            float *out = (float *)a.out_dev + row * a.out_stride + (size_t)head * HD + W * HO;
+            pp_store<float, HD>(a, smem + C::OFF_Q + warp * (64 * HD),
+                                real ? (float *)a.out_dev + row * a.out_stride + (size_t)head * HD + W * HO : nullptr, lane,
+                                [&](int k, float (&y)[32]) {
 #pragma unroll
-            for (int k = 0; k < HO / 32; ++k) pp_store<float>(a, out + 32 * k, o + 32 * k, l, inv);
-            if (a.lse_dev && W == 0) a.lse_dev[(size_t)row * a.n_heads + head] = pp_lse(m, l);
+                                    for (int e = 0; e < 32; ++e) y[e] = l == 0.f ? 0.f : o[32 * k + e] * inv;
+                                });
+            if (a.lse_dev && W == 0 && real) a.lse_dev[(size_t)row * a.n_heads + head] = pp_lse(m, l);
         }
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         pp_operands<HD>(P, B, smem, I, warp, lane);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 12 && I.nblk > 0) {
             const uint32_t qb = smem_u32(smem + C::OFF_Q), kb = smem_u32(smem + C::OFF_K), vb = smem_u32(smem + C::OFF_V);
             const uint32_t one = pp_elect();
