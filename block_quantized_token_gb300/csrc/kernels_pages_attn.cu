@@ -5,7 +5,10 @@
 // rescale).
 //
 // What bounds it: the cache's bytes (18 / 32 a value); next, instructions, two a value to turn codes into operands
-// and feed the tensor cores, so a tile's codes are laid out as the operands take them.
+// and feed the tensor cores, so a tile's codes are laid out as the operands take them.  Measured, 16 sequences of 8192 rows,
+// 32 / 8 heads of 128: bf16 47.6 us (3.2 TB/s of cache, 0.48 of a copy's rate), fp32 62 us; about a quarter of that is the
+// way to the first tile and the joining of states, the rest the loop at half the SM's issue rate (long chains of
+// dependent products and exponentials in 2 or 3 warps a scheduler).
 //
 // Work split.  A unit is a (sequence, group of 8 query rows, KV head); a query row is a (token, head of the KV
 // head's group).  The 16-row tiles that the units attend form one list in order of unit; CTA c of C takes the

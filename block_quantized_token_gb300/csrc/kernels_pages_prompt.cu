@@ -15,24 +15,28 @@
 //   O starts from 0 and is added to sums in registers, rounded to nearest.
 //     warps 0-3, 4-7  two threads a row, one for either half of the columns of S and of O: softmax, as above, with the
 //                     row's largest score exchanged through shared memory; then o = o * factor + the last block's O.
-//                     (One thread a row is bound by its own latency: 212 us against 167 for 4 x 500 tokens.  For 16-bit rows, where two
-//                     tiles take turns, two threads a row cost more than they gave: 546 us against 492 for 8192 tokens.)
+//                     (One thread a row is bound by its own latency: 212 us against 167 for 4 x 500 tokens.  For 16-bit
+//                     rows, where two tiles take turns, two threads a row cost more than they gave: 546 us against 492
+//                     for 8192 tokens.)
 //     warp 12         S of the block after next goes to the buffer whose P is used up, so the softmax never waits for it
 //     TMEM: two buffers of S/P, two of a block's O.
 //   Both: warps 8-11 turn codes into fp16 operands in shared memory, exactly (pages.cuh), K and V K-major with the
 //   128-byte swizzle, two stages each; warp 13 requests the cached tiles: bulk copies into a ring of half blocks, each
 //   used by two operand warps.
 //
-// Registers (the launch's 128 a thread, shared out anew: 2 softmax + operands + rest = 512).  16 bits: 208, 48, 48 hold everything;
-// a spill in any role delays the others (8192 bf16 tokens: 433 us; 200, 80, 32: 485; 208, 64, 32: 460; 200, 64, 48: 446).
+// Registers (the launch's 128 a thread, shared out anew: 2 softmax + operands + rest = 512).  16 bits: 208, 48, 48 hold
+// everything; a spill in any role delays the others (8192 bf16 tokens: 433 us; 200, 80, 32: 485; 208, 64, 32: 460; 200, 64,
+// 48: 446).
 // fp32: 200, 64, 48 (4 x 500 tokens: 134 us; 200, 80, 32: 138).
 //
 // The block's rows are put in the order k' = 32 a + 8 t + 4 b + 2 i + e for row 32 a + 16 b + 8 i + 2 t + e, in K's rows,
 // hence S's and P's columns, and in V's K dimension: so a thread that holds a code word of V of two 16-row tiles
 // holds 16 bytes of the operand.
 //
-// What bounds it: the products (2 x 1024 cycles a block and two tiles at HD = 128, 2048 a block for fp32) and the
-// softmax's latency between them.
+// What bounds it: shared memory's reads by the products and writes of their operands (2048 cycles a block and two tiles at
+// HD = 128, as many a block for fp32), and what the softmax and its hand-overs add to that (together about 3000 cycles).
+// Measured: 8192 bf16 tokens, 32 / 8 heads of 128: 433 us = 1.27 PFLOP/s, 0.66 of the library's matrix product; 4 x
+// 300..500 fp32 tokens over 900..4100 rows: 134 us.
 //
 // Masks.  Blocks that some row attends only in part mask S; there, rows of V that no row of the CTA attends are
 // zeroed (they may hold anything), and a NaN value of V is carried by K instead, so only rows that attend it see it.
@@ -644,8 +648,7 @@ ER_DEV float pp_probabilities(const float (&s)[N], uint32_t tP, float down, floa
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
-// N = 2 HD / sizeof(T) values of an output row a thread, columns tO .. of TMEM or (tO = NONE) o, times inv, to `mine` (NULL: not
-// a real row).  Through shared memory (`stage`: 2 HD bytes a row, the warp's own place in the queries, which nothing reads any
+// N = 2 HD / sizeof(T) values of an output row a thread, 32 at a time from `load`, to `mine` (NULL: not a real row).  Through shared memory (`stage`: 2 HD bytes a row, the warp's own place in the queries, which nothing reads any
 // more), so that neighbouring lanes write a row: a thread a row takes a cycle a 16-byte piece.
 template <class T, int HD, class Load>
 ER_DEV void pp_store(const er_pages_attention_args &a, uint8_t *stage, T *mine, int lane, Load load) {

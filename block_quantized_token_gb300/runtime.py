@@ -165,6 +165,10 @@ _ROW_TYPES = {torch.float32: er.ER_F32, torch.float16: er.ER_F16, torch.bfloat16
 _ROPE_STYLES = {"pairs": er.ER_ROPE_PAIRS, "halves": er.ER_ROPE_HALVES}
 
 
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
 def rope_table(head_dim: int, base: float, n_positions: int, device: str = "cuda") -> torch.Tensor:
     """(cos, sin) of p * base^(-2 i / head_dim), fp32 [n_positions, head_dim / 2, 2], made on the device."""
     out = torch.empty((n_positions, head_dim // 2, 2), dtype=torch.float32, device=device)
@@ -190,29 +194,32 @@ class PagedCache:
             pool = torch.empty(need, dtype=torch.uint8, device=device)
         if not pool.is_cuda or not pool.is_contiguous() or pool.numel() * pool.element_size() != need:
             raise ValueError(f"pool must be a dense CUDA tensor of {need} bytes")
-        self.pool, self.device = pool, pool.device
+        self.pool, self.device, self._index = pool, pool.device, pool.get_device()
         with torch.cuda.device(self.device):
             self.handle = er.er_pages_create(self.cfg, pool.data_ptr())
 
+    # The checks below stand before calls that take the GPU 6 us, so they ask each tensor as little as they can (a
+    # device's index and a raw stream cost a tenth of the device and stream objects).
     def _stream(self, stream: int | None) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
+        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream
 
     def _ints(self, n: int, *tensors: torch.Tensor) -> None:
         for t in tensors:
-            if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n or t.device != self.device:
+            if t.dtype is not torch.int32 or t.get_device() != self._index or t.numel() < n or not t.is_contiguous():
                 raise ValueError(f"a dense int32 tensor of {n} values on {self.device} is needed")
 
     def _rows(self, x: torch.Tensor, n: int, heads: int | None, dtype: torch.dtype | None) -> int:
         """Checks row tensors [n, heads, head_dim]; returns the stride between tokens."""
-        if x.dim() != 3 or x.shape[2] != self.head_dim or (heads is not None and x.shape[1] != heads):
+        shape = x.shape
+        if len(shape) != 3 or shape[2] != self.head_dim or (heads is not None and shape[1] != heads):
             raise ValueError(f"rows must be [tokens, heads, {self.head_dim}]")
-        st = x.stride()
-        if x.shape[0] < n or x.device != self.device or (dtype is not None and x.dtype != dtype) or st[2] != 1 or \
-                (x.shape[1] > 1 and st[1] != self.head_dim):
+        s0, s1, s2 = x.stride()
+        if shape[0] < n or x.get_device() != self._index or (dtype is not None and x.dtype is not dtype) or s2 != 1 or \
+                (s1 != self.head_dim and shape[1] > 1):
             raise ValueError(f"rows must be {n} dense heads' rows of one type on {self.device}")
-        if x.dtype not in _ROW_TYPES:
+        if dtype is None and x.dtype not in _ROW_TYPES:
             raise ValueError("rows must be float32, float16 or bfloat16")
-        return st[0] if x.shape[0] > 1 else x.shape[1] * self.head_dim
+        return s0 if shape[0] > 1 else shape[1] * self.head_dim
 
     def _table(self, tables: torch.Tensor, n_seqs: int) -> int:
         self._ints(0, tables)
@@ -261,25 +268,21 @@ class PagedCache:
             qs, os_ = self._rows(q, n, heads, k.dtype), self._rows(q_out, n, heads, k.dtype)
         self._ints(n, slots)
         for g in (q_gain, k_gain):
-            if g is not None and (g.dtype != torch.float32 or g.numel() != hd or not g.is_contiguous() or
-                                  g.device != self.device):
+            if g is not None and (g.dtype is not torch.float32 or g.numel() != hd or not g.is_contiguous() or
+                                  g.get_device() != self._index):
                 raise ValueError(f"a gain must be {hd} float32 values")
         if rope is not None:
-            if rope.dtype != torch.float32 or not rope.is_contiguous() or rope.device != self.device or \
-                    rope.dim() != 3 or tuple(rope.shape[1:]) != (hd // 2, 2):
+            if rope.dtype is not torch.float32 or not rope.is_contiguous() or rope.get_device() != self._index or \
+                    rope.dim() != 3 or rope.shape[1] != hd // 2 or rope.shape[2] != 2:
                 raise ValueError(f"the rope table must be float32 [positions, {hd // 2}, 2]")
             if positions is None:
                 raise ValueError("a rope table needs positions")
             self._ints(n, positions)
         if rope_style not in _ROPE_STYLES:
             raise ValueError(f"rope_style must be one of {sorted(_ROPE_STYLES)}")
-
-        def ptr(t):
-            return None if t is None else t.data_ptr()
-
         a = er.er_pages_append_args(n, heads, _ROW_TYPES[k.dtype], _ROPE_STYLES[rope_style],
-                                    0 if rope is None else rope.shape[0], ptr(q), k.data_ptr(), v.data_ptr(), ptr(q_out),
-                                    qs, ks, vs, os_, ptr(q_gain), ptr(k_gain), ptr(rope),
+                                    0 if rope is None else rope.shape[0], _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out),
+                                    qs, ks, vs, os_, _ptr(q_gain), _ptr(k_gain), _ptr(rope),
                                     None if rope is None else positions.data_ptr(), slots.data_ptr(), eps)
         er.er_pages_append(self.handle, layer, a, self._stream(stream))
 
@@ -298,8 +301,7 @@ class PagedCache:
         if dtype is None:
             return
         er.er_pages_read(self.handle, layer, n, slots.data_ptr(), _ROW_TYPES[dtype],
-                         None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
-                         self._stream(stream))
+                         _ptr(k_out), _ptr(v_out), self._stream(stream))
 
     def attention(self, layer: int, q: torch.Tensor, out: torch.Tensor, q_start: torch.Tensor, lens: torch.Tensor,
                   tables: torch.Tensor, scale: float = 0.0, window: int = 0, lse: torch.Tensor | None = None,
@@ -310,11 +312,11 @@ class PagedCache:
         qs, os_ = self._rows(q, n, heads, None), self._rows(out, n, heads, q.dtype)
         self._ints(seqs, lens)
         self._ints(seqs + 1, q_start)
-        if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != self.device or
+        if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != self._index or
                                 lse.numel() < n * heads):
             raise ValueError("lse must be dense float32 [tokens, heads]")
         a = er.er_pages_attention_args(seqs, n, heads, _ROW_TYPES[q.dtype], self._table(tables, seqs), window,
-                                       q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), qs, os_,
+                                       q.data_ptr(), out.data_ptr(), _ptr(lse), qs, os_,
                                        q_start.data_ptr(), lens.data_ptr(), tables.data_ptr(), scale)
         er.er_pages_attention(self.handle, layer, a, self._stream(stream))
 
