@@ -14,7 +14,7 @@ namespace er {
 // need_b = ceil((len_b + new_b) / R) - ceil(len_b / R) pages; the first page given to b is number
 // P_b = sum_{i<b} need_i, its first token row T_b = sum_{i<b} new_i, both over the admitted prefix.  Every block scans all the
 // requests (4 ints each) and writes its share of tables and slots, so one launch does.  A few KB: latency bounds it (two
-// dependent global reads, a scan, a search; 16 requests 6.6 us, 512 prompts 8.5 us).
+// dependent global reads, a scan, a search; 16 requests as 512 prompts about 8.5 us).
 constexpr int PL_THREADS = 512;
 
 struct PlanShared {

@@ -990,3 +990,40 @@ def test_more_refusals():
     torch.cuda.synchronize()
     assert (x == 0).all() and (i == 0).all()
     fine(cache)
+
+
+@pytest.mark.parametrize("dtype,new", [("f32", 1), ("bf16", 1), ("f32", 60), ("bf16", 200)])
+def test_pool_past_4_gib(dtype, new):
+    """Pages and a layer whose bytes start past 32 bits: rows written, read and attended there as in a small pool."""
+    b = Batch([500, 260], [new, new], 8, 8, 128, 128, dtype, seed=43)
+    want, wz = b.run()
+    page_bytes = b.cache.pool.numel() // b.pages
+    pages = (9 << 29) // page_bytes  # 4.5 GiB a layer
+    big = paged(pages, 128, 8, 128, layers=2)
+    high = pages - b.pages
+    big.pool.view(2, pages, page_bytes)[1, high:].copy_(b.cache.pool.view(b.pages, page_bytes))
+    tables = ints(np.where(b.tables >= 0, b.tables + high, b.tables))
+    out, lse = torch.empty_like(want), torch.empty_like(wz)
+    big.attention(1, b.q, out, ints(b.start), ints(b.lens), tables, lse=lse)
+    assert torch.equal(out, want) and torch.equal(lse, wz)
+    rng = np.random.default_rng(44)
+    k, v = (make_rows(rng, 40, 8, 128, dtype) for _ in range(2))
+    slots = ints((pages - 1) * 128 + np.arange(60, 100))
+    big.append(1, None, k, v, None, slots)
+    small = paged(1, 128, 8, 128)
+    small.append(0, None, k, v, None, ints(np.arange(60, 100)))
+    got = [torch.empty((40, 8, 128), dtype=k.dtype, device="cuda") for _ in range(4)]
+    big.read(1, slots, *got[:2])
+    small.read(0, ints(np.arange(60, 100)), *got[2:])
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+    fine(big)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_among_many_idle_sequences(dtype):
+    """Fewer tokens than sequences, all of them one sequence's; and a padded batch whose rows end far before its tensors."""
+    b = Batch([40] * 75 + [300] + [0] * 74, [0] * 75 + [100] + [0] * 74, 16, 2, 64, 32, dtype, seed=45, tail=30)
+    b.check(*b.run())
+    b = Batch([70, 130, 9], [70, 3, 0], 4, 2, 128, 16, dtype, seed=46, tail=500)
+    b.check(*b.run())
+    fine(b.cache)
