@@ -23,10 +23,10 @@
 //
 // Arithmetic (mma.sync m16n8k16, fp32 sums), the cached side as the A operand, the 8 query rows as B's columns:
 //   S^T = K Q^T.  fp32 and fp16 queries: K's values as they are (fp16 numbers, pages.cuh), Q exact (fp16) or as hi + lo
-//         halves (fp32: 2^-22 of the row's largest).  bf16 queries: K's codes without scale or offset, 1024 + c and 64 +
-//         c as a mask leaves them (5 instructions for 8 codes against 14); the accumulator starts at minus the
-//         offsets' sum and the row's scale multiplies the block's sum.  That costs 2^-23 of 1032 sum |q|, 2^-15 of
-//         scale sum |q||k| at worst, where a bf16 output keeps 2^-9.
+//         halves (fp32: 2^-22 of the row's largest).  bf16 queries, exact too: K's codes c - 8 without their scale (9
+//         instructions for 8 codes against 14), and the row's scale multiplies the block's sum.  (With the offsets of 1032 and
+//         72 left in the codes and taken off the sums it is 5 instructions and the same time, but the error goes with sum
+//         |q| d, however small the values beside a block's largest are.)
 //   O^T += V^T P^T.  One code word is a lane's whole A operand, a mask and one FMA a pair, exact.  Probabilities go from
 //         the scores' layout to B's by movmatrix, as hi + lo halves (2^-22; bf16 outputs: hi alone, 2^-11).
 // Masks.  Tiles that some row of the unit attends only in part go through a path that masks scores and zeroes the
@@ -49,7 +49,7 @@ constexpr float PD_SLACK = 8.f;  // scores may pass m by this much
 constexpr float PD_NONE = -3e38f;  // m before any score
 
 template <class T>
-struct PdType;  // RAW: K enters as codes (bf16); QLO: queries have a lo half; PLO: probabilities have one
+struct PdType;  // RAW: K enters as codes c - 8 (bf16); QLO: queries have a lo half; PLO: probabilities have one
 template <>
 struct PdType<float> {
     static constexpr bool RAW = false, QLO = true, PLO = true;
@@ -126,6 +126,13 @@ template <int N>
 ER_DEV uint32_t pd_code(uint32_t w) {
     return lop3_and_or(N == 0 ? w << 6 : N == 1 ? w << 2 : N == 2 ? w >> 2 : w >> 6, 0x03C003C0u, 0x4C004C00u);
 }
+ER_DEV uint32_t h2_add(uint32_t a, uint32_t b) {
+    __half2 r = __hadd2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+    return *reinterpret_cast<uint32_t *>(&r);
+}
+// nibble 0 / 1 of each half of w as the fp16 pair c - 8: 1024 + c or 64 + c as a mask leaves it, less 1032 or 72
+ER_DEV uint32_t pd_low(uint32_t w) { return h2_add(lop3_and_or(w, 0x000F000Fu, 0x64006400u), 0xE408E408u); }
+ER_DEV uint32_t pd_high(uint32_t w) { return h2_add(lop3_and_or(w, 0x00F000F0u, 0x54005400u), 0xD480D480u); }
 constexpr uint32_t PD_M24 = 0xCE00CE00u;  // half2(-24, -24)
 // d += A B without volatile: the compiler may move it between the loads and conversions of other tiles
 ER_DEV void pd_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -391,7 +398,6 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
         // the queries as B: k16 steps 2 bb + i, the lane's dims 32 bb + 8 t + 4 i .. + 3 of column g
         uint32_t qh[2 * C::NB][2];
         [[maybe_unused]] uint32_t ql[2 * C::NB][2];
-        [[maybe_unused]] float bias[C::NB][4];  // RAW: minus the offsets' sum of columns 2 t, 2 t + 1 (twice)
         float down[2];
         {
             float top = 0.f;
@@ -407,15 +413,13 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             odd = __ballot_sync(0xffffffffu, odd) >> (lane & ~3) & 15;
-            // a power of two, up, brings the row's largest to [2^TOP, 2^(TOP + 1)): 14 keeps its lo halves normal, 0
-            // keeps the offsets' sums small
-            constexpr int TOP = Y::RAW ? 0 : 14;
-            const int ex = min(max((int)(__float_as_uint(top) >> 23), TOP + 1), 253);
-            const float up = odd ? 0.f : __uint_as_float((uint32_t)(254 + TOP - ex) << 23);
-            const float dn = odd ? NAN : __uint_as_float((uint32_t)(ex - TOP) << 23);
+            // a power of two, up, brings the row's largest to [2^14, 2^15): its lo halves are normal, and of a 16-bit row
+            // the values down to 2^-31 of that are exact
+            const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 253);
+            const float up = odd ? 0.f : __uint_as_float((uint32_t)(268 - ex) << 23);
+            const float dn = odd ? NAN : __uint_as_float((uint32_t)(ex - 14) << 23);
 #pragma unroll
             for (int bb = 0; bb < C::NB; ++bb) {
-                float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x0 = odd ? 0.f : pg_ld<T>(&raw[bb][2 * i]) * up, x1 = odd ? 0.f : pg_ld<T>(&raw[bb][2 * i + 1]) * up;
@@ -424,16 +428,6 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                     } else {
                         qh[2 * bb + (i >> 1)][i & 1] = pd_pack(x0, x1);
                     }
-                    if constexpr (Y::RAW) {
-                        const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&qh[2 * bb + (i >> 1)][i & 1]));
-                        sum += (z.x + z.y) * ((i & 1) ? -72.f : -1032.f);
-                    }
-                }
-                if constexpr (Y::RAW) {
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    bias[bb][0] = bias[bb][2] = __shfl_sync(0xffffffffu, sum, 8 * t);
-                    bias[bb][1] = bias[bb][3] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
                 }
             }
 #pragma unroll
@@ -472,15 +466,14 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
 #pragma unroll
                     for (int bb = 0; bb < C::NB; ++bb) {
                         const uint32_t w0 = kw[0][bb], w1 = kw[1][bb], u0 = w0 >> 8, u1 = w1 >> 8;
-                        const uint32_t a0[4] = {lop3_and_or(w0, 0x000F000Fu, 0x64006400u), lop3_and_or(w1, 0x000F000Fu, 0x64006400u),
-                                                lop3_and_or(w0, 0x00F000F0u, 0x54005400u), lop3_and_or(w1, 0x00F000F0u, 0x54005400u)};
-                        const uint32_t a1[4] = {lop3_and_or(u0, 0x000F000Fu, 0x64006400u), lop3_and_or(u1, 0x000F000Fu, 0x64006400u),
-                                                lop3_and_or(u0, 0x00F000F0u, 0x54005400u), lop3_and_or(u1, 0x00F000F0u, 0x54005400u)};
+                        const uint32_t a0[4] = {pd_low(w0), pd_low(w1), pd_high(w0), pd_high(w1)};
+                        const uint32_t a1[4] = {pd_low(u0), pd_low(u1), pd_high(u0), pd_high(u1)};
                         const float2 e0 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[0][bb >> 1]));
                         const float2 e1 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[1][bb >> 1]));
                         const float d0 = (bb & 1) ? e0.y : e0.x, d1 = (bb & 1) ? e1.y : e1.x;
                         float acc[4];
-                        pd_mma_c(acc, a0, qh[2 * bb][0], qh[2 * bb][1], bias[bb]);
+                        const float none[4] = {0.f, 0.f, 0.f, 0.f};
+                        pd_mma_c(acc, a0, qh[2 * bb][0], qh[2 * bb][1], none);
                         pd_mma(acc, a1, qh[2 * bb + 1][0], qh[2 * bb + 1][1]);
                         sc[0] = fmaf(d0, acc[0], sc[0]); sc[1] = fmaf(d0, acc[1], sc[1]);
                         sc[2] = fmaf(d1, acc[2], sc[2]); sc[3] = fmaf(d1, acc[3], sc[3]);
