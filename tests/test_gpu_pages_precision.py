@@ -92,7 +92,7 @@ def test_blocks_of_one_large_value(dtype, heads, kv, hd, new):
     check(b, *b.run())
 
 
-@pytest.mark.parametrize("dtype,new", [("f16", 1)])
+@pytest.mark.parametrize("dtype,new", [("f16", 1), ("bf16", 1)])
 def test_small_queries_beside_a_large_one(dtype, new):
     """16-bit queries enter exactly: one value of a row is 2^20 times the others and meets keys of zero."""
     rng = np.random.default_rng(60)
@@ -103,3 +103,19 @@ def test_small_queries_beside_a_large_one(dtype, new):
     b.q *= 2.0 ** -20
     b.q[..., 5] = 1.0
     check(b, *b.run())
+
+
+@pytest.mark.parametrize("dtype,new", [("f32", 1), ("f16", 1), ("bf16", 1), ("f32", 100)])
+@pytest.mark.parametrize("heads,kv,hd", [(8, 2, 128), (8, 4, 64)])
+def test_probabilities_all_alike(dtype, new, heads, kv, hd):
+    """One row scores above all others, which score the same: whatever a probability loses on its way to the values' product
+    is the same in every row and does not average out."""
+    rng = np.random.default_rng(70)
+    for scale in (0.02, 0.031):
+        b = Batch([400, 130], [new, new], heads, kv, hd, 16, dtype, seed=52, scale=scale)
+        for s, n in enumerate(b.lens):
+            k = np.full((n, kv, hd), 0.5)
+            k[0] = 1.0
+            rewrite(b, s, k, rng.uniform(0.5, 1.0, (n, kv, hd)))
+        b.q.copy_(torch.tensor(rng.uniform(0.5, 2.0, tuple(b.q.shape)), device="cuda"))
+        check(b, *b.run())
