@@ -5,14 +5,16 @@
 // Work.  A CTA takes one (sequence, KV head) and some query rows (a row is a (token, head of the KV head's group), so
 // a group's heads share the cached rows), and walks the cached rows in blocks of 128.
 //   16-bit rows (pages_prompt_kernel): two tiles of 128 query rows.
-//     warps 0-3, 4-7  a tile's softmax: thread = row = TMEM lane.  Reads S, writes P over it (fp16, the A operand of
-//                     the second product), keeps m and l, rescales O when it has to, writes the output.
-//     warp 12         one thread issues the products: S = Q K^T (M = 128, N = 128), O += P V (N = HD), the two tiles in
-//                     turn, so the tensor cores work on one tile while the other's softmax runs.
+//     warps 0-3, 4-7  a tile's softmax: thread = row = TMEM lane.  Reads S, writes P over it (hi and lo fp16 halves, 2^-22:
+//                     A operands of the second product), keeps m and l, rescales O when it has to, writes the output.
+//     warp 12         one thread issues the products: S = Q K^T (M = 128, N = 128), O += P V (N = HD, hi and lo of P), the
+//                     two tiles in turn, so the tensor cores work on one tile while the other's softmax runs.
 //     TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x HD).
-//   fp32 rows (pages_prompt32_kernel): one tile; queries and probabilities enter as hi + lo fp16 halves (2^-22), two
-//   products each.  The tensor cores' sums truncate (over thousands of rows 2^-18 of the output and growing), so a block's
-//   O starts from 0 and is added to sums in registers, rounded to nearest.
+//   P as one half (2^-11) would be 434 us for 8192 bf16 tokens against 554, but then a bf16 output in twenty differs by its
+//   last bit from what exact probabilities give, and an fp16 output is off by as much again as its own rounding.
+//   fp32 rows (pages_prompt32_kernel): one tile; queries enter as hi + lo halves too, two products each.  The tensor cores'
+//   sums truncate (over thousands of rows 2^-18 of the output and growing), so a block's O starts from 0 and is added to
+//   sums in registers, rounded to nearest.
 //     warps 0-3, 4-7  two threads a row, one for either half of the columns of S and of O: softmax, as above, with the
 //                     row's largest score exchanged through shared memory; then o = o * factor + the last block's O.
 //                     (One thread a row is bound by its own latency: 212 us against 167 for 4 x 500 tokens.  For 16-bit
@@ -24,19 +26,19 @@
 //   128-byte swizzle, two stages each; warp 13 requests the cached tiles: bulk copies into a ring of half blocks, each
 //   used by two operand warps.
 //
-// Registers (the launch's 128 a thread, shared out anew: 2 softmax + operands + rest = 512).  16 bits: 208, 48, 48 hold
-// everything; a spill in any role delays the others (8192 bf16 tokens: 433 us; 200, 80, 32: 485; 208, 64, 32: 460; 200, 64,
-// 48: 446).
-// fp32: 200, 64, 48 (4 x 500 tokens: 134 us; 200, 80, 32: 138).
+// Registers (the launch's 128 a thread, shared out anew: 2 softmax + operands + rest = 512).  A spill in any role delays the
+// others.  16 bits: 208, 48, 48 (8 bytes spilled at HD = 128; 8192 bf16 tokens: 554 us; 200, 56, 56: 585; 200, 64, 48: 588).
+// fp32: 200, 64, 48 (8 bytes; 4 x 500 tokens: 135 us; 200, 80, 32: 138).
 //
 // The block's rows are put in the order k' = 32 a + 8 t + 4 b + 2 i + e for row 32 a + 16 b + 8 i + 2 t + e, in K's rows,
 // hence S's and P's columns, and in V's K dimension: so a thread that holds a code word of V of two 16-row tiles
 // holds 16 bytes of the operand.
 //
-// What bounds it: shared memory's reads by the products and writes of their operands (2048 cycles a block and two tiles at
-// HD = 128, as many a block for fp32), and what the softmax and its hand-overs add to that (together about 3000 cycles).
-// Measured: 8192 bf16 tokens, 32 / 8 heads of 128: 433 us = 1.27 PFLOP/s, 0.66 of the library's matrix product; 4 x
-// 300..500 fp32 tokens over 900..4100 rows: 134 us.
+// What bounds it: at HD = 128 a block and two tiles take the tensor cores 3072 cycles (six products of 512; as many for one
+// tile of fp32), shared memory 2560 (the products' reads, the operands' writes), and about 3840 in all with the softmax and
+// its hand-overs.
+// Measured: 8192 bf16 tokens, 32 / 8 heads of 128: 554 us = 0.99 PFLOP/s, 0.52 of the library's matrix product (with the lo
+// halves' product counted 0.77); 4 x 300..500 fp32 tokens over 900..4100 rows: 135 us.
 //
 // Masks.  Blocks that some row attends only in part mask S; there, rows of V that no row of the CTA attends are
 // zeroed (they may hold anything), and a NaN value of V is carried by K instead, so only rows that attend it see it.
@@ -599,11 +601,15 @@ ER_DEV void pp_score(uint32_t d, uint32_t q, uint32_t k, bool more, uint32_t one
         pp_mma_ss(d, pp_desc(q) + (at >> 4), pp_desc(k) + (at >> 4), pp_idesc(128), more || i > 0, one);
     }
 }
+// P's lo halves lie 64 columns after the hi ones
 template <int HD>
 ER_DEV void pp_value(uint32_t d, uint32_t p, uint32_t v, bool more, uint32_t one) {
 #pragma unroll
-    for (int i = 0; i < PP_BLOCK / 16; ++i)
-        pp_mma_ts(d, p + i * 8, pp_desc(v) + (((i >> 2) * (HD * 128) + (i & 3) * 32) >> 4), pp_idesc(HD), more || i > 0, one);
+    for (int i = 0; i < PP_BLOCK / 16; ++i) {
+        const uint64_t b = pp_desc(v) + (((i >> 2) * (HD * 128) + (i & 3) * 32) >> 4);
+        pp_mma_ts(d, p + i * 8, b, pp_idesc(HD), more || i > 0, one);
+        pp_mma_ts(d, p + 64 + i * 8, b, pp_idesc(HD), 1, one);
+    }
 }
 
 // One block's scores of a row in registers: masked, their largest, and the probabilities written over them.
@@ -622,15 +628,15 @@ ER_DEV float pp_largest(const float (&s)[N]) {
         for (int e = 0; e < 4; ++e) mx[e] = pp_max3(mx[e], s[k + 2 * e], s[k + 2 * e + 1]);
     return pp_max3(pp_max3(mx[0], mx[1], fmaxf(s[N - 4], s[N - 3])), pp_max3(mx[2], mx[3], s[N - 2]), s[N - 1]);
 }
-// p = 2^(s down - m + PP_UP) as fp16 to N / 2 columns at tP (LO: the lo halves 64 columns on); returns their sum
-template <bool LO, int N>
+// p = 2^(s down - m + PP_UP) as hi and lo halves to N / 2 columns at tP and 64 columns on; returns their sum
+template <int N>
 ER_DEV float pp_probabilities(const float (&s)[N], uint32_t tP, float down, float m) {
     const float2 nb = make_float2(PP_UP - m, PP_UP - m), dn = make_float2(down, down);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int q = 0; q < N / 32; ++q) {  // 32 columns of S become 16 of P: few registers beside S itself
         uint32_t ph[16];
-        [[maybe_unused]] uint32_t pl[16];
+        uint32_t pl[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             float2 x = pp_fma2(make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), dn, nb);
@@ -638,13 +644,11 @@ ER_DEV float pp_probabilities(const float (&s)[N], uint32_t tP, float down, floa
             x.y = pp_ex2(x.y);
             sum[k & 1] = pp_add2(sum[k & 1], x);
             ph[k] = pp_pack(x.x, x.y);
-            if constexpr (LO) {
-                const float2 z = pp_fma2(__half22float2(*reinterpret_cast<const __half2 *>(&ph[k])), make_float2(-1.f, -1.f), x);
-                pl[k] = pp_pack(z.x, z.y);
-            }
+            const float2 z = pp_fma2(__half22float2(*reinterpret_cast<const __half2 *>(&ph[k])), make_float2(-1.f, -1.f), x);
+            pl[k] = pp_pack(z.x, z.y);
         }
         pp_st16(tP + 16 * q, ph);
-        if constexpr (LO) pp_st16(tP + 64 + 16 * q, pl);
+        pp_st16(tP + 64 + 16 * q, pl);
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -749,7 +753,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                         }
                     }
                 }
-                l += pp_probabilities<false>(s, tS, down, m);
+                l += pp_probabilities(s, tS, down, m);
                 pp_wait_st();
                 pp_fence_before();
                 __syncwarp();
@@ -915,7 +919,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             const float corr = mn == m ? 1.f : pp_ex2(m - mn);
             l *= corr;
             m = mn;
-            l += pp_probabilities<true>(s, tS + 32 * W, down, m);
+            l += pp_probabilities(s, tS + 32 * W, down, m);
             pp_wait_st();
             pp_fence_before();
             __syncwarp();
@@ -975,7 +979,6 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
                 if (!ok) break;
                 pp_fence_after();
                 pp_value<HD>(PP_TMEM + 256 + st * HD, PP_TMEM + st * 128, vb + st * C::OP, false, one);
-                pp_value<HD>(PP_TMEM + 256 + st * HD, PP_TMEM + st * 128 + 64, vb + st * C::OP, true, one);
                 pp_commit(B.o + st, one);
                 pp_commit(B.vempty + st, one);
                 if (j + 2 < I.nblk) {

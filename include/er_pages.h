@@ -147,9 +147,9 @@ ER_API er_status er_pages_read(er_pages *p, int32_t layer, int32_t n, const int3
  * be NULL): log of sum_r exp(scale q . k_r).  A token that attends no row (p < 0) gets zeros and
  * -infinity.  Any mix of single tokens and prompts; rows of q_dev that belong to
  * no sequence are left alone.  Scores, softmax and sums are fp32; fp32 queries
- * and probabilities enter the tensor cores as two fp16 halves each (2^-22), 16-bit
- * queries exactly (but for values below 2^-31 of their row's largest) and their
- * probabilities as two halves or one (2^-11 of each).  Results do not depend on timing.
+ * and the probabilities of every type enter the tensor cores as two fp16 halves
+ * each (2^-22), 16-bit queries exactly (but for values below 2^-31 of their row's
+ * largest).  Results do not depend on timing.
  *   - A q_start_dev that falls or passes n_tokens, a length below 0, past the
  *     table or past 2^31 - 1025, and a table entry outside the pool set flag bit 1 and leave that
  *     sequence's outputs unspecified; nothing outside the pool is read.

@@ -92,7 +92,7 @@ def test_blocks_of_one_large_value(dtype, heads, kv, hd, new):
     check(b, *b.run())
 
 
-@pytest.mark.parametrize("dtype,new", [("f16", 1), ("bf16", 1)])
+@pytest.mark.parametrize("dtype,new", [("f16", 1), ("bf16", 1), ("f16", 100), ("bf16", 100)])
 def test_small_queries_beside_a_large_one(dtype, new):
     """16-bit queries enter exactly: one value of a row is 2^20 times the others and meets keys of zero."""
     rng = np.random.default_rng(60)
@@ -105,7 +105,7 @@ def test_small_queries_beside_a_large_one(dtype, new):
     check(b, *b.run())
 
 
-@pytest.mark.parametrize("dtype,new", [("f32", 1), ("f16", 1), ("bf16", 1), ("f32", 100)])
+@pytest.mark.parametrize("dtype,new", [("f32", 1), ("f16", 1), ("bf16", 1), ("f32", 100), ("f16", 100), ("bf16", 100), ("f16", 300)])
 @pytest.mark.parametrize("heads,kv,hd", [(8, 2, 128), (8, 4, 64)])
 def test_probabilities_all_alike(dtype, new, heads, kv, hd):
     """One row scores above all others, which score the same: whatever a probability loses on its way to the values' product
