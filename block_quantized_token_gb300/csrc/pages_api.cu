@@ -221,6 +221,8 @@ er_status er_pages_error(er_pages *p, int32_t *code) {
     if (e == cudaSuccess) e = cudaMemset(p->flags, 0, sizeof(int));
     // a kernel that gave up may have left its arrival counters short
     if (e == cudaSuccess && (f & ER_FLAG_WAIT)) e = cudaMemset(p->cnt, 0, (size_t)p->num_sms * sizeof(int));
+    // cudaMemset returns before it is done, and a stream that does not wait for the null stream may run a call of this handle next
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return er_fail_cuda(e, "er_pages_error");
     *code = f & (ER_PAGES_FLAG_FULL | ER_PAGES_FLAG_RANGE | ER_FLAG_WAIT);
     return *code ? er_fail_status(ER_EDEVICE, "device flags set") : ER_OK;
