@@ -905,6 +905,7 @@ er_status er_get_device_error(er_kv *kv, int32_t *code, int32_t *non_finite) {
     int f = 0;
     ER_CUDA(cudaMemcpy(&f, kv->flags, sizeof(int), cudaMemcpyDeviceToHost));
     ER_CUDA(cudaMemset(kv->flags, 0, sizeof(int)));
+    ER_CUDA(cudaDeviceSynchronize());  // the memset returns before it is done; a step on another stream may set a flag next
     *code = f & (ER_FLAG_TOKEN | ER_FLAG_POS | ER_FLAG_WAIT);
     *non_finite = (f & ER_FLAG_NONFINITE) ? 1 : 0;
     return *code ? fail(ER_EDEVICE, "device flags 0x%x", f) : ER_OK;
