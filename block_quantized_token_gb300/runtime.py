@@ -172,7 +172,8 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 def rope_table(head_dim: int, base: float, n_positions: int, device: str = "cuda") -> torch.Tensor:
     """(cos, sin) of p * base^(-2 i / head_dim), fp32 [n_positions, head_dim / 2, 2], made on the device."""
     out = torch.empty((n_positions, head_dim // 2, 2), dtype=torch.float32, device=device)
-    er.er_rope_table(head_dim, base, n_positions, out.data_ptr(), torch.cuda.current_stream(out.device).cuda_stream)
+    with torch.cuda.device(out.device):  # (a default stream's handle is the same on every device)
+        er.er_rope_table(head_dim, base, n_positions, out.data_ptr(), torch.cuda.current_stream(out.device).cuda_stream)
     return out
 
 
@@ -180,7 +181,7 @@ class PagedCache:
     """Owns an er_pages handle and, unless given, its pool: a paged 4-bit K/V cache (er_pages_* in er_pages.h).
 
     Row tensors are [tokens, heads, head_dim] with dense heads and any stride between tokens; int tensors are dense
-    int32; all on the cache's device.
+    int32; all on the cache's device, which need not be the current one.
     """
 
     def __init__(self, n_layers: int, n_pages: int, page_rows: int, n_kv_heads: int, head_dim: int,
@@ -200,6 +201,13 @@ class PagedCache:
 
     # The checks below stand before calls that take the GPU 6 us, so they ask each tensor as little as they can (a
     # device's index and a raw stream cost a tenth of the device and stream objects).
+    def _call(self, fn: Callable, *args):
+        """fn(handle, ...) with the cache's device current."""
+        if torch._C._cuda_getDevice() == self._index:
+            return fn(self.handle, *args)
+        with torch.cuda.device(self._index):
+            return fn(self.handle, *args)
+
     def _stream(self, stream: int | None) -> int:
         return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream
 
@@ -241,7 +249,7 @@ class PagedCache:
                                   free_count.data_ptr(), tables.data_ptr(), lens_out.data_ptr(),
                                   free_count_out.data_ptr(), q_start.data_ptr(), positions.data_ptr(), slots.data_ptr(),
                                   seqs.data_ptr())
-        er.er_pages_plan(self.handle, a, self._stream(stream))
+        self._call(er.er_pages_plan, a, self._stream(stream))
 
     def release(self, done: torch.Tensor, lens: torch.Tensor, tables: torch.Tensor, free: torch.Tensor,
                 free_count: torch.Tensor, stream: int | None = None) -> None:
@@ -250,8 +258,8 @@ class PagedCache:
         self._ints(n, done, lens)
         self._ints(1, free_count)
         self._ints(self.cfg.n_pages, free)
-        er.er_pages_release(self.handle, n, done.data_ptr(), lens.data_ptr(), tables.data_ptr(),
-                            self._table(tables, n), free.data_ptr(), free_count.data_ptr(), self._stream(stream))
+        self._call(er.er_pages_release, n, done.data_ptr(), lens.data_ptr(), tables.data_ptr(), self._table(tables, n),
+                   free.data_ptr(), free_count.data_ptr(), self._stream(stream))
 
     def append(self, layer: int, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
                positions: torch.Tensor | None, slots: torch.Tensor, q_out: torch.Tensor | None = None,
@@ -284,7 +292,7 @@ class PagedCache:
                                     0 if rope is None else rope.shape[0], _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out),
                                     qs, ks, vs, os_, _ptr(q_gain), _ptr(k_gain), _ptr(rope),
                                     None if rope is None else positions.data_ptr(), slots.data_ptr(), eps)
-        er.er_pages_append(self.handle, layer, a, self._stream(stream))
+        self._call(er.er_pages_append, layer, a, self._stream(stream))
 
     def read(self, layer: int, slots: torch.Tensor, k_out: torch.Tensor | None, v_out: torch.Tensor | None,
              stream: int | None = None) -> None:
@@ -300,8 +308,8 @@ class PagedCache:
                 dtype = t.dtype
         if dtype is None:
             return
-        er.er_pages_read(self.handle, layer, n, slots.data_ptr(), _ROW_TYPES[dtype],
-                         _ptr(k_out), _ptr(v_out), self._stream(stream))
+        self._call(er.er_pages_read, layer, n, slots.data_ptr(), _ROW_TYPES[dtype], _ptr(k_out), _ptr(v_out),
+                   self._stream(stream))
 
     def attention(self, layer: int, q: torch.Tensor, out: torch.Tensor, q_start: torch.Tensor, lens: torch.Tensor,
                   tables: torch.Tensor, scale: float = 0.0, window: int = 0, lse: torch.Tensor | None = None,
@@ -318,11 +326,11 @@ class PagedCache:
         a = er.er_pages_attention_args(seqs, n, heads, _ROW_TYPES[q.dtype], self._table(tables, seqs), window,
                                        q.data_ptr(), out.data_ptr(), _ptr(lse), qs, os_,
                                        q_start.data_ptr(), lens.data_ptr(), tables.data_ptr(), scale)
-        er.er_pages_attention(self.handle, layer, a, self._stream(stream))
+        self._call(er.er_pages_attention, layer, a, self._stream(stream))
 
     def error(self) -> tuple[int, int]:
         """(status, flags) of the calls so far; synchronises (er_pages_error)."""
-        return er.er_pages_error(self.handle)
+        return self._call(er.er_pages_error)
 
     def close(self) -> None:
         if getattr(self, "handle", None):

@@ -2,7 +2,11 @@
 
 from __future__ import annotations
 
+import pytest
+
 import fake_cuda
+
+torch = pytest.importorskip("torch")
 
 
 def test_error_words_are_cleared_when_the_call_returns(tmp_path):
@@ -35,3 +39,66 @@ word("fake_pending").value = 0
 er.er_get_device_error(kv)
 assert word("fake_pending").value == 0
 """)
+
+
+class Current:
+    """Stands for torch.cuda.device: which device a call found current."""
+
+    def __init__(self, start):
+        self.now = start
+
+    def __call__(self, device):
+        return _Held(self, device)
+
+
+class _Held:
+    def __init__(self, current, device):
+        self.current, self.device = current, device
+
+    def __enter__(self):
+        self.before, self.current.now = self.current.now, self.device
+
+    def __exit__(self, *_):
+        self.current.now = self.before
+
+
+def _runtime(monkeypatch, current):
+    from block_quantized_token_gb300 import build
+    build.build()
+    from block_quantized_token_gb300 import er, runtime
+    seen = []
+    for name in ("er_rope_table", "er_pages_plan", "er_pages_release", "er_pages_append", "er_pages_read", "er_pages_attention",
+                 "er_pages_error"):
+        monkeypatch.setattr(er, name, lambda *a, name=name: seen.append((name, current.now)))
+    monkeypatch.setattr(torch.cuda, "device", current)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current.now, raising=False)
+    return runtime, seen
+
+
+def test_rope_table_runs_on_the_device_of_its_memory(monkeypatch):
+    current = Current(3)
+    runtime, seen = _runtime(monkeypatch, current)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: type("S", (), dict(cuda_stream=0)))
+    runtime.rope_table(64, 10000.0, 4, device="cpu")
+    assert seen == [("er_rope_table", torch.device("cpu"))] and current.now == 3
+
+
+def test_paged_calls_run_on_the_cache_s_device(monkeypatch):
+    current = Current(3)
+    runtime, seen = _runtime(monkeypatch, current)
+    from block_quantized_token_gb300 import er
+    c = object.__new__(runtime.PagedCache)
+    c.n_kv_heads, c.head_dim, c.cfg, c.handle = 2, 64, er.er_pages_config(1, 4, 16, 2, 64, er.ER_Q4_0), 1
+    c.device, c._index = torch.device("cpu"), -1  # (a CPU tensor's index)
+    try:
+        i, x, t = torch.zeros(8, dtype=torch.int32), torch.zeros(4, 2, 64), torch.zeros(1, 2, dtype=torch.int32)
+        one = i[:1]
+        c.plan(one, one, t, i, one, one, one, i, i, i, i, stream=0)
+        c.release(one, one, t, i, one, stream=0)
+        c.append(0, None, x, x, None, i, stream=0)
+        c.read(0, i[:4], x, x, stream=0)
+        c.attention(0, x, x, i, one, t, stream=0)
+        c.error()
+        assert [d for _, d in seen] == [-1] * 6 and current.now == 3
+    finally:
+        c.handle = None
