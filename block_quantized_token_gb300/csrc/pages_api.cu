@@ -43,6 +43,17 @@ bool words(const P *...p) {  // int32 and float arrays (NULL is)
     return (((uintptr_t)p | ...) & 3) == 0;
 }
 
+// refuses memory of another device than the current one, where a kernel would reach it as a peer's or fault
+er_status check_memory(const void *p, const char *what) {
+    int dev = -1;
+    cudaPointerAttributes a;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaPointerGetAttributes(&a, p);
+    if (e != cudaSuccess) return er_fail_cuda(e, what);
+    return a.type == cudaMemoryTypeDevice && a.device != dev
+               ? er_fail_status(ER_EINVAL, "the memory belongs to another device than the current one")
+               : ER_OK;
+}
 er_status check_handle(const er_pages *p) {
     if (!p) return er_fail_status(ER_EINVAL, "handle is NULL");
     int dev = -1;
@@ -75,6 +86,7 @@ er_status er_pages_create(const er_pages_config *cfg, void *pool, er_pages **out
     if (er_status s = check_config(cfg); s != ER_OK) return s;
     if (!pool) return er_fail_status(ER_EINVAL, "pool is NULL");
     if (!aligned(pool, 16)) return er_fail_status(ER_EINVAL, "pool must be 16-byte aligned");
+    if (er_status s = check_memory(pool, "er_pages_create"); s != ER_OK) return s;
     er_pages *p = new (std::nothrow) er_pages();
     if (!p) return er_fail_status(ER_ENOMEM, "out of host memory");
     p->cfg = *cfg;
@@ -143,6 +155,8 @@ er_status er_rope_table(int32_t head_dim, double base, int32_t n, float *out, vo
     if (!(base > 0) || !isfinite(base)) return er_fail_status(ER_EINVAL, "base must be positive and finite");
     if (n < 0 || (n && !out)) return er_fail_status(ER_EINVAL, "n_positions negative or out NULL");
     if (!aligned(out, 4)) return er_fail_status(ER_EINVAL, "out must be 4-byte aligned");
+    if (!n) return ER_OK;
+    if (er_status s = check_memory(out, "er_rope_table"); s != ER_OK) return s;
     return done(launch_rope_table(head_dim, base, n, out, (cudaStream_t)stream), "er_rope_table");
 }
 

@@ -47,7 +47,8 @@ enum { ER_BF16 = 30 };
  * Configuration.  page_rows: a multiple of 16 up to 1024; head_dim 64 or 128
  * (else ER_EUNSUPPORTED); kv_type ER_Q4_0 (another er_dtype: ER_EUNSUPPORTED);
  * n_pages * page_rows < 2^31 and that times n_kv_heads < 2^35.  The handle owns scratch only; it belongs to the
- * device it was created on (a call with another device current is ER_EINVAL).
+ * device it was created on, and so do the pool and every array of a call (a pool of another device, or a call with another
+ * device current, is ER_EINVAL).
  * The calls of one handle share its scratch: order them (one stream, or
  * events), captured graphs of them included.  Work that overlaps takes a handle
  * each: any number of handles may be made over one pool. */
@@ -94,7 +95,8 @@ ER_API er_status er_pages_release(er_pages *p, int32_t n_seqs, const int32_t *do
                                   int32_t *free_count_dev, void *stream);
 
 /* (cos, sin) of p * base^(-2 i / head_dim), computed in float64, as fp32
- * out_dev[n_positions][head_dim / 2][2], the table er_pages_append reads. */
+ * out_dev[n_positions][head_dim / 2][2], the table er_pages_append reads.  Memory of
+ * another device than the current one is ER_EINVAL. */
 ER_API er_status er_rope_table(int32_t head_dim, double base, int32_t n_positions, float *out_dev, void *stream);
 
 /* Norms of queries and keys for each head, their rotation and the K/V append, in

@@ -41,6 +41,21 @@ assert word("fake_pending").value == 0
 """)
 
 
+def test_memory_of_another_device_is_refused(tmp_path):
+    fake_cuda.run(tmp_path, """
+for own, other in ((0, 1), (1, 0)):
+    word("fake_device").value, word("fake_pointer_device").value = own, other
+    assert refused(er.er_rope_table, 64, 10000.0, 4, at) == er.ER_EINVAL
+    assert refused(er.er_pages_create, cfg, pool_ptr) == er.ER_EINVAL
+    assert word("fake_launches").value == own
+    word("fake_pointer_device").value = own
+    assert refused(er.er_rope_table, 64, 10000.0, 4, at) == er.ER_OK
+    h = er.er_pages_create(cfg, pool_ptr)
+    word("fake_device").value = other
+    assert refused(er.er_pages_read, h, 0, 4, at, er.ER_F32, pool_ptr, None) == er.ER_EINVAL
+    er.er_pages_destroy(h)
+""")
+
 class Current:
     """Stands for torch.cuda.device: which device a call found current."""
 
