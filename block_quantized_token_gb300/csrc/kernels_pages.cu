@@ -404,6 +404,8 @@ ER_DEV void st_row(T *row, int c, bool vec, const float (&x)[8]) {
 // AP_ERR: the sum of HD squares takes at most 10 float32 steps (half of that in its root), the reciprocal root and its
 // argument 4, gain times cosine 1, the rotation 2, the last product 1: below 14 steps of 2^-24.
 constexpr float AP_ERR = 14.f * 5.9604645e-8f;
+// A mean square (and eps) between these is as exact as that counts: no square that matters has underflowed or overflowed.
+constexpr float AP_SMALL = 0x1p-90f, AP_LARGE = 0x1p120f;
 
 template <bool HALVES, bool CHECK>
 ER_DEV bool ap_quant(const float (&y)[8], uint32_t &codes, float (&d)[2], int lane) {
@@ -554,15 +556,19 @@ ER_DEV void append_qk(const AppendArgs &A) {
             }
         }
     };
-    auto row_of = [&](const float (&x)[8], bool norm, float (&y)[8]) {
+    // returns false where the sum of squares may have left fp32's range on its way
+    auto row_of = [&](const float (&x)[8], bool norm, float eps, float (&y)[8]) {
         float rs = 1.f;
+        bool in_range = true;
         if (norm) {
             float ss = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
             for (int o = 1; o < LG; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            rs = rsqrtf(ss * (1.f / HD) + a.eps);
+            const float ms = ss * (1.f / HD) + eps;
+            in_range = ms > AP_SMALL && ms < AP_LARGE;
+            rs = rsqrtf(ms);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -570,6 +576,7 @@ ER_DEV void append_qk(const AppendArgs &A) {
             y[e0] = (x[e0] * co[e0] - x[e1] * si[e1]) * rs;
             y[e1] = (x[e1] * co[e1] + x[e0] * si[e0]) * rs;
         }
+        return in_range;
     };
     // Whole warps go round together (its groups' tokens and parts may differ), U rows of a group at a time: their loads are
     // in flight together.  work returns whether the row is to be done again by the exact steps, after the others of its U.
@@ -608,12 +615,32 @@ ER_DEV void append_qk(const AppendArgs &A) {
     if (a.n_heads) {
         factors(a.q_gain_dev);
         T *dst = (T *)a.q_out_dev + t * a.q_out_stride;
-        rows_of((const T *)a.q_dev, a.q_stride, vq, a.n_heads, [&](int r, bool live, const float (&x)[8]) {
-            float y[8];
-            row_of(x, a.q_gain_dev != nullptr, y);
+        auto put = [&](int r, bool live, const float (&y)[8]) {
             if (live) st_row<T, HD, HALVES>(dst + (size_t)r * HD, c, vo, y);
             return false;
-        }, never);
+        };
+        if (a.q_gain_dev && a.eps <= AP_SMALL) {
+            // eps keeps no mean square in range: the row and eps times the power of two that brings the larger to [1, 2)
+            rows_of((const T *)a.q_dev, a.q_stride, vq, a.n_heads, [&](int r, bool live, const float (&x)[8]) {
+                unsigned top = __float_as_uint(sqrtf(a.eps));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+                for (int o = 1; o < LG; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float up = __uint_as_float((254u - min(max(top >> 23, 1u), 253u)) << 23);
+                float z[8], y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = x[e] * up;
+                row_of(z, true, a.eps * up * up, y);
+                return put(r, live, y);
+            }, never);
+        } else {
+            rows_of((const T *)a.q_dev, a.q_stride, vq, a.n_heads, [&](int r, bool live, const float (&x)[8]) {
+                float y[8];
+                row_of(x, a.q_gain_dev != nullptr, a.eps, y);
+                return put(r, live, y);
+            }, never);
+        }
     }
     const bool norm = a.k_gain_dev != nullptr;
     factors(a.k_gain_dev);
@@ -674,8 +701,8 @@ ER_DEV void append_qk(const AppendArgs &A) {
         rows_of((const T *)a.k_dev, a.k_stride, vk, p.KV, [&](int r, bool live, const float (&x)[8]) {
             uint32_t codes;
             float d[2], y[8];
-            row_of(x, norm, y);
-            const bool unsure = ap_quant<HALVES, true>(y, codes, d, lane);
+            const bool in_range = row_of(x, norm, a.eps, y);
+            const bool unsure = ap_quant<HALVES, true>(y, codes, d, lane) || !in_range;
             store(r, live, codes, d);
             return unsure && live;
         }, exact);

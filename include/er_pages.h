@@ -108,7 +108,8 @@ ER_API er_status er_rope_table(int32_t head_dim, double base, int32_t n_position
  *   dims (2 i, 2 i + 1), ER_ROPE_HALVES (i, i + head_dim / 2).
  * Queries go to q_out_dev (`type`, rows q_out_stride apart, may be q_dev itself),
  * keys (normed and rotated) and values (as they are) into slot slots_dev[t] of
- * `layer`.  A key's codes are those of the formula in float64 rounded to float32:
+ * `layer`.  Queries are worked in float32: with eps above 2^-90, a query row whose
+ * squares' sum passes float32's largest number becomes zeros.  A key's codes are those of the formula in float64 rounded to float32:
  * rows near a border are computed again in float64.
  *   - A row with a negative slot is skipped whole: nothing of it is read or
  *     written.  A slot past the pool, or with a rope table a position outside

@@ -1,0 +1,68 @@
+"""The paged 4-bit K/V cache on the GPU: rows at the ends of the float range, waits that give up, flags between streams."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import pages as op
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from test_gpu_pages import HALF, fine, host, ints, noise, paged  # noqa: E402
+
+LEAST = {"f32": 2.0 ** -150, "f16": 2.0 ** -25, "bf16": 2.0 ** -134}  # half the smallest step of a type
+
+
+@pytest.mark.parametrize("style", ["pairs", "halves"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype,sizes", [("f32", (1e-44, 1e-38, 1e-30, 1e-22, 1e-15, 1e-9, 1e9, 1e18, 1e25, 1e37)),
+                                         ("bf16", (1e-38, 1e-30, 1e-22, 1e-15, 1e18, 1e30, 1e37)), ("f16", (1e-7, 1e-3, 1e4))])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-30, 1e-5])
+def test_norm_of_rows_at_the_ends_of_the_range(style, hd, dtype, sizes, eps):
+    """The norm takes a row's size away whatever it is: squares below fp32's smallest and above its largest number (queries: the
+    latter only with an eps up to 2^-90, and zeros else).  Queries
+    within 16 roundings of a pair and the output's own, keys with the codes of the float64 formula."""
+    from block_quantized_token_gb300 import runtime
+    rng = np.random.default_rng(80)
+    n, heads, kv = 3 * len(sizes), 5, 3
+    size = np.repeat(sizes, 3)[rng.permutation(n), None, None]  # neighbours of other sizes
+    def rows(h):
+        x = torch.tensor(np.clip(rng.standard_normal((n, h, hd)), -3, 3) * size, device="cuda")
+        return x.to({"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dtype])
+    q, k = rows(heads), rows(kv)
+    gains = [(1 + 0.2 * rng.standard_normal(hd)).astype(np.float32) for _ in range(2)]
+    gd = [torch.tensor(g, device="cuda") for g in gains]
+    positions = rng.integers(0, 500, n)
+    table = runtime.rope_table(hd, 10000.0, 500)
+    cs = host(table)[positions]
+    cache = paged(n // 16 + 1, 16, kv, hd, fill=noise(81))
+    q_out = torch.empty_like(q)
+    cache.append(0, q, k, k, ints(positions), ints(np.arange(n)), q_out, q_gain=gd[0], k_gain=gd[1], eps=eps, rope=table,
+                 rope_style=style)
+    out = torch.empty((n, kv, hd), device="cuda")
+    cache.read(0, ints(np.arange(n)), out, None)
+    want = op.norm_rope(host(k), gains[1], eps, cs, style).astype(np.float32)
+    np.testing.assert_array_equal(host(out), op.dequant_kv_q4_0(*op.quantize_kv_q4_0(want)))
+    want, flat = op.norm_rope(host(q), gains[0], eps, cs, style), np.abs(op.norm_rope(host(q), gains[0], eps, None, style))
+    a, b = (slice(0, hd, 2), slice(1, hd, 2)) if style == "pairs" else (slice(0, hd // 2), slice(hd // 2, hd))
+    pair = np.empty_like(flat)
+    pair[..., a] = pair[..., b] = flat[..., a] + flat[..., b]
+    # below fp32's smallest normal number a rounding is 2^-150 whatever the value: three of them times 1 / sqrt(mean square),
+    # and the output's own
+    low = 4 * 2.0 ** -150 / np.sqrt(max(eps, 2.0 ** -90)) + LEAST[dtype]
+    tol = 16 * 2.0 ** -24 * pair + HALF[dtype] * np.abs(want) * 1.001 + low
+    squares = (host(q) ** 2).sum(-1, keepdims=True)
+    zero = (squares > 2.0 ** 127) & (eps > 2.0 ** -90)
+    assert (host(q_out)[np.broadcast_to(zero & (squares > 2.0 ** 129), q.shape)] == 0).all()
+    assert (np.abs(host(q_out) - want) <= tol)[np.broadcast_to(~zero, q.shape)].all()
+    # over the queries themselves
+    same = q.clone()
+    cache.append(0, same, k, k, ints(positions), ints(np.arange(n)), same, q_gain=gd[0], k_gain=gd[1], eps=eps, rope=table,
+                 rope_style=style)
+    assert torch.equal(same, q_out)
+    fine(cache)
