@@ -56,6 +56,18 @@ for own, other in ((0, 1), (1, 0)):
     er.er_pages_destroy(h)
 """)
 
+def test_release_refuses_more_entries_than_it_can_number(tmp_path):
+    """The kernel's running number of an entry must not pass an int, nor the first of the block's width after the last."""
+    fake_cuda.run(tmp_path, """
+h = er.er_pages_create(cfg, pool_ptr)
+for n, stride in ((1024, 1 << 21), (2, 2**30), (1, 2**31 - 1), (1, 2**31 - 1023)):
+    assert refused(er.er_pages_release, h, n, at, at, at, stride, at, at) == er.ER_EINVAL, (n, stride)
+assert word("fake_launches").value == 0
+for n, stride in ((1023, 1 << 21), (1, 2**31 - 1024), (1024, 1)):
+    assert refused(er.er_pages_release, h, n, at, at, at, stride, at, at) == er.ER_OK, (n, stride)
+er.er_pages_destroy(h)
+""")
+
 class Current:
     """Stands for torch.cuda.device: which device a call found current."""
 
