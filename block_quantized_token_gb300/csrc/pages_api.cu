@@ -144,8 +144,8 @@ er_status er_pages_release(er_pages *p, int32_t n_seqs, const int32_t *done_dev,
     if (n_seqs < 1 || n_seqs > ER_PAGES_MAX_SEQS) return er_fail_status(ER_EINVAL, "n_seqs must be in 1..1024");
     if (table_stride < 1) return er_fail_status(ER_EINVAL, "table_stride must be positive");
     // (the kernel numbers the entries given back with an int, a block's width at a time)
-    if ((long long)n_seqs * table_stride > 2147483647ll - 1024)
-        return er_fail_status(ER_EINVAL, "n_seqs * table_stride must be below 2^31 - 1024");
+    if ((long long)n_seqs * table_stride > 2147483648ll - 1024)
+        return er_fail_status(ER_EINVAL, "n_seqs * table_stride must be at most 2^31 - 1024");
     if (!words(done_dev, lens, tables, free_list, free_count)) return er_fail_status(ER_EINVAL, "int arrays must be 4-byte aligned");
     if (er_status s = check_handle(p); s != ER_OK) return s;
     return done(launch_pages_release(view_of(p, 0), n_seqs, done_dev, lens, tables, table_stride, free_list, free_count,

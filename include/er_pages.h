@@ -89,7 +89,7 @@ ER_API er_status er_pages_plan(er_pages *p, const er_pages_plan_args *a, void *s
  * free_dev in order of request and block, *free_count_dev grows, lens_dev[b]
  * becomes 0 and the table's entries of the pages become -1.  An entry outside the
  * pool, or one for which free_dev (n_pages long) has no room, is dropped (flag
- * bit 1).  n_seqs * table_stride: below 2^31 - 1024. */
+ * bit 1).  n_seqs * table_stride: at most 2^31 - 1024. */
 ER_API er_status er_pages_release(er_pages *p, int32_t n_seqs, const int32_t *done_dev, int32_t *lens_dev,
                                   int32_t *tables_dev, int32_t table_stride, int32_t *free_dev,
                                   int32_t *free_count_dev, void *stream);
