@@ -707,8 +707,8 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
     if (bad) {
         if (lane == 0) atomicOr(P.p.flags, ER_FLAG_WAIT);
         ms.wait_bad = 1;
-        // copies may still be landing: wait for them (each again with a limit)
-        for (int k = max(0, inext - PD_SLOTS); k < inext; ++k) mbar_wait(bars + k % PD_SLOTS, (k / PD_SLOTS) & 1);
+        // copies may still be landing
+        for (int k = max(0, inext - PD_SLOTS); k < inext; ++k) pg_drain(bars + k % PD_SLOTS, (k / PD_SLOTS) & 1);
     }
     __syncthreads();
     if (warp == 0) {  // runs of neighbouring states of one unit; lane e looks at the e-th place for one

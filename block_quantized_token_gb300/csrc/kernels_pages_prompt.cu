@@ -78,7 +78,7 @@ struct PpArgs {
 };
 
 struct PpBars {
-    uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], oempty[2], x[2], q;
+    uint64_t raw[PP_RAW], rawfree[PP_RAW], kfull[2], kempty[2], vfull[2], vempty[2], s[2], p[2], o[2], oempty[2], x[2], q, end;
     uint32_t tmem;
     int item[6];  // sequence, first query row, KV head, found, first row of q, query rows
 };
@@ -544,9 +544,8 @@ ER_DEV void pp_copies(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem &I
             par ^= 1;
         }
     }
-    // given up: copies may still be landing
-    if (!ok)
-        for (int k = max(0, i - PP_RAW); k < i; ++k) mbar_wait(B.raw + k % PP_RAW, (k / PP_RAW) & 1);
+    // copies may still be landing where this warp or one that uses them gave up
+    for (int k = max(0, i - PP_RAW); k < i; ++k) pg_drain(B.raw + k % PP_RAW, (k / PP_RAW) & 1);
 }
 
 // barriers (thread 0) and the whole of TMEM (warp 12)
@@ -569,6 +568,7 @@ ER_DEV void pp_setup(PpBars &B, int tid, int warp, int query_warps, int softmax_
             mbar_init(B.x + i, 8);
         }
         mbar_init(&B.q, query_warps);
+        mbar_init(&B.end, 1);
         fence_mbar_init();
     }
     if (warp == 12) {
@@ -818,8 +818,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 }
             }
             if (!ok) {  // given up: products in flight read shared memory and TMEM until they end
-                pp_commit(B.o, one);
-                for (int k = 0; k < 2; ++k) mbar_wait(B.o, k);
+                pp_commit(&B.end, one);
+                pg_drain(&B.end, 0);
             }
         } else if (warp == 13) {
             pp_copies<HD>(P, B, smem, I, lane);
@@ -989,8 +989,8 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
                 }
             }
             if (!ok) {  // given up: products in flight read shared memory and TMEM until they end
-                pp_commit(B.vempty, one);
-                for (int k = 0; k < 2; ++k) mbar_wait(B.vempty, k);
+                pp_commit(&B.end, one);
+                pg_drain(&B.end, 0);
             }
         } else if (warp == 13) {
             pp_copies<HD>(P, B, smem, I, lane);

@@ -75,6 +75,14 @@ ER_DEV __half pg_cvt<__half>(float v) { return __float2half_rn(v); }
 template <>
 ER_DEV __nv_bfloat16 pg_cvt<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Waits for what a CTA has in flight before it ends.  With a limit of its own: under the one that er_set_wait_limit_ns sets
+// the CTA could end while copies still write its shared memory, by then another's.
+ER_DEV void pg_drain(uint64_t *bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < ER_WAIT_NS) {
+    }
+}
+
 constexpr int PG_MAX_LEN = 2147483647 - 1024;
 // a sequence's rows at most: what its table holds, and fewer than 2^31 by so much that sums with a block or a page stay ints
 ER_DEV int pg_max_len(int table_stride, int page_rows) {

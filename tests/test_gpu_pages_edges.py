@@ -13,7 +13,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
-from test_gpu_pages import HALF, fine, host, ints, noise, paged  # noqa: E402
+from test_gpu_pages import HALF, Batch, fine, host, ints, noise, paged  # noqa: E402
 
 LEAST = {"f32": 2.0 ** -150, "f16": 2.0 ** -25, "bf16": 2.0 ** -134}  # half the smallest step of a type
 
@@ -66,3 +66,36 @@ def test_norm_of_rows_at_the_ends_of_the_range(style, hd, dtype, sizes, eps):
                  rope_style=style)
     assert torch.equal(same, q_out)
     fine(cache)
+
+
+def _batch(kind):
+    """A call of each attention kernel: a long sequence over all CTAs, and prompts of several blocks of rows."""
+    dtype, lens, new = {"decode_f32": ("f32", [9000, 70], [1, 1]), "decode_bf16": ("bf16", [9000, 70], [1, 1]),
+                        "prompt_f32": ("f32", [900, 300, 40], [400, 300, 1]),
+                        "prompt_bf16": ("bf16", [900, 300, 40], [400, 300, 1])}[kind]
+    return Batch(lens, new, 8, 2, 128, 16, dtype, seed=90)
+
+
+KINDS = ["decode_f32", "decode_bf16", "prompt_f32", "prompt_bf16"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_shortest_wait_limit(kind):
+    """Waits that give up at the first look: the result is right or flag bit 2 says that it is not, copies and products in
+    flight are waited for all the same, and after er_pages_error the next call is right."""
+    from block_quantized_token_gb300 import er
+    b = _batch(kind)
+    want, wz = b.run()
+    fine(b.cache)
+    er.er_set_wait_limit_ns(1)
+    try:
+        for _ in range(20):
+            out, lse = b.run()
+            _, code = b.cache.error()
+            assert code in (0, 4), code
+            assert code == 4 or torch.equal(out, want) and torch.equal(lse, wz)
+    finally:
+        er.er_set_wait_limit_ns(0)
+    out, lse = b.run()
+    assert torch.equal(out, want) and torch.equal(lse, wz)
+    fine(b.cache)
