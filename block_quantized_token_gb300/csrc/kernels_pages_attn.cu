@@ -160,6 +160,7 @@ struct PdArgs {
     int max_rows;  // sequences with as many query rows a KV head, or more, are another kernel's
     float *part;  // [CTAs][2] states of units that several CTAs share
     int *cnt;     // [CTAs] arrivals, zero between launches
+    int shortfall;  // tests of the give-up path: arrivals that CTA 0 waits for in vain
 };
 
 // the first row that any of a sequence's qn new tokens attends
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
     const int KV = P.p.KV, G = a.n_heads / KV, R = P.p.page_rows;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BARS) + warp * PD_SLOTS;
     uint8_t *ring = smem + warp * C::RING;
-    if (lane < PD_SLOTS) mbar_init(bars + lane, 1);
+    if (lane < PD_SLOTS) mbar_init(bars + lane, 1 + (blockIdx.x == 0 ? P.shortfall : 0));
     if (tid == 0) ms.wait_bad = 0;
     if (lane < 2) ms.seg[2 * warp + lane].off = -1;
     fence_mbar_init();
@@ -707,7 +708,10 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
     if (bad) {
         if (lane == 0) atomicOr(P.p.flags, ER_FLAG_WAIT);
         ms.wait_bad = 1;
-        // copies may still be landing
+        // copies may still be landing; an injected shortfall's arrivals are made up for, so that the barriers tell
+        if (blockIdx.x == 0 && lane < PD_SLOTS)
+            for (int k = 0; k < P.shortfall; ++k) pg_arrive(bars + lane);
+        __syncwarp();
         for (int k = max(0, inext - PD_SLOTS); k < inext; ++k) pg_drain(bars + k % PD_SLOTS, (k / PD_SLOTS) & 1);
     }
     __syncthreads();
@@ -886,14 +890,14 @@ static cudaError_t decode_t(const PdArgs &P, int num_sms, cudaStream_t st) {
 constexpr int PD_PROMPT_ROWS = 64;
 
 cudaError_t launch_pages_attention(const PagesView &p, const er_pages_attention_args &a, float *part, int *cnt,
-                                   int num_sms, cudaStream_t st) {
+                                   int shortfall, int num_sms, cudaStream_t st) {
     // The lengths are on the device, so the split is made there, sequence by sequence; here only what the sizes
     // rule out: no sequence that long, or (at most a token each on average) a decode step, which stays one launch.
     const bool prompts = (long long)a.n_tokens * (a.n_heads / p.KV) >= PD_PROMPT_ROWS && (a.n_tokens > a.n_seqs || a.n_seqs == 1);
     if (prompts)
-        if (cudaError_t e = launch_pages_prompt(p, a, PD_PROMPT_ROWS, st); e != cudaSuccess) return e;
+        if (cudaError_t e = launch_pages_prompt(p, a, PD_PROMPT_ROWS, shortfall, st); e != cudaSuccess) return e;
     for (int b = 0; b < a.n_seqs; b += PD_SEQS) {
-        PdArgs P = {p, a, prompts ? PD_PROMPT_ROWS : 2147483647, part, cnt};
+        PdArgs P = {p, a, prompts ? PD_PROMPT_ROWS : 2147483647, part, cnt, shortfall};
         P.a.n_seqs = a.n_seqs - b < PD_SEQS ? a.n_seqs - b : PD_SEQS;
         P.a.q_start_dev += b;
         P.a.lens_dev += b;

@@ -75,6 +75,7 @@ struct PpArgs {
     PagesView p;
     er_pages_attention_args a;
     int min_rows;  // sequences with fewer query rows a KV head are another kernel's
+    int shortfall;  // tests of the give-up path: arrivals that CTA 0 waits for in vain
 };
 
 struct PpBars {
@@ -125,9 +126,6 @@ ER_DEV uint32_t pp_elect() {
     asm volatile(
         "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
     return one;
-}
-ER_DEV void pp_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // 32 consecutive 32-bit columns of this thread's lane
 ER_DEV void pp_st32(uint32_t taddr, const uint32_t *v) {
@@ -490,15 +488,15 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
         else keys(std::false_type{}, raw, kd);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) pp_arrive(B.kfull + st);
+        if (lane == 0) pg_arrive(B.kfull + st);
         if (j >= 2) ok = wait(B.vempty + st, ph ^ 1);
         if (!ok) break;
         if (edge) vals(std::true_type{}, raw, vd, r0);
         else vals(std::false_type{}, raw, vd, r0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) pp_arrive(B.vfull + st);
-        if (lane == 0) pp_arrive(B.rawfree + slot);
+        if (lane == 0) pg_arrive(B.vfull + st);
+        if (lane == 0) pg_arrive(B.rawfree + slot);
         slot += 2;
         if (slot >= PP_RAW) {
             slot -= PP_RAW;
@@ -550,14 +548,14 @@ ER_DEV void pp_copies(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem &I
 
 // barriers (thread 0) and the whole of TMEM (warp 12)
 // query_warps, softmax_warps: warps that make the queries' operands, and that share a tile's P
-ER_DEV void pp_setup(PpBars &B, int tid, int warp, int query_warps, int softmax_warps) {
+ER_DEV void pp_setup(PpBars &B, int tid, int warp, int query_warps, int softmax_warps, int shortfall) {
     if (tid == 0) {
         for (int i = 0; i < PP_RAW; ++i) {
             mbar_init(B.raw + i, 1);
             mbar_init(B.rawfree + i, 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(B.kfull + i, 4);
+            mbar_init(B.kfull + i, 4 + (blockIdx.x == 0 ? shortfall : 0));
             mbar_init(B.kempty + i, 1);
             mbar_init(B.vfull + i, 4);
             mbar_init(B.vempty + i, 1);
@@ -700,7 +698,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
     PpItem I;
     if (!pp_find<256>(P, B, warp, lane, I)) return;
     const int nx = I.nf > 128 ? 2 : 1;  // tiles
-    pp_setup(B, tid, warp, 4 * nx, 4);
+    pp_setup(B, tid, warp, 4 * nx, 4, P.shortfall);
     // a softmax thread's tile and row
     const int X = warp >> 2, r = tid & 127, f = I.f0 + X * 128 + r, tok = f / G;
     const int row = I.q0 + tok, head = I.h * G + (f - tok * G);
@@ -721,7 +719,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                                          32 * (warp & 3), lane);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) pp_arrive(&B.q);
+            if (lane == 0) pg_arrive(&B.q);
             const float down = rows[r];
             bool ok = true;
             for (int j = 0; j < I.nblk; ++j) {
@@ -757,7 +755,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 pp_wait_st();
                 pp_fence_before();
                 __syncwarp();
-                if (lane == 0) pp_arrive(B.p + X);
+                if (lane == 0) pg_arrive(B.p + X);
             }
             if (ok) ok = I.nblk > 0 ? wait(B.o + X, 0) : wait(&B.q, 0);  // the queries' place is free
             if (ok) {
@@ -841,7 +839,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
     const int G = a.n_heads / P.p.KV;
     PpItem I;
     if (!pp_find<128>(P, B, warp, lane, I)) return;
-    pp_setup(B, tid, warp, 8, 8);
+    pp_setup(B, tid, warp, 8, 8, P.shortfall);
     // warps 0-3 and 4-7: thread = query row, W = which half of its columns
     const int r = tid & 127, W = warp >> 2, f = I.f0 + r, tok = f / G;
     const int row = I.q0 + tok, head = I.h * G + (f - tok * G);
@@ -868,7 +866,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
                                         row0, lane);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) pp_arrive(&B.q);
+        if (lane == 0) pg_arrive(&B.q);
         bool ok = wait(&B.q, 0);
         const float down = xch[256 + r];
         auto gather = [&](int j) {  // o = o * factor + O of block j
@@ -889,7 +887,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             }
             pp_fence_before();
             __syncwarp();
-            if (lane == 0) pp_arrive(B.oempty + buf);
+            if (lane == 0) pg_arrive(B.oempty + buf);
             return true;
         };
         for (int j = 0; ok && j < I.nblk; ++j) {
@@ -910,7 +908,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             xch[buf * 256 + W * 128 + r] = mine;
             pp_fence_before();
             __syncwarp();
-            if (lane == 0) pp_arrive(B.x + buf);
+            if (lane == 0) pg_arrive(B.x + buf);
             ok = wait(B.x + buf, ph);
             if (!ok) break;
             pp_fence_after();
@@ -923,7 +921,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             pp_wait_st();
             pp_fence_before();
             __syncwarp();
-            if (lane == 0) pp_arrive(B.p + buf);
+            if (lane == 0) pg_arrive(B.p + buf);
             if (j > 0) {
                 ok = gather(j - 1);
                 if (!ok) break;
@@ -935,7 +933,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             const int buf = I.nblk & 1;
             xch[buf * 256 + W * 128 + r] = l;
             __syncwarp();
-            if (lane == 0) pp_arrive(B.x + buf);
+            if (lane == 0) pg_arrive(B.x + buf);
             ok = wait(B.x + buf, (I.nblk >> 1) & 1);
         }
         if (ok) {
@@ -1024,8 +1022,9 @@ static cudaError_t prompt_t(const PpArgs &P, unsigned grid, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_pages_prompt(const PagesView &p, const er_pages_attention_args &a, int min_rows, cudaStream_t st) {
-    const PpArgs P = {p, a, min_rows};
+cudaError_t launch_pages_prompt(const PagesView &p, const er_pages_attention_args &a, int min_rows, int shortfall,
+                                cudaStream_t st) {
+    const PpArgs P = {p, a, min_rows, shortfall};
     const long long G = a.n_heads / p.KV, rows = a.type == ER_F32 ? 128 : 256;  // query rows of a CTA
     const long long items = ((long long)a.n_tokens * G + rows - 1) / rows + (a.n_seqs < a.n_tokens ? a.n_seqs : a.n_tokens);
     if (items * p.KV > 2147483647ll) return cudaErrorInvalidValue;

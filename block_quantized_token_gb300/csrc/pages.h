@@ -26,11 +26,12 @@ cudaError_t launch_pages_append(const PagesView &p, const er_pages_append_args &
 cudaError_t launch_pages_read(const PagesView &p, int n, const int32_t *slots, int type, void *k, void *v,
                               cudaStream_t st);
 cudaError_t launch_pages_attention(const PagesView &p, const er_pages_attention_args &a, float *part, int *cnt,
-                                   int num_sms, cudaStream_t st);
+                                   int shortfall, int num_sms, cudaStream_t st);
 size_t pages_attn_part_floats(int num_sms);  // `part`; cnt: one int per SM, zero
 cudaError_t pages_attn_prepare();            // kernel attributes
 // sequences with at least min_rows query rows a KV head (kernels_pages_prompt.cu)
-cudaError_t launch_pages_prompt(const PagesView &p, const er_pages_attention_args &a, int min_rows, cudaStream_t st);
+cudaError_t launch_pages_prompt(const PagesView &p, const er_pages_attention_args &a, int min_rows, int shortfall,
+                                cudaStream_t st);
 cudaError_t pages_prompt_prepare();
 cudaError_t set_wait_limit_prompt(unsigned long long ns);
 cudaError_t set_wait_limit_pages(unsigned long long ns);
@@ -45,5 +46,6 @@ struct er_pages {
     int *flags;   // er_pages_error
     int *ticket;  // arrival counter of the plan kernel (zero between launches)
     int *cnt;     // arrival counters of the attention kernel [SMs] (zero between launches)
+    int shortfall;  // er_pages_inject_wait_shortfall
     float *part;  // states of units shared by several CTAs (pages_attn_part_floats)
 };

@@ -94,6 +94,7 @@ er_status er_pages_create(const er_pages_config *cfg, void *pool, er_pages **out
     p->layer_bytes = layer_bytes(cfg);
     p->flags = p->ticket = p->cnt = nullptr;
     p->part = nullptr;
+    p->shortfall = 0;
     cudaError_t e = cudaGetDevice(&p->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device);
     if (e == cudaSuccess) e = pages_attn_prepare();
@@ -226,7 +227,15 @@ er_status er_pages_attention(er_pages *p, int32_t layer, const er_pages_attentio
         return er_fail_status(ER_EINVAL, "rows must be aligned to their type");
     if (a->out_dev == a->q_dev && a->out_stride != a->q_stride)
         return er_fail_status(ER_EINVAL, "out may be q only with the same stride");
-    return done(launch_pages_attention(view_of(p, layer), *a, p->part, p->cnt, p->num_sms, (cudaStream_t)stream), "er_pages_attention");
+    return done(launch_pages_attention(view_of(p, layer), *a, p->part, p->cnt, p->shortfall, p->num_sms, (cudaStream_t)stream),
+                "er_pages_attention");
+}
+
+er_status er_pages_inject_wait_shortfall(er_pages *p, int32_t extra) {
+    if (!p) return er_fail_status(ER_EINVAL, "handle is NULL");
+    if (extra < 0 || extra > 1024) return er_fail_status(ER_EINVAL, "extra must be in 0..1024");
+    p->shortfall = extra;
+    return ER_OK;
 }
 
 er_status er_pages_error(er_pages *p, int32_t *code) {

@@ -120,6 +120,7 @@ def _load() -> ctypes.CDLL:
         "er_pages_append": (I32, [VP, I32, P(er_pages_append_args), VP]),
         "er_pages_read": (I32, [VP, I32, I32, VP, I32, VP, VP, VP]),
         "er_pages_attention": (I32, [VP, I32, P(er_pages_attention_args), VP]),
+        "er_pages_inject_wait_shortfall": (I32, [VP, I32]),
         "er_pages_error": (I32, [VP, P(I32)]),
         "er_gguf_open": (I32, [ctypes.c_char_p, P(VP)]),
         "er_gguf_close": (None, [VP]),
@@ -150,7 +151,8 @@ EXPORTED = ("er_model_create", "er_model_destroy", "er_model_device_bytes", "er_
             "er_gguf_tensor_count", "er_gguf_tensor_info", "er_gguf_find", "er_gguf_config",
             "er_model_create_from_gguf", "er_kv_create_typed", "er_kv_type", "er_kv_read_blocks", "er_prefill", "er_pages_pool_bytes",
             "er_pages_create", "er_pages_destroy", "er_pages_plan", "er_pages_release", "er_rope_table",
-            "er_pages_append", "er_pages_read", "er_pages_attention", "er_pages_error", "er_status_str",
+            "er_pages_append", "er_pages_read", "er_pages_attention", "er_pages_inject_wait_shortfall", "er_pages_error",
+            "er_status_str",
             "er_last_error")
 
 
@@ -366,6 +368,10 @@ def er_pages_read(pages: int, layer: int, n: int, slots: int | None, type: int, 
 
 def er_pages_attention(pages: int, layer: int, args: er_pages_attention_args, stream: int = 0) -> None:
     _check(_lib.er_pages_attention(pages, layer, args, stream), "er_pages_attention")
+
+
+def er_pages_inject_wait_shortfall(pages: int, extra: int) -> None:
+    _check(_lib.er_pages_inject_wait_shortfall(pages, extra), "er_pages_inject_wait_shortfall")
 
 
 def er_pages_error(pages: int) -> tuple[int, int]:

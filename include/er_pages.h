@@ -172,10 +172,18 @@ typedef struct {
 } er_pages_attention_args;
 ER_API er_status er_pages_attention(er_pages *p, int32_t layer, const er_pages_attention_args *a, void *stream);
 
+/* Failure injection for tests of the bounded waits, as er_kv_inject_wait_shortfall
+ * for the paged attention: with extra > 0 the first CTA of each of its kernels waits,
+ * in calls made (or captured) from then on, for `extra` more arrivals than there are.
+ * The wait runs out (er_set_wait_limit_ns) and the kernel returns.  extra = 0 (the
+ * default) restores normal calls.  ER_EINVAL outside 0..1024. */
+ER_API er_status er_pages_inject_wait_shortfall(er_pages *p, int32_t extra);
+
 /* Synchronises the device, then reports and clears the handle's flags: bit 0: a
  * request was not admitted (pages or rows ran out), bit 1: a length, position,
  * slot or table entry was out of range, bit 2: a wait inside a kernel gave up
- * (internal error).  Returns ER_EDEVICE if *code != 0, else ER_OK. */
+ * (internal error): what that attention and any later one of the handle wrote before
+ * this call is unspecified.  Returns ER_EDEVICE if *code != 0, else ER_OK. */
 ER_API er_status er_pages_error(er_pages *p, int32_t *code);
 
 #ifdef __cplusplus

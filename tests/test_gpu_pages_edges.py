@@ -99,3 +99,42 @@ def test_shortest_wait_limit(kind):
     out, lse = b.run()
     assert torch.equal(out, want) and torch.equal(lse, wz)
     fine(b.cache)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_wait_gives_up_and_the_next_call_is_right(kind):
+    """One CTA's wait runs out: every kernel returns, bit 2 is reported, and er_pages_error puts right what the CTAs that
+    shared a sequence with it had counted."""
+    import time
+
+    from block_quantized_token_gb300 import er
+    b = _batch(kind)
+    want, wz = b.run()
+    fine(b.cache)
+    er.er_set_wait_limit_ns(5_000_000)
+    er.er_pages_inject_wait_shortfall(b.cache.handle, 1)
+    try:
+        for _ in range(3):
+            t0 = time.perf_counter()
+            b.run()
+            torch.cuda.synchronize()
+            elapsed = time.perf_counter() - t0
+            st, code = b.cache.error()
+            assert st == er.ER_EDEVICE and code == 4, (st, code)
+            assert elapsed < 0.5, f"gave up after {elapsed:.3f} s with a 5 ms limit"
+    finally:
+        er.er_pages_inject_wait_shortfall(b.cache.handle, 0)
+        er.er_set_wait_limit_ns(0)
+    for _ in range(3):
+        out, lse = b.run()
+        assert torch.equal(out, want) and torch.equal(lse, wz)
+    fine(b.cache)
+
+
+def test_shortfall_refusals():
+    from block_quantized_token_gb300 import er
+    cache = paged(4, 16, 2, 64)
+    for handle, extra in ((cache.handle, -1), (cache.handle, 1025), (None, 0)):
+        with pytest.raises(er.ErError) as e:
+            er.er_pages_inject_wait_shortfall(handle, extra)
+        assert e.value.status == er.ER_EINVAL
