@@ -733,7 +733,7 @@ ER_DEV void append_v(const AppendArgs &A, uint32_t (&cw)[16][HD / 8 + 2], unsign
     const bool starts = there && (slot % 16 == 0 || slot != prev + 1 || !good(prev, ppos));
     const unsigned sm = __ballot_sync(0xffffffffu, starts), tm = __ballot_sync(0xffffffffu, there);
     // the runs that start among the chunk's tokens (one may reach past it, up to 15 tokens on)
-    for (unsigned left = sm & (A.chunk == 32 ? 0xffffffffu : (1u << A.chunk) - 1u); left; left &= left - 1) {
+    for (unsigned left = sm & ((1u << A.chunk) - 1u); left; left &= left - 1) {
         const int first = __ffs(left) - 1;
         const unsigned stop = (sm | ~tm) & ~((2u << first) - 1u);  // the next start, or the next token without a row
         const int n = min((stop ? __ffs(stop) - 1 : 32) - first, 16);
@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(256) pages_read_kernel(PagesView p, int n, con
     }
     if (v) {
         // dims 8 c .. + 7: nibbles c & 1 of 8 bytes, 64 apart
-        const uint8_t *src = tile + pg_off_v(HD) + pg_v_byte(r, 8 * (c >> 1), HD);
+        const uint8_t *src = tile + pg_off_v(HD) + pg_v_byte(r, 8 * (c >> 1));
         const float d = __half2float(reinterpret_cast<const __half *>(tile + pg_off_vs(HD))[pg_vs_half(r, c >> 2, HD)]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = d * (float)((int)((src[64 * j] >> (4 * (c & 1))) & 15) - 8);

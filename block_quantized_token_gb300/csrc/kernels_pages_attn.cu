@@ -104,28 +104,10 @@ struct PdMisc {
     int last[2];
 };
 
-ER_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-ER_DEV uint32_t h2_mul(uint32_t a, uint32_t b) {
-    __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
-    return *reinterpret_cast<uint32_t *>(&r);
-}
-ER_DEV uint32_t pd_pack(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 ER_DEV void pd_split(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pd_pack(a, b);
+    hi = pg_pack(a, b);
     const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    lo = pd_pack(a - h.x, b - h.y);
-}
-// nibble n of each half of w (bits 4 n ..) as the fp16 pair 16 + c
-template <int N>
-ER_DEV uint32_t pd_code(uint32_t w) {
-    return lop3_and_or(N == 0 ? w << 6 : N == 1 ? w << 2 : N == 2 ? w >> 2 : w >> 6, 0x03C003C0u, 0x4C004C00u);
+    lo = pg_pack(a - h.x, b - h.y);
 }
 ER_DEV uint32_t h2_add(uint32_t a, uint32_t b) {
     __half2 r = __hadd2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
@@ -134,7 +116,6 @@ ER_DEV uint32_t h2_add(uint32_t a, uint32_t b) {
 // nibble 0 / 1 of each half of w as the fp16 pair c - 8: 1024 + c or 64 + c as a mask leaves it, less 1032 or 72
 ER_DEV uint32_t pd_low(uint32_t w) { return h2_add(lop3_and_or(w, 0x000F000Fu, 0x64006400u), 0xE408E408u); }
 ER_DEV uint32_t pd_high(uint32_t w) { return h2_add(lop3_and_or(w, 0x00F000F0u, 0x54005400u), 0xD480D480u); }
-constexpr uint32_t PD_M24 = 0xCE00CE00u;  // half2(-24, -24)
 // d += A B without volatile: the compiler may move it between the loads and conversions of other tiles
 ER_DEV void pd_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -428,7 +409,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                     if constexpr (Y::QLO) {
                         pd_split(x0, x1, qh[2 * bb + (i >> 1)][i & 1], ql[2 * bb + (i >> 1)][i & 1]);
                     } else {
-                        qh[2 * bb + (i >> 1)][i & 1] = pd_pack(x0, x1);
+                        qh[2 * bb + (i >> 1)][i & 1] = pg_pack(x0, x1);
                     }
                 }
             }
@@ -485,12 +466,12 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
 #pragma unroll
                     for (int bb = 0; bb < C::NB; ++bb) {
                         const uint32_t w0 = kw[0][bb], w1 = kw[1][bb];
-                        const uint32_t d0 = prmt(ks[0][bb >> 1], 0u, (bb & 1) ? 0x3232u : 0x1010u), z0 = h2_mul(d0, PD_M24);
-                        const uint32_t d1 = prmt(ks[1][bb >> 1], 0u, (bb & 1) ? 0x3232u : 0x1010u), z1 = h2_mul(d1, PD_M24);
-                        const uint32_t a0[4] = {h2_fma(pd_code<0>(w0), d0, z0), h2_fma(pd_code<0>(w1), d1, z1),
-                                                h2_fma(pd_code<1>(w0), d0, z0), h2_fma(pd_code<1>(w1), d1, z1)};
-                        const uint32_t a1[4] = {h2_fma(pd_code<2>(w0), d0, z0), h2_fma(pd_code<2>(w1), d1, z1),
-                                                h2_fma(pd_code<3>(w0), d0, z0), h2_fma(pd_code<3>(w1), d1, z1)};
+                        const uint32_t d0 = prmt(ks[0][bb >> 1], 0u, (bb & 1) ? 0x3232u : 0x1010u), z0 = pg_m24(d0);
+                        const uint32_t d1 = prmt(ks[1][bb >> 1], 0u, (bb & 1) ? 0x3232u : 0x1010u), z1 = pg_m24(d1);
+                        const uint32_t a0[4] = {h2_fma(pg_code<0>(w0), d0, z0), h2_fma(pg_code<0>(w1), d1, z1),
+                                                h2_fma(pg_code<1>(w0), d0, z0), h2_fma(pg_code<1>(w1), d1, z1)};
+                        const uint32_t a1[4] = {h2_fma(pg_code<2>(w0), d0, z0), h2_fma(pg_code<2>(w1), d1, z1),
+                                                h2_fma(pg_code<3>(w0), d0, z0), h2_fma(pg_code<3>(w1), d1, z1)};
                         pd_mma(sc, a0, qh[2 * bb][0], qh[2 * bb][1]);
                         pd_mma(part, a1, qh[2 * bb + 1][0], qh[2 * bb + 1][1]);
                         if constexpr (Y::QLO) {
@@ -534,7 +515,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
                     const float mn = mt > m[c] + PD_SLACK ? mt : m[c];
-                    const float corr = mn == m[c] ? 1.f : ex2(m[c] - mn);
+                    const float corr = mn == m[c] ? 1.f : pg_ex2(m[c] - mn);
                     l[c] *= corr;
 #pragma unroll
                     for (int j = 0; j < HD / 16; ++j) {
@@ -550,7 +531,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
             for (int n = 0; n < 2; ++n) {
                 float p[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) p[k] = ex2(x[n][k] - (m[k & 1] - PD_UP));
+                for (int k = 0; k < 4; ++k) p[k] = pg_ex2(x[n][k] - (m[k & 1] - PD_UP));
                 l[0] += p[0] + p[2];
                 l[1] += p[1] + p[3];
 #pragma unroll
@@ -594,12 +575,12 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                 }
 #pragma unroll
                 for (int bb = 0; bb < C::NB; ++bb) {
-                    const uint32_t d0 = vd[bb][0], d1 = vd[bb][1], z0 = h2_mul(d0, PD_M24), z1 = h2_mul(d1, PD_M24);
+                    const uint32_t d0 = vd[bb][0], d1 = vd[bb][1], z0 = pg_m24(d0), z1 = pg_m24(d1);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const uint32_t w = vw[bb >> 1][2 * (bb & 1) + u];
-                        const uint32_t va[4] = {h2_fma(pd_code<0>(w), d0, z0), h2_fma(pd_code<1>(w), d0, z0),
-                                                h2_fma(pd_code<2>(w), d1, z1), h2_fma(pd_code<3>(w), d1, z1)};
+                        const uint32_t va[4] = {h2_fma(pg_code<0>(w), d0, z0), h2_fma(pg_code<1>(w), d0, z0),
+                                                h2_fma(pg_code<2>(w), d1, z1), h2_fma(pg_code<3>(w), d1, z1)};
                         if constexpr (Y::QLO) {
                             float sum[4] = {0.f, 0.f, 0.f, 0.f};
                             pd_mma(sum, va, ph[n][0], ph[n][1]);
@@ -760,7 +741,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
         const float own = M;
 #pragma unroll
         for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        const float f = lane < ne ? ex2(own - M) : 0.f;
+        const float f = lane < ne ? pg_ex2(own - M) : 0.f;
         float L = lane < ne ? f * mine[PD_ROWS * HD + 8 + r] : 0.f;
 #pragma unroll
         for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
@@ -837,7 +818,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                 }
 #pragma unroll
                 for (int k2 = 0; k2 < 4; ++k2) {
-                    const float w = c0_ + k2 * parts < nc ? ex2(f[k2] - M) : 0.f;
+                    const float w = c0_ + k2 * parts < nc ? pg_ex2(f[k2] - M) : 0.f;
                     if (c0_ + k2 * parts < nc) {
                         L += w * ll[k2];
 #pragma unroll

@@ -166,11 +166,6 @@ ER_DEV void pp_wait_ld(float *v) {
                  :
                  : "memory");
 }
-ER_DEV float pp_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // two fp32 operations an instruction
 ER_DEV float2 pp_fma2(float2 a, float2 b, float2 c) {
     uint64_t d;
@@ -189,25 +184,14 @@ ER_DEV float pp_max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-ER_DEV uint32_t pp_pack(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-// nibble N of each half of w (bits 4 N ..) as the fp16 pair 16 + c, and c's value with scale pair d, z = -24 d
+// values of nibble N of each half of w with scale pair d, z = -24 d
 template <int N>
 ER_DEV uint32_t pp_val(uint32_t w, uint32_t d, uint32_t z) {
-    return h2_fma(lop3_and_or(N == 0 ? w << 6 : N == 1 ? w << 2 : N == 2 ? w >> 2 : w >> 6, 0x03C003C0u, 0x4C004C00u), d, z);
+    return h2_fma(pg_code<N>(w), d, z);
 }
-ER_DEV uint32_t pp_m24(uint32_t d) {
-    __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&d), __halves2half2(__ushort_as_half(0xCE00), __ushort_as_half(0xCE00)));
-    return *reinterpret_cast<uint32_t *>(&r);
-}
-// row of a block at place k' (see the header) and the place of row r
+// row of a block at place k' (see the header)
 __host__ __device__ constexpr int pp_row(int k) {
     return (k & ~31) + ((k >> 2) & 1) * 16 + ((k >> 1) & 1) * 8 + ((k >> 3) & 3) * 2 + (k & 1);
-}
-__host__ __device__ constexpr int pp_place(int r) {
-    return (r & ~31) + ((r >> 1) & 3) * 8 + ((r >> 4) & 1) * 4 + ((r >> 3) & 1) * 2 + (r & 1);
 }
 
 // What a CTA works on: query rows f0 .. f0 + nf - 1 of sequence b, KV head h, against rows any_lo .. any_hi (those that
@@ -343,10 +327,10 @@ ER_DEV void pp_queries(const er_pages_attention_args &a, uint8_t *dst, float *do
 #pragma unroll
         for (int k = 0; k < V / 2; ++k) {
             const float y0 = x[2 * k] * up, y1 = x[2 * k + 1] * up;
-            hi[k] = pp_pack(y0, y1);
+            hi[k] = pg_pack(y0, y1);
             if constexpr (LO) {
                 const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
-                lo[k] = pp_pack(y0 - z.x, y1 - z.y);
+                lo[k] = pg_pack(y0 - z.x, y1 - z.y);
             }
         }
         uint8_t *d = place(r, V * c / 8);
@@ -408,7 +392,7 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
             const uint32_t ch = kch ^ (uint32_t)(at << 4);
 #pragma unroll
             for (int k = 0; k < C::NB; ++k) {
-                const uint32_t d = prmt(ds[k >> 1], 0u, (k & 1) ? sel1 : sel0), z = pp_m24(d);
+                const uint32_t d = prmt(ds[k >> 1], 0u, (k & 1) ? sel1 : sel0), z = pg_m24(d);
                 *reinterpret_cast<uint4 *>(dst + (k >> 1) * 16384 + (ch ^ ((k & 1) * 64u))) =
                     make_uint4(pp_val<0>(w[k], d, z), pp_val<1>(w[k], d, z), pp_val<2>(w[k], d, z), pp_val<3>(w[k], d, z));
             }
@@ -461,7 +445,7 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 const uint32_t a0 = da[u >> 1][0], a1 = da[u >> 1][1], b0 = db[u >> 1][0], b1 = db[u >> 1][1];
-                const uint32_t za0 = pp_m24(a0), za1 = pp_m24(a1), zb0 = pp_m24(b0), zb1 = pp_m24(b1);
+                const uint32_t za0 = pg_m24(a0), za1 = pg_m24(a1), zb0 = pg_m24(b0), zb1 = pg_m24(b1);
                 const int d = 64 * q + 16 * (u0 + u) + g;
                 *reinterpret_cast<uint4 *>(dst + d * 128) =
                     make_uint4(pp_val<0>(wa[u], a0, za0), pp_val<2>(wa[u], a1, za1), pp_val<0>(wb[u], b0, zb0),
@@ -638,12 +622,12 @@ ER_DEV float pp_probabilities(const float (&s)[N], uint32_t tP, float down, floa
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             float2 x = pp_fma2(make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), dn, nb);
-            x.x = pp_ex2(x.x);
-            x.y = pp_ex2(x.y);
+            x.x = pg_ex2(x.x);
+            x.y = pg_ex2(x.y);
             sum[k & 1] = pp_add2(sum[k & 1], x);
-            ph[k] = pp_pack(x.x, x.y);
+            ph[k] = pg_pack(x.x, x.y);
             const float2 z = pp_fma2(__half22float2(*reinterpret_cast<const __half2 *>(&ph[k])), make_float2(-1.f, -1.f), x);
-            pl[k] = pp_pack(z.x, z.y);
+            pl[k] = pg_pack(z.x, z.y);
         }
         pp_st16(tP + 16 * q, ph);
         pp_st16(tP + 64 + 16 * q, pl);
@@ -736,7 +720,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 const float mt = pp_largest(s) * down;
                 if (__any_sync(0xffffffffu, mt > m + PP_SLACK)) {
                     const float mn = mt > m + PP_SLACK ? mt : m;
-                    const float corr = mn == m ? 1.f : pp_ex2(m - mn);
+                    const float corr = mn == m ? 1.f : pg_ex2(m - mn);
                     l *= corr;
                     m = mn;
                     if (j > 0) {
@@ -914,7 +898,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             pp_fence_after();
             const float mt = fmaxf(mine, xch[buf * 256 + (W ^ 1) * 128 + r]);
             const float mn = mt > m + PP_SLACK ? mt : m;
-            const float corr = mn == m ? 1.f : pp_ex2(m - mn);
+            const float corr = mn == m ? 1.f : pg_ex2(m - mn);
             l *= corr;
             m = mn;
             l += pp_probabilities(s, tS + 32 * W, down, m);

@@ -31,9 +31,8 @@ __host__ __device__ constexpr int pg_off_vs(int hd) { return 17 * hd; }
 
 // byte of a tile that holds dims d and (V) d + 8 / (K) the code of dim d of row r; nibble: its bits
 __host__ __device__ inline int pg_k_word(int r, int w, int hd) { return r * (hd / 2) + 4 * w; }  // word w of row r
-__host__ __device__ inline int pg_v_byte(int r, int j, int hd) {  // byte of dims 16 (j / 8) + j % 8 and + 8, j < hd / 2
+__host__ __device__ inline int pg_v_byte(int r, int j) {  // byte of dims 16 (j / 8) + j % 8 and + 8, j < hd / 2
     const int q = j >> 5, u = (j >> 3) & 3, g = j & 7, t = (r & 7) >> 1, e = r & 1, i = r >> 3;
-    (void)hd;
     return ((((q * 8 + g) * 4 + t) * 4) + u) * 4 + i + 2 * e;
 }
 __host__ __device__ inline int pg_vs_half(int r, int b, int hd) {  // index of the V scale of (row r, block b)
@@ -51,10 +50,6 @@ ER_DEV float pg_scale(float m) {
     const float d = __bfloat162float(__float2bfloat16_rn(m * -0.125f));
     if (isnan(d)) return d;
     return __half2float(__float2half_rn(fminf(fmaxf(d, -PG_DMAX), PG_DMAX)));
-}
-ER_DEV int pg_code(float x, float d) {
-    if (!(d != 0.f) || isnan(d)) return 8;
-    return (int)fminf(fmaxf(roundf(x / d) + 8.f, 0.f), 15.f);
 }
 
 // one value of a row of `type` (ER_F32, ER_F16, ER_BF16) by its index
@@ -84,6 +79,26 @@ ER_DEV void pg_drain(uint64_t *bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < ER_WAIT_NS) {
     }
+}
+
+ER_DEV float pg_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+ER_DEV uint32_t pg_pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// nibble N of each half of w (bits 4 N ..) as the fp16 pair 16 + c; fma(that, d, pg_m24(d)) are the values of scale pair d
+template <int N>
+ER_DEV uint32_t pg_code(uint32_t w) {
+    return lop3_and_or(N == 0 ? w << 6 : N == 1 ? w << 2 : N == 2 ? w >> 2 : w >> 6, 0x03C003C0u, 0x4C004C00u);
+}
+ER_DEV uint32_t pg_m24(uint32_t d) {
+    const uint32_t m = 0xCE00CE00u;  // half2(-24, -24)
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&d), *reinterpret_cast<const __half2 *>(&m));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 constexpr int PG_MAX_LEN = 2147483647 - 1024;
