@@ -691,7 +691,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
         ms.wait_bad = 1;
         // copies may still be landing; an injected shortfall's arrivals are made up for, so that the barriers tell
         if (blockIdx.x == 0 && lane < PD_SLOTS)
-            for (int k = 0; k < P.shortfall; ++k) pg_arrive(bars + lane);
+            for (int k = 0; k < P.shortfall; ++k) mbar_arrive(bars + lane);
         __syncwarp();
         for (int k = max(0, inext - PD_SLOTS); k < inext; ++k) pg_drain(bars + k % PD_SLOTS, (k / PD_SLOTS) & 1);
     }

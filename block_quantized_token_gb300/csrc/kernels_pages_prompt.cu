@@ -88,13 +88,6 @@ static_assert(sizeof(PpBars) <= 512, "barriers");
 // ---------------------------------------------------------------------------
 // tcgen05 wrappers
 // ---------------------------------------------------------------------------
-ER_DEV void pp_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-ER_DEV void pp_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// K-major operand, 128-byte swizzle: atoms of 8 rows x 128 bytes, 1024 bytes apart
-ER_DEV uint64_t pp_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
 // kind::f16: fp16 A and B (both K-major), fp32 D, M = 128
 constexpr uint32_t pp_idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24); }
 // The products are issued by code that the whole warp runs with equal operands (so they can sit in uniform
@@ -472,15 +465,15 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
         else keys(std::false_type{}, raw, kd);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) pg_arrive(B.kfull + st);
+        if (lane == 0) mbar_arrive(B.kfull + st);
         if (j >= 2) ok = wait(B.vempty + st, ph ^ 1);
         if (!ok) break;
         if (edge) vals(std::true_type{}, raw, vd, r0);
         else vals(std::false_type{}, raw, vd, r0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) pg_arrive(B.vfull + st);
-        if (lane == 0) pg_arrive(B.rawfree + slot);
+        if (lane == 0) mbar_arrive(B.vfull + st);
+        if (lane == 0) mbar_arrive(B.rawfree + slot);
         slot += 2;
         if (slot >= PP_RAW) {
             slot -= PP_RAW;
@@ -558,16 +551,16 @@ ER_DEV void pp_setup(PpBars &B, int tid, int warp, int query_warps, int softmax_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pp_fence_before();
+    tc_fence_before();
     __syncthreads();
-    pp_fence_after();
+    tc_fence_after();
 }
 ER_DEV void pp_close(PpBars &B, int warp) {
     __syncwarp();
-    pp_fence_before();
+    tc_fence_before();
     __syncthreads();
     if (warp == 12) {
-        pp_fence_after();
+        tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(B.tmem), "r"(512) : "memory");
     }
 }
@@ -580,7 +573,7 @@ ER_DEV void pp_score(uint32_t d, uint32_t q, uint32_t k, bool more, uint32_t one
 #pragma unroll
     for (int i = 0; i < HD / 16; ++i) {
         const uint32_t at = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32);
-        pp_mma_ss(d, pp_desc(q) + (at >> 4), pp_desc(k) + (at >> 4), pp_idesc(128), more || i > 0, one);
+        pp_mma_ss(d, tc_desc_sw128(q) + (at >> 4), tc_desc_sw128(k) + (at >> 4), pp_idesc(128), more || i > 0, one);
     }
 }
 // P's lo halves lie 64 columns after the hi ones
@@ -588,7 +581,7 @@ template <int HD>
 ER_DEV void pp_value(uint32_t d, uint32_t p, uint32_t v, bool more, uint32_t one) {
 #pragma unroll
     for (int i = 0; i < PP_BLOCK / 16; ++i) {
-        const uint64_t b = pp_desc(v) + (((i >> 2) * (HD * 128) + (i & 3) * 32) >> 4);
+        const uint64_t b = tc_desc_sw128(v) + (((i >> 2) * (HD * 128) + (i & 3) * 32) >> 4);
         pp_mma_ts(d, p + i * 8, b, pp_idesc(HD), more || i > 0, one);
         pp_mma_ts(d, p + 64 + i * 8, b, pp_idesc(HD), 1, one);
     }
@@ -703,13 +696,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                                          32 * (warp & 3), lane);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) pg_arrive(&B.q);
+            if (lane == 0) mbar_arrive(&B.q);
             const float down = rows[r];
             bool ok = true;
             for (int j = 0; j < I.nblk; ++j) {
                 ok = wait(B.s + X, j & 1);
                 if (!ok) break;
-                pp_fence_after();
+                tc_fence_after();
                 float s[128];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) pp_ld32(tS + 32 * k, s + 32 * k);
@@ -737,13 +730,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 }
                 l += pp_probabilities(s, tS, down, m);
                 pp_wait_st();
-                pp_fence_before();
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pg_arrive(B.p + X);
+                if (lane == 0) mbar_arrive(B.p + X);
             }
             if (ok) ok = I.nblk > 0 ? wait(B.o + X, 0) : wait(&B.q, 0);  // the queries' place is free
             if (ok) {
-                pp_fence_after();
+                tc_fence_after();
                 const float inv = 1.f / l;
                 // the row once more, from shared memory: it would cost registers in the loop
                 const volatile int *item = B.item;
@@ -771,7 +764,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
             const uint32_t one = pp_elect();
             bool ok = wait(&B.q, 0) && wait(B.kfull + 0, 0);
             if (ok) {
-                pp_fence_after();
+                tc_fence_after();
                 for (int x = 0; x < nx; ++x) {
                     pp_score<HD>(PP_TMEM + x * 128, qb + x * C::OP, kb, false, one);
                     pp_commit(B.s + x, one);
@@ -784,7 +777,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                 for (int x = 0; ok && x < nx; ++x) {
                     ok = wait(B.p + x, j & 1);
                     if (!ok) break;
-                    pp_fence_after();
+                    tc_fence_after();
                     pp_value<HD>(PP_TMEM + 256 + x * HD, PP_TMEM + x * 128, vb + st * C::OP, j > 0, one);
                     if (x == nx - 1) pp_commit(B.vempty + st, one);
                     if (j1 == I.nblk) {
@@ -792,7 +785,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt_kernel(const PpArg
                     } else {
                         if (x == 0) ok = wait(B.kfull + st1, (j1 >> 1) & 1);
                         if (!ok) break;
-                        pp_fence_after();
+                        tc_fence_after();
                         pp_score<HD>(PP_TMEM + x * 128, qb + x * C::OP, kb + st1 * C::OP, false, one);
                         pp_commit(B.s + x, one);
                         if (x == nx - 1) pp_commit(B.kempty + st1, one);
@@ -850,13 +843,13 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
                                         row0, lane);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) pg_arrive(&B.q);
+        if (lane == 0) mbar_arrive(&B.q);
         bool ok = wait(&B.q, 0);
         const float down = xch[256 + r];
         auto gather = [&](int j) {  // o = o * factor + O of block j
             const int buf = j & 1;
             if (!wait(B.o + buf, (j >> 1) & 1)) return false;
-            pp_fence_after();
+            tc_fence_after();
             float d[HO];
 #pragma unroll
             for (int k = 0; k < HO / 32; ++k) pp_ld32(tl + 256 + buf * HD + W * HO + 32 * k, d + 32 * k);
@@ -869,16 +862,16 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
                 o[e] = y.x;
                 o[e + 1] = y.y;
             }
-            pp_fence_before();
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) pg_arrive(B.oempty + buf);
+            if (lane == 0) mbar_arrive(B.oempty + buf);
             return true;
         };
         for (int j = 0; ok && j < I.nblk; ++j) {
             const int buf = j & 1, ph = (j >> 1) & 1;
             ok = wait(B.s + buf, ph);
             if (!ok) break;
-            pp_fence_after();
+            tc_fence_after();
             const uint32_t tS = tl + buf * 128;
             float s[64];
             pp_ld32(tS + 64 * W, s);
@@ -890,12 +883,12 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             const float mine = pp_largest(s) * down;
             // the other half's largest; past this wait both halves of S are in registers, and P may go over them
             xch[buf * 256 + W * 128 + r] = mine;
-            pp_fence_before();
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) pg_arrive(B.x + buf);
+            if (lane == 0) mbar_arrive(B.x + buf);
             ok = wait(B.x + buf, ph);
             if (!ok) break;
-            pp_fence_after();
+            tc_fence_after();
             const float mt = fmaxf(mine, xch[buf * 256 + (W ^ 1) * 128 + r]);
             const float mn = mt > m + PP_SLACK ? mt : m;
             const float corr = mn == m ? 1.f : pg_ex2(m - mn);
@@ -903,9 +896,9 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             m = mn;
             l += pp_probabilities(s, tS + 32 * W, down, m);
             pp_wait_st();
-            pp_fence_before();
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) pg_arrive(B.p + buf);
+            if (lane == 0) mbar_arrive(B.p + buf);
             if (j > 0) {
                 ok = gather(j - 1);
                 if (!ok) break;
@@ -917,7 +910,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             const int buf = I.nblk & 1;
             xch[buf * 256 + W * 128 + r] = l;
             __syncwarp();
-            if (lane == 0) pg_arrive(B.x + buf);
+            if (lane == 0) mbar_arrive(B.x + buf);
             ok = wait(B.x + buf, (I.nblk >> 1) & 1);
         }
         if (ok) {
@@ -950,7 +943,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
             for (int j = 0; ok && j < min(2, I.nblk); ++j) {
                 ok = wait(B.kfull + j, 0);
                 if (!ok) break;
-                pp_fence_after();
+                tc_fence_after();
                 score(j);
             }
             for (int j = 0; ok && j < I.nblk; ++j) {
@@ -959,14 +952,14 @@ __global__ void __launch_bounds__(PP_THREADS, 1) pages_prompt32_kernel(const PpA
                 if (ok && j >= 2) ok = wait(B.oempty + st, ph ^ 1);
                 if (ok) ok = wait(B.p + st, ph);
                 if (!ok) break;
-                pp_fence_after();
+                tc_fence_after();
                 pp_value<HD>(PP_TMEM + 256 + st * HD, PP_TMEM + st * 128, vb + st * C::OP, false, one);
                 pp_commit(B.o + st, one);
                 pp_commit(B.vempty + st, one);
                 if (j + 2 < I.nblk) {
                     ok = wait(B.kfull + st, ph ^ 1);
                     if (!ok) break;
-                    pp_fence_after();
+                    tc_fence_after();
                     score(j + 2);
                 }
             }

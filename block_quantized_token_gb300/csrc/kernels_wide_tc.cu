@@ -35,6 +35,7 @@
 // chunk c ^ n), the 16 lo rows right after the 16 hi rows.  The slice's sum
 // of squares of x per column goes to global memory for the finisher's 1/rms.
 #include "gemv_core.cuh"
+#include "tcgen05.cuh"
 
 namespace er {
 
@@ -76,15 +77,6 @@ __host__ __device__ inline int tw_cta0(int s, int S, int C) { return (int)((long
 // ---------------------------------------------------------------------------
 // tcgen05 wrappers
 // ---------------------------------------------------------------------------
-ER_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-ER_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row atoms of
-// 1024 bytes (stride between atoms 1024), descriptor version 1
-ER_DEV uint64_t tc_desc_sw128(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
 // instruction descriptor, kind::f16: fp16 A and B (both K-major), fp32 D, N = 32, M = 128
 constexpr uint32_t TW_IDESC = (1u << 4) | ((32u >> 3) << 17) | ((128u >> 4) << 24);
 
@@ -112,9 +104,6 @@ ER_DEV void tc_ld32(uint32_t taddr, uint32_t (&v)[32]) {
 // waits for the loads above; the registers pass through so no use moves ahead of it
 ER_DEV void tc_wait_ld(uint32_t (&a)[32], uint32_t (&b)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]), "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15]), "+r"(b[16]), "+r"(b[17]), "+r"(b[18]), "+r"(b[19]), "+r"(b[20]), "+r"(b[21]), "+r"(b[22]), "+r"(b[23]), "+r"(b[24]), "+r"(b[25]), "+r"(b[26]), "+r"(b[27]), "+r"(b[28]), "+r"(b[29]), "+r"(b[30]), "+r"(b[31]) : : "memory");
-}
-ER_DEV void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 ER_DEV unsigned ld_acquire_cta(const unsigned *p) {
     unsigned v;

@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace er {
 
@@ -70,9 +71,6 @@ ER_DEV __half pg_cvt<__half>(float v) { return __float2half_rn(v); }
 template <>
 ER_DEV __nv_bfloat16 pg_cvt<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-ER_DEV void pg_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 // Waits for what a CTA has in flight before it ends.  With a limit of its own: under the one that er_set_wait_limit_ns sets
 // the CTA could end while copies still write its shared memory, by then another's.
 ER_DEV void pg_drain(uint64_t *bar, uint32_t parity) {
