@@ -138,7 +138,7 @@ ER_DEV uint32_t pd_trans(uint32_t x) {
 struct PdArgs {
     PagesView p;
     er_pages_attention_args a;
-    int max_rows;  // sequences with as many query rows a KV head, or more, are another kernel's
+    int max_rows;  // pg_prompt: sequences of another kernel
     float *part;  // [CTAs][2] states of units that several CTAs share
     int *cnt;     // [CTAs] arrivals, zero between launches
     int shortfall;  // tests of the give-up path: arrivals that CTA 0 waits for in vain
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                                  len > pg_max_len(a.table_stride, R);
                 if (bad) {
                     if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
-                } else if ((long long)(q1 - q0) * G >= P.max_rows) {
+                } else if (pg_prompt(q1 - q0, G, P.max_rows)) {
                     ns = 0;
                 } else if (q1 > q0 && len > 0) {
                     ns = (len - 1) / PD_STEP - pd_row0(len, q1 - q0, a.window) / PD_STEP + 1;
@@ -867,14 +867,23 @@ static cudaError_t decode_t(const PdArgs &P, int num_sms, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-// From this many query rows of a KV head on, a sequence goes to the prompt kernel.
+// From this many query rows of a KV head on, several tokens of a sequence go to the prompt kernel.  Its CTA takes as long for 16
+// rows as for 128 and walks all of a sequence's rows by itself; this file's kernel takes rows in eights and spreads them over
+// the SMs.  us, bf16, 32 / 8 heads of 128, 16 / 32 / 64 / 128 / 256 query rows of each of 8 sequences over 4096 rows: here
+// 33 / 49 / 82 / 147 / 277, there 81 / 82 / 82 / 83 / 87; fp32 38 / 61 / 108 / 201 / 381 and 70 / 70 / 71 / 71 / 71; bf16
+// heads of 64: 25 / 35 / 58 / 101 / 187 and 63 / 64 / 64 / 66 / 75.  So 64 is the crossing where prompts fill the SMs.
+// One sequence alone crosses later, near 512 rows (bf16, 4096 rows: 19 / 23 / 26 / 33 / 49, at 512 82, against 79 to 83; fp32 21
+// / 23 / 27 / 38 / 61, at 512 108, against 70): which kernel is the faster there depends on the whole call, which no rule here
+// looks at.  A single token with all heads on one K/V head is 64 rows and always this kernel's: 64 / 1 heads of 128, bf16,
+// 512 / 4096 / 32768 rows, 13 / 15 / 23 us here, 21 / 80 / 555 there.
 constexpr int PD_PROMPT_ROWS = 64;
 
 cudaError_t launch_pages_attention(const PagesView &p, const er_pages_attention_args &a, float *part, int *cnt,
                                    int shortfall, int num_sms, cudaStream_t st) {
-    // The lengths are on the device, so the split is made there, sequence by sequence; here only what the sizes
-    // rule out: no sequence that long, or (at most a token each on average) a decode step, which stays one launch.
-    const bool prompts = (long long)a.n_tokens * (a.n_heads / p.KV) >= PD_PROMPT_ROWS && (a.n_tokens > a.n_seqs || a.n_seqs == 1);
+    // The lengths are on the device, so the split is made there, sequence by sequence.  Here: too few rows for any prompt, or a
+    // step of at most as many tokens as sequences, taken for a decode step, which stays one launch.  (A prompt among that
+    // many idle sequences is worked by the kernel of few rows too: right, but slower the longer it is.)
+    const bool prompts = (long long)a.n_tokens * (a.n_heads / p.KV) >= PD_PROMPT_ROWS && a.n_tokens > a.n_seqs;
     if (prompts)
         if (cudaError_t e = launch_pages_prompt(p, a, PD_PROMPT_ROWS, shortfall, st); e != cudaSuccess) return e;
     for (int b = 0; b < a.n_seqs; b += PD_SEQS) {

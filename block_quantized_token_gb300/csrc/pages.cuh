@@ -104,6 +104,8 @@ constexpr int PG_MAX_LEN = 2147483647 - 1024;
 ER_DEV int pg_max_len(int table_stride, int page_rows) {
     return (int)min((long long)table_stride * page_rows, (long long)PG_MAX_LEN);
 }
+// whether a sequence's new tokens, of G query rows a KV head each, are the prompt kernel's: never a single token
+ER_DEV bool pg_prompt(int tokens, int G, int min_rows) { return tokens > 1 && (long long)tokens * G >= min_rows; }
 // the first row that the token at position p attends (p < 0: none, whatever this says)
 ER_DEV int pg_first(int p, int window) { return window ? max(0, max(p, 0) - (window - 1)) : 0; }
 

@@ -68,6 +68,20 @@ for n, stride in ((1023, 1 << 21), (1, 2**31 - 1024), (1024, 1)):
 er.er_pages_destroy(h)
 """)
 
+def test_a_single_token_is_no_prompt(tmp_path):
+    """A token's 64 query heads on one K/V head are one launch of the kernel that spreads the cached rows over the SMs."""
+    fake_cuda.run(tmp_path, """
+one = er.er_pages_config(1, 10, 32, 1, 64, er.ER_Q4_0)
+h = er.er_pages_create(one, pool_ptr)
+def launches(seqs, tokens):
+    before = word("fake_launches").value
+    er.er_pages_attention(h, 0, er.er_pages_attention_args(seqs, tokens, 64, er.ER_BF16, 10, 0, pool_ptr, pool_ptr, None, 4096,
+                                                           4096, at, at, at, 0.0))
+    return word("fake_launches").value - before
+assert launches(1, 1) == 1 and launches(3, 3) == 1 and launches(1, 2) == 2 and launches(3, 4) == 2
+er.er_pages_destroy(h)
+""")
+
 class Current:
     """Stands for torch.cuda.device: which device a call found current."""
 
