@@ -300,7 +300,7 @@ cudaError_t launch_rope_table(int hd, double base, int n, float *out, cudaStream
 // slots follow one another inside a tile, so that a prompt's tiles leave as whole 16-byte words although a V word
 // mixes four rows; a lone row leaves as bytes.
 // ---------------------------------------------------------------------------
-// append + read of 8192 bf16 tokens, 32 query and 8 K/V heads of 128: 71 us (33.6 for the bytes alone at the copy rate).
+// append + read of 8192 bf16 tokens, 32 query and 8 K/V heads of 128: 72 us (33.6 for the bytes alone at the copy rate).
 // What costs is instructions and latency, so warps count before registers: blocks of 8 warps 2 an SM 139 us, 3 104, 4 97;
 // then with the factors joined, 16-bit values kept as words and the unsure rows done after the others (few spills) 73,
 // and 71 in blocks of 4 warps.
@@ -397,12 +397,14 @@ ER_DEV void st_row(T *row, int c, bool vec, const float (&x)[8]) {
 // s of the lane (HALVES: one in each half of the head, else d[0]).  The lanes of a block are neighbours; whole warps call
 // this.  A quotient comes from the scale's reciprocal where that leaves no doubt about its code, else from the division.
 //
-// CHECK: y is off the exact row by at most AP_ERR times |a| + |b| of its rotated pair (a, b), hence by 2 AP_ERR times
-// the pair's larger value, hence by E = 2 AP_ERR max |m| over the blocks that hold the lane's pairs (that block and,
+// CHECK: y is off the exact row by at most E = 2 AP_ERR max |m| over the blocks that hold the lane's pairs (that block and,
 // for halves, its counterpart in the other half, which the same lanes hold).  Returns whether some code or scale is
 // not certain within E.
-// AP_ERR: the sum of HD squares takes at most 10 float32 steps (half of that in its root), the reciprocal root and its
-// argument 4, gain times cosine 1, the rotation 2, the last product 1: below 14 steps of 2^-24.
+// In steps of u = 2^-24, relative to |a c| + |b s| of a pair (a, b) times its gains: the sum of HD squares takes 8 fused steps
+// and 3 or 4 additions, eps 1 more, together 13, of which the root keeps 6.5; the reciprocal root 4 (2 ulp); gain times
+// cosine 1, the rotation 2, the last product 1: 14.5.  (c, s) turn and scale the pair, so |a c| + |b s| is at most sqrt(2) times
+// the larger of the two results: 20.5.  The exact value's own rounding to float32 and that of |m| +- E below: 22.5.  E counts
+// 2 * 14 = 28.
 constexpr float AP_ERR = 14.f * 5.9604645e-8f;
 // A mean square (and eps) between these is as exact as that counts: no square that matters has underflowed or overflowed.
 constexpr float AP_SMALL = 0x1p-90f, AP_LARGE = 0x1p120f;

@@ -6,7 +6,7 @@
 //
 // What bounds it: the cache's bytes (18 / 32 a value); next, instructions, two a value to turn codes into operands
 // and feed the tensor cores, so a tile's codes are laid out as the operands take them.  Measured, 16 sequences of 8192 rows,
-// 32 / 8 heads of 128: bf16 47.6 us (3.2 TB/s of cache, 0.48 of a copy's rate), fp32 62 us; about a quarter of that is the
+// 32 / 8 heads of 128: bf16 51 us (3.0 TB/s of cache, 0.45 of a copy's rate), fp32 62 us; about a quarter of that is the
 // way to the first tile and the joining of states, the rest the loop at half the SM's issue rate (long chains of
 // dependent products and exponentials in 2 or 3 warps a scheduler).
 //
@@ -44,7 +44,7 @@ constexpr int PD_MAX_WARPS = 12;
 constexpr int PD_STEP = 32;      // rows of a step: two tiles
 constexpr int PD_ROWS = 8;       // query rows of a unit
 constexpr int PD_SEQS = 512;     // sequences of a launch (more: several launches)
-constexpr int PD_MIN_STEPS = 8;  // steps of a CTA at least: one a warp (fewer only add states to join)
+constexpr int PD_MIN_STEPS = 8;  // steps of a CTA at least (fewer only add states to join); of 12 warps 4 have none then
 constexpr float PD_UP = 7.f;     // p = 2^(s - m + PD_UP)
 constexpr float PD_SLACK = 8.f;  // scores may pass m by this much
 constexpr float PD_NONE = -3e38f;  // m before any score
@@ -67,9 +67,9 @@ struct PdType<__nv_bfloat16> {
 struct PdSeq {  // a sequence: its rows of q, its length, its steps (-1: rows with nothing to attend)
     int q0, qn, len, ns;
 };
-// 12 warps hide more latency than 8 where 168 registers a thread hold a warp's state, which they do for HD = 64 and for
-// bf16 queries (ragged 61 x 0..4001, bf16: 45 us against 50; 1 x 2048, 64 dims, fp32: 12.7 against 14.7); fp32 and fp16
-// queries at 128 dims spill then (16 x 8192 fp32: 69 us against 62).
+// 12 warps hide more latency than 8 where 168 registers a thread nearly hold a warp's state, which they do for HD = 64 (fp32
+// spills 8 bytes) and for bf16 queries at 128 dims (32 bytes stored, 44 loaded): ragged 61 x 0..4001, bf16: 45 us against 51;
+// 1 x 2048, 64 dims, fp32: 12.7 against 14.7.  fp32 and fp16 queries at 128 dims spill more (16 x 8192 fp32: 69 us against 62).
 template <class T, int HD>
 struct PdCfg {
     static constexpr int WARPS = HD == 64 || sizeof(T) == 2 && PdType<T>::RAW ? PD_MAX_WARPS : 8;

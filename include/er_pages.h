@@ -155,7 +155,7 @@ ER_API er_status er_pages_read(er_pages *p, int32_t layer, int32_t n, const int3
  * largest).  Results do not depend on timing.
  *   - A q_start_dev that falls or passes n_tokens, a length below 0, past the
  *     table or past 2^31 - 1025, and a table entry outside the pool set flag bit 1 and leave that
- *     sequence's outputs unspecified; nothing outside the pool is read.
+ *     sequence's outputs unspecified (a q_start_dev that falls: all outputs); nothing outside the pool is read.
  *   - A NaN in a cached row makes NaN of at least its 32 dims (of a value) or of
  *     the whole head (of a key) in every token that attends the row, and of
  *     nothing in those that do not.
