@@ -68,7 +68,7 @@ struct PdSeq {  // a sequence: its rows of q, its length, its steps (-1: rows wi
     int q0, qn, len, ns;
 };
 // 12 warps hide more latency than 8 where 168 registers a thread nearly hold a warp's state, which they do for HD = 64 (fp32
-// spills 8 bytes) and for bf16 queries at 128 dims (32 bytes stored, 44 loaded): ragged 61 x 0..4001, bf16: 45 us against 51;
+// stores 12 bytes) and for bf16 queries at 128 dims (32 bytes stored, 44 loaded): ragged 61 x 0..4001, bf16: 45 us against 51;
 // 1 x 2048, 64 dims, fp32: 12.7 against 14.7.  fp32 and fp16 queries at 128 dims spill more (16 x 8192 fp32: 69 us against 62).
 template <class T, int HD>
 struct PdCfg {
@@ -138,7 +138,7 @@ ER_DEV uint32_t pd_trans(uint32_t x) {
 struct PdArgs {
     PagesView p;
     er_pages_attention_args a;
-    int max_rows;  // pg_prompt: sequences of another kernel
+    int max_rows;  // sequences with as many query rows a KV head, or more, are another kernel's
     float *part;  // [CTAs][2] states of units that several CTAs share
     int *cnt;     // [CTAs] arrivals, zero between launches
     int shortfall;  // tests of the give-up path: arrivals that CTA 0 waits for in vain
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__((PdCfg<T, HD>::THREADS), 1) pages_decode_kerne
                                  len > pg_max_len(a.table_stride, R);
                 if (bad) {
                     if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
-                } else if (pg_prompt(q1 - q0, G, P.max_rows)) {
+                } else if ((long long)(q1 - q0) * G >= P.max_rows) {
                     ns = 0;
                 } else if (q1 > q0 && len > 0) {
                     ns = (len - 1) / PD_STEP - pd_row0(len, q1 - q0, a.window) / PD_STEP + 1;
@@ -883,11 +883,12 @@ cudaError_t launch_pages_attention(const PagesView &p, const er_pages_attention_
     // The lengths are on the device, so the split is made there, sequence by sequence.  Here: too few rows for any prompt, or a
     // step of at most as many tokens as sequences, taken for a decode step, which stays one launch.  (A prompt among that
     // many idle sequences is worked by the kernel of few rows too: right, but slower the longer it is.)
-    const bool prompts = (long long)a.n_tokens * (a.n_heads / p.KV) >= PD_PROMPT_ROWS && a.n_tokens > a.n_seqs;
+    const int G = a.n_heads / p.KV, from = PD_PROMPT_ROWS > G ? PD_PROMPT_ROWS : G + 1;  // (G rows are a single token)
+    const bool prompts = (long long)a.n_tokens * G >= from && a.n_tokens > a.n_seqs;
     if (prompts)
-        if (cudaError_t e = launch_pages_prompt(p, a, PD_PROMPT_ROWS, shortfall, st); e != cudaSuccess) return e;
+        if (cudaError_t e = launch_pages_prompt(p, a, from, shortfall, st); e != cudaSuccess) return e;
     for (int b = 0; b < a.n_seqs; b += PD_SEQS) {
-        PdArgs P = {p, a, prompts ? PD_PROMPT_ROWS : 2147483647, part, cnt, shortfall};
+        PdArgs P = {p, a, prompts ? from : 2147483647, part, cnt, shortfall};
         P.a.n_seqs = a.n_seqs - b < PD_SEQS ? a.n_seqs - b : PD_SEQS;
         P.a.q_start_dev += b;
         P.a.lens_dev += b;

@@ -74,7 +74,7 @@ struct PpCfg {
 struct PpArgs {
     PagesView p;
     er_pages_attention_args a;
-    int min_rows;  // pg_prompt: the others are another kernel's
+    int min_rows;  // sequences with fewer query rows a KV head are another kernel's
     int shortfall;  // tests of the give-up path: arrivals that CTA 0 waits for in vain
 };
 
@@ -209,7 +209,7 @@ ER_DEV bool pp_find(const PpArgs &P, PpBars &B, int warp, int lane, PpItem &I) {
                 len = a.lens_dev[b];
                 if (q0 < 0 || q1 < q0 || q1 > a.n_tokens || len < 0 || len > pg_max_len(a.table_stride, R)) {
                     if (blockIdx.x == 0) atomicOr(P.p.flags, ER_PAGES_FLAG_RANGE);
-                } else if (pg_prompt(q1 - q0, G, P.min_rows)) {
+                } else if ((long long)(q1 - q0) * G >= P.min_rows) {
                     n = (int)(((long long)(q1 - q0) * G + ROWS - 1) / ROWS);
                 }
             }
