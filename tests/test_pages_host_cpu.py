@@ -2,6 +2,8 @@
 
 from __future__ import annotations
 
+import functools
+
 import pytest
 
 import fake_cuda
@@ -103,14 +105,22 @@ class _Held:
         self.current.now = self.before
 
 
-def _runtime(monkeypatch, current):
+def _runtime(monkeypatch, current, home=None):
     from block_quantized_token_gb300 import build
     build.build()
     from block_quantized_token_gb300 import er, runtime
     seen = []
+
+    def call(name, *a):
+        if name != "er_rope_table" and current.now != home:  # as the library refuses it
+            raise er.ErError(name, er.ER_EINVAL)
+        if a[0] is None:
+            raise er.ErError(name, er.ER_EUNSUPPORTED)
+        seen.append((name, current.now))
+
     for name in ("er_rope_table", "er_pages_plan", "er_pages_release", "er_pages_append", "er_pages_read", "er_pages_attention",
                  "er_pages_error"):
-        monkeypatch.setattr(er, name, lambda *a, name=name: seen.append((name, current.now)))
+        monkeypatch.setattr(er, name, functools.partial(call, name))
     monkeypatch.setattr(torch.cuda, "device", current)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current.now, raising=False)
     return runtime, seen
@@ -126,7 +136,7 @@ def test_rope_table_runs_on_the_device_of_its_memory(monkeypatch):
 
 def test_paged_calls_run_on_the_cache_s_device(monkeypatch):
     current = Current(3)
-    runtime, seen = _runtime(monkeypatch, current)
+    runtime, seen = _runtime(monkeypatch, current, home=-1)
     from block_quantized_token_gb300 import er
     c = object.__new__(runtime.PagedCache)
     c.n_kv_heads, c.head_dim, c.cfg, c.handle = 2, 64, er.er_pages_config(1, 4, 16, 2, 64, er.ER_Q4_0), 1
@@ -141,5 +151,13 @@ def test_paged_calls_run_on_the_cache_s_device(monkeypatch):
         c.attention(0, x, x, i, one, t, stream=0)
         c.error()
         assert [d for _, d in seen] == [-1] * 6 and current.now == 3
+        # any other refusal stays one, wherever it happens
+        c.handle = None
+        for now in (3, -1):
+            current.now = now
+            for f in (c.error, lambda: c.read(0, i[:4], x, x, stream=0)):
+                with pytest.raises(er.ErError) as e:
+                    f()
+                assert e.value.status == er.ER_EUNSUPPORTED and current.now == now
     finally:
         c.handle = None
