@@ -46,6 +46,7 @@
 
 #include "pages.cuh"
 #include "pages.h"
+#include "ring.h"
 
 namespace er {
 
@@ -450,12 +451,13 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
         }
     };
     bool ok = true;
-    int slot = half, par = 0;  // of half block 2 j + half
-    for (int j = 0; j < nblk; ++j) {
+    RingWalk<PP_RAW> at(half);  // of half block 2 j + half
+    for (int j = 0; j < nblk; ++j, at.step()) {
         const int st = j & 1, ph = (j >> 1) & 1;
-        ok = wait(B.raw + slot, par);
+        ok = at.ready([&](int slot, int par) { return wait(B.rawfree + slot, par); },
+                      [&](int slot, int par) { return wait(B.raw + slot, par); });
         if (!ok) break;
-        const uint8_t *raw = ring + slot * (4 * C::TILE);
+        const uint8_t *raw = ring + at.slot * (4 * C::TILE);
         const int r0 = base + PP_BLOCK * j;
         const bool edge = r0 < all_lo || r0 + PP_BLOCK - 1 > all_hi;
         if (j >= 2) ok = wait(B.kempty + st, ph ^ 1);
@@ -472,13 +474,9 @@ ER_DEV void pp_operands(const PpArgs &P, PpBars &B, uint8_t *smem, const PpItem 
         else vals(std::false_type{}, raw, vd, r0);
         fence_proxy_async_smem();
         __syncwarp();
+        // in this order: no warp gets three blocks ahead of one that has not given its slot back (RingWalk)
+        if (lane == 0) mbar_arrive(B.rawfree + at.slot);
         if (lane == 0) mbar_arrive(B.vfull + st);
-        if (lane == 0) mbar_arrive(B.rawfree + slot);
-        slot += 2;
-        if (slot >= PP_RAW) {
-            slot -= PP_RAW;
-            par ^= 1;
-        }
     }
 }
 

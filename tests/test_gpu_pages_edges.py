@@ -138,3 +138,36 @@ def test_shortfall_refusals():
         with pytest.raises(er.ErError) as e:
             er.er_pages_inject_wait_shortfall(handle, extra)
         assert e.value.status == er.ER_EINVAL
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("window", [0, 161])
+def test_prompt_whose_first_rows_come_late(dtype, window):
+    """Copies of cached rows land in any order: every prompt's first 64 rows lie in a page far from the others, out of L2 and
+    of the address cache, the rows after them close together.  Every run is the first one's."""
+    n, kv, hd, page = 12, 8, 128, 64
+    lens, new = [400 + 37 * i for i in range(n)], [300 + 11 * i for i in range(n)]
+    b = Batch(lens, new, kv, kv, hd, page, dtype, seed=91, window=window)
+    want, wz = b.run()
+    b.check(want, wz, seqs=[0, n - 1])
+    page_bytes = b.cache.pool.numel() // b.pages
+    far = (1 << 31) // page_bytes  # 2 GiB on
+    big = paged(far + n * 4099, page, kv, hd)
+    pages, small = big.pool.view(-1, page_bytes), b.cache.pool.view(-1, page_bytes)
+    pages[:b.pages].copy_(small)
+    tables = b.tables.copy()
+    for i in range(n):
+        at = far + i * 4099
+        pages[at].copy_(small[tables[i, 0]])
+        tables[i, 0] = at
+    args = ints(b.start), ints(b.lens), ints(tables)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(want), torch.empty_like(wz)
+    bad = torch.zeros((), device="cuda")
+    for i in range(200):
+        flush.fill_(i)
+        small_rows = pages[:b.pages].sum()  # the close pages are in L2
+        big.attention(0, b.q, out, *args, window=window, lse=lse)
+        bad += (out != want).any() | (lse != wz).any()
+    assert bad.item() == 0 and small_rows.item() >= 0
+    fine(big)
