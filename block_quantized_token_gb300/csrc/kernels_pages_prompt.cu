@@ -10,7 +10,7 @@
 //     warp 12         one thread issues the products: S = Q K^T (M = 128, N = 128), O += P V (N = HD, hi and lo of P), the
 //                     two tiles in turn, so the tensor cores work on one tile while the other's softmax runs.
 //     TMEM: S/P of both tiles (2 x 128 columns), O of both (2 x HD).
-//   P as one half (2^-11) would be 434 us for 8192 bf16 tokens against 552, but then a bf16 output in twenty differs by its
+//   P as one half (2^-11) would be 434 us for 8192 bf16 tokens against 557, but then a bf16 output in twenty differs by its
 //   last bit from what exact probabilities give, and an fp16 output is off by as much again as its own rounding.
 //   fp32 rows (pages_prompt32_kernel): one tile; queries enter as hi + lo halves too, two products each.  The tensor cores'
 //   sums truncate (over thousands of rows 2^-18 of the output and growing), so a block's O starts from 0 and is added to
@@ -23,11 +23,11 @@
 //     warp 12         S of the block after next goes to the buffer whose P is used up, so the softmax never waits for it
 //     TMEM: two buffers of S/P, two of a block's O.
 //   Both: warps 8-11 turn codes into fp16 operands in shared memory, exactly (pages.cuh), K and V K-major with the
-//   128-byte swizzle, two stages each; warp 13 requests the cached tiles: bulk copies into a ring of half blocks, each
-//   used by two operand warps.
+//   128-byte swizzle, two stages each; warp 13 requests the cached tiles: bulk copies into a ring of three half blocks, each
+//   used by two operand warps (ring.h).
 //
 // Registers (the launch's 128 a thread, shared out anew: 2 softmax + operands + rest = 512).  A spill in any role delays the
-// others.  16 bits: 208, 48, 48 (8 bytes spilled at HD = 128; 8192 bf16 tokens: 552 us; 200, 56, 56: 585; 200, 64, 48: 588).
+// others.  16 bits: 208, 48, 48 (8 bytes spilled at HD = 128; 8192 bf16 tokens: 552 us in the build that had these figures; 200, 56, 56: 585; 200, 64, 48: 588).
 // fp32: 200, 64, 48 (8 bytes; 4 x 500 tokens: 135 us; 200, 80, 32: 138).
 //
 // The block's rows are put in the order k' = 32 a + 8 t + 4 b + 2 i + e for row 32 a + 16 b + 8 i + 2 t + e, in K's rows,
@@ -37,8 +37,8 @@
 // What bounds it: at HD = 128 a block and two tiles take the tensor cores 3072 cycles (six products of 512; one tile of
 // fp32 2048), shared memory 2560 (the products' reads, the operands' writes), and about 4000 in all with the softmax and
 // its hand-overs (4770 of the whole launch's, the ways in and out and the last, uneven CTAs among them).
-// Measured: 8192 bf16 tokens, 32 / 8 heads of 128: 552 us = 1.0 PFLOP/s, 0.52 of the library's matrix product (with the lo
-// halves' product counted 0.78); 4 x 300..500 fp32 tokens over 900..4100 rows: 135 us.
+// Measured: 8192 bf16 tokens, 32 / 8 heads of 128: 557 us = 0.99 PFLOP/s, 0.52 of the library's matrix product (with the lo
+// halves' product counted 0.77); 4 x 300..500 fp32 tokens over 900..4100 rows: 135 us.
 //
 // Masks.  Blocks that some row attends only in part mask S; there, rows of V that no row of the CTA attends are
 // zeroed (they may hold anything), and a NaN value of V is carried by K instead, so only rows that attend it see it.
