@@ -34,8 +34,8 @@
 // hence S's and P's columns, and in V's K dimension: so a thread that holds a code word of V of two 16-row tiles
 // holds 16 bytes of the operand.
 //
-// What bounds it: at HD = 128 a block and two tiles take the tensor cores 3072 cycles (six products of 512; one tile of
-// fp32 2048), shared memory 2560 (the products' reads, the operands' writes), and about 4000 in all with the softmax and
+// What bounds it: at HD = 128 a block and two tiles take the tensor cores six products of 512 cycles (one tile of fp32
+// four), shared memory 2560 (the products' reads, the operands' writes), and about 4000 in all with the softmax and
 // its hand-overs (4770 of the whole launch's, the ways in and out and the last, uneven CTAs among them).
 // Measured: 8192 bf16 tokens, 32 / 8 heads of 128: 557 us = 0.99 PFLOP/s, 0.52 of the library's matrix product (with the lo
 // halves' product counted 0.77); 4 x 300..500 fp32 tokens over 900..4100 rows: 135 us.
