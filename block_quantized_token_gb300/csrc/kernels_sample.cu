@@ -48,6 +48,7 @@ struct SampleArgs {
     long long stride;
     const float *temperature, *top_p, *min_p, *uniform;
     const int32_t *top_k;
+    const int64_t *top_k64;  // (in its place)
     int32_t *tokens;
     float *logprobs;
 };
@@ -294,7 +295,8 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleArgs 
 
     float temp = a.temperature ? a.temperature[row] : 1.f;
     if (temp > 0.f) temp = fmaxf(temp, 0x1p-120f);  // (1 / (T ln 2) stays a number)
-    const int k = a.top_k ? a.top_k[row] : 0, kk = k <= 0 || k >= a.V ? a.V : k;
+    const long long k = a.top_k ? a.top_k[row] : a.top_k64 ? a.top_k64[row] : 0;
+    const int kk = k <= 0 || k >= a.V ? a.V : (int)k;
     const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f;
     float u = a.uniform[row];
     u = u > 0.f ? fminf(u, 1.f) : 0.f;
@@ -910,6 +912,7 @@ cudaError_t launch_sample(const er_sample_args &s, cudaStream_t st) {
     a.min_p = s.min_p_dev;
     a.uniform = s.uniform_dev;
     a.top_k = s.top_k_dev;
+    a.top_k64 = s.top_k64_dev;
     a.tokens = s.tokens_dev;
     a.logprobs = s.logprobs_dev;
     return s.type == ER_F32 ? sm_launch<float>(a, st) : s.type == ER_F16 ? sm_launch<__half>(a, st) : sm_launch<__nv_bfloat16>(a, st);

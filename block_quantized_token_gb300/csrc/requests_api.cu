@@ -167,6 +167,8 @@ er_status er_sample(const er_sample_args *a, void *stream) {
                             (uintptr_t)a->min_p_dev | (uintptr_t)a->uniform_dev | (uintptr_t)a->tokens_dev |
                             (uintptr_t)a->logprobs_dev;
     if (words & 3) return er_fail_status(ER_EINVAL, "int and float arrays must be 4-byte aligned");
+    if (!aligned(a->top_k64_dev, 8)) return er_fail_status(ER_EINVAL, "top_k64 must be 8-byte aligned");
+    if (a->top_k_dev && a->top_k64_dev) return er_fail_status(ER_EINVAL, "top_k and top_k64 must not be given together");
     return done(launch_sample(*a, (cudaStream_t)stream), "er_sample");
 }
 

@@ -84,7 +84,7 @@ class er_matrix_mul_args(ctypes.Structure):
 
 class er_sample_args(ctypes.Structure):
     _fields_ = _struct(c_int32="n_rows vocab type", c_void_p="logits", c_int64="stride",
-                       c_void_p_="temperature top_k top_p min_p uniform tokens logprobs")
+                       c_void_p_="temperature top_k top_p min_p uniform tokens logprobs top_k64")
 
 
 def _load() -> ctypes.CDLL:

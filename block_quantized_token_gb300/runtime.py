@@ -506,13 +506,18 @@ class Matrix:
 def sample(logits: torch.Tensor, uniform: torch.Tensor, tokens: torch.Tensor, temperature: torch.Tensor | None = None,
            top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
            logprobs: torch.Tensor | None = None, stream: int | None = None) -> None:
-    """tokens[i]: a token of row i of logits [rows, vocab] by its own parameters and uniform[i] in [0, 1) (er_sample)."""
+    """tokens[i]: a token of row i of logits [rows, vocab] by its own parameters and uniform[i] in [0, 1) (er_sample).
+
+    top_k is int32 or int64, the other parameters float32, tokens int32.
+    """
     index = logits.get_device()
     if logits.dim() != 2 or logits.dtype not in _ROW_TYPES or not logits.is_cuda or \
             logits.stride(1) != 1 and logits.shape[1] > 1:
         raise ValueError("logits must be dense rows [rows, vocab] of float32, float16 or bfloat16")
     n, vocab = logits.shape
-    for t, dtype in ((uniform, torch.float32), (tokens, torch.int32), (temperature, torch.float32), (top_k, torch.int32),
+    k64 = top_k is not None and top_k.dtype is torch.int64
+    for t, dtype in ((uniform, torch.float32), (tokens, torch.int32), (temperature, torch.float32),
+                     (top_k, torch.int64 if k64 else torch.int32),
                      (top_p, torch.float32), (min_p, torch.float32), (logprobs, torch.float32)):
         if t is not None and (t.dtype is not dtype or t.get_device() != index or t.numel() < n or not t.is_contiguous()):
             raise ValueError(f"{n} dense {dtype} values on device {index} are needed")
@@ -520,6 +525,6 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, tokens: torch.Tensor, te
         with torch.cuda.device(index):
             return sample(logits, uniform, tokens, temperature, top_k, top_p, min_p, logprobs, stream)
     a = er.er_sample_args(n, vocab, _ROW_TYPES[logits.dtype], logits.data_ptr(), logits.stride(0) if n > 1 else vocab,
-                          _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), uniform.data_ptr(), tokens.data_ptr(),
-                          _ptr(logprobs))
+                          _ptr(temperature), None if k64 else _ptr(top_k), _ptr(top_p), _ptr(min_p), uniform.data_ptr(),
+                          tokens.data_ptr(), _ptr(logprobs), _ptr(top_k) if k64 else None)
     er.er_sample(a, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream)

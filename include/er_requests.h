@@ -81,7 +81,8 @@ ER_API er_status er_matrix_mul_inject_wait_shortfall(er_matrix *mat, int32_t ext
  * times their sum; uniform in [0, 1) (below or NaN: 0; 1 and above: the last kept with a mass).
  * logprobs_dev[i] (may be NULL): log of the token's share of the kept sum.
  * T <= 0 or NaN, top_k 1, top_p <= 0: the largest logit, lowest index on ties, and 0; T in (0, 2^-120) counts as 2^-120.  A row without any mass (all NaN or
- * -infinity): token -1 and -infinity.  Arrays of parameters are [n_rows] or NULL (temperature 1, nothing left out).
+ * -infinity): token -1 and -infinity.  Arrays of parameters are [n_rows] or NULL (temperature 1, nothing left out); top_k64_dev is
+ * top_k in 64 bits, for callers who have it so: with both ER_EINVAL.
  * The choice is that of the definition in 64 bits, but where a border lies within some 2^-40 of the sum; masses below 2^-45 of
  * the largest count as none, and differences of finite logits past float32's largest number as that.  vocab: at most
  * ER_SAMPLE_MAX_VOCAB (else ER_EUNSUPPORTED).  One launch, no scratch. */
@@ -95,6 +96,7 @@ typedef struct {
     const float *top_p_dev, *min_p_dev, *uniform_dev;
     int32_t *tokens_dev;
     float *logprobs_dev;
+    const int64_t *top_k64_dev;
 } er_sample_args;
 ER_API er_status er_sample(const er_sample_args *a, void *stream);
 

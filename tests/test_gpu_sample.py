@@ -293,3 +293,30 @@ def test_greedy_is_the_decode_step_s_argmax():
     check(logits, [0.7], temperature=[0.8], top_k=[40], top_p=[0.95])
     state.close()
     model.close()
+
+
+def test_top_k_of_either_integer_type():
+    """int64 is what torch makes of Python's numbers: taken as it is, numbers past 31 bits among them."""
+    from block_quantized_token_gb300 import runtime
+    rng = np.random.default_rng(15)
+    ks = [50, 0, -3, 2 ** 40, -2 ** 40, 7, 2500, 2 ** 32 + 5, -2 ** 63, 2 ** 63 - 1, 1, 2 ** 31, 2 ** 32]
+    n = len(ks)
+    x, u = torch.tensor(bulk(rng, n, 9000)).float().cuda(), rng.random(n, np.float32) * 0.98 + 0.01
+    want = check(x, u, top_k=[min(max(k, -1), 2 ** 31 - 1) for k in ks])
+    tokens, lp = torch.full((n + 2,), -7, dtype=torch.int32, device="cuda"), torch.empty(n, device="cuda")
+    k = torch.tensor(ks + [3], device="cuda")
+    assert k.dtype is torch.int64
+    runtime.sample(x, dev(u), tokens, top_k=k, logprobs=lp)
+    assert (tokens[:n].cpu().numpy() == want).all() and (tokens[n:] == -7).all()
+    for bad in (lambda: runtime.sample(x, dev(u), tokens, top_k=k.short()), lambda: runtime.sample(x, dev(u), tokens, top_k=k[: n - 1]),
+                lambda: runtime.sample(x, dev(u), tokens, top_k=k.cpu())):
+        with pytest.raises(ValueError):
+            bad()
+    # captured, with numbers that change
+    g, du = torch.cuda.CUDAGraph(), dev(u)
+    with torch.cuda.graph(g):
+        runtime.sample(x, du, tokens, top_k=k)
+    for number in (1, 2 ** 33, 2100):
+        k.fill_(number)
+        g.replay()
+        assert torch.equal(tokens[:n], run(x, u, top_k=[min(number, 2 ** 31 - 1)] * n)[0])
