@@ -188,7 +188,7 @@ def _logits(g, c):
     row = torch.arange(n, device="cuda")
 
     def pick(values, step, on):
-        t = torch.tensor(values, dtype=torch.float32 if isinstance(values[0], float) else torch.int32, device="cuda")
+        t = torch.tensor(values, device="cuda")
         return t[(row * step + int(torch.randint(0, len(values), (1,), generator=g, device="cuda"))) % len(values)].contiguous() if on else None
 
     m = c["mode"]
