@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(256) mul_prep_kernel(const T *x, long long str
     pdl_launch_dependents();
     pdl_wait();
     mu_prep_row(x + (size_t)t * stride, t, K, UPR, out, plane, natoms, tok_up, tok_down, tops);
-    for (int i = t * 256 + threadIdx.x; i < ncnt; i += gridDim.x * 256) cnt[i] = 0;
+    for (long long i = t * 256ll + threadIdx.x; i < ncnt; i += gridDim.x * 256ll) cnt[i] = 0;  // (256 times 2^23 tokens pass 31 bits)
 }
 
 // Adapters as steps of the product: for every kind of adapter among a tile's tokens, every 16 of its rank and every pair of

@@ -297,6 +297,29 @@ def test_outputs_past_2_31_elements():
     c.fine()
 
 
+def test_tokens_past_2_23():
+    """256 threads a token: their numbers pass 31 bits.  Every row against fp32 sums (32 terms and 4 of an adapter: 36 2^-24 of the
+    terms' size on both sides, 2^-16 of the adapter's, half a step of bf16)."""
+    c = Case("q8_0", 17, 32, ranks=[4])
+    n = 2 ** 23 + 300
+    x = torch.randn((n, 32), device="cuda").bfloat16()
+    w, f = torch.tensor(c.w, device="cuda").float(), x.float()
+    out = torch.full((n, 17), float("nan"), dtype=torch.bfloat16, device="cuda")
+    c.m.mul(x, out)
+    y, s = f @ w.T, f.abs() @ w.abs().T
+    assert bool(((out.float() - y).abs() <= 1e-5 * s + 2.0 ** -8 * y.abs()).all())
+    c.check(x[-300:], out[-300:], "bf16")
+    scale, a, b = c.known[0]
+    a, b = torch.tensor(a, device="cuda").float() * scale, torch.tensor(b, device="cuda").float()
+    ids = torch.arange(n, dtype=torch.int32, device="cuda") % 2 - 1
+    c.m.mul(x, out, adapters=c.ad, ids=ids)
+    mine = (ids == 0)[:, None]
+    y += (f @ a.T) @ b.T * mine
+    s += (f.abs() @ a.abs().T) @ b.abs().T * mine
+    assert bool(((out.float() - y).abs() <= 3e-5 * s + 2.0 ** -8 * y.abs()).all())
+    c.fine()
+
+
 def test_no_rows_and_longer_buffers():
     c = Case("q8_0", 40, 64, ranks=[4])
     out = torch.full((8, 40), 7.0, device="cuda")
