@@ -158,16 +158,26 @@ __global__ void adapters_a_kernel(AdaptersView v, int slot, int rank, int cols, 
         out[k] = __float2half_rn(j < rank && k < cols ? pg_ld<T>(a + (size_t)j * cols + k) * up : 0.f);
     if (tid == 0) {
         const_cast<float *>(v.down)[(size_t)slot * v.r16 + j] = mu_pow2(-e) * scale;
-        if (j == 0) const_cast<int *>(v.rank)[slot] = (rank + 15) & ~15;
+        if (j == 0) {
+            const_cast<int *>(v.rank)[slot] = (rank + 15) & ~15;
+            const_cast<int *>(v.wild)[slot] = 0;
+        }
     }
 }
 
+// Behind adapters_a_kernel, which empties the slot's `wild`.  B's rows are operands that all tokens of a tile meet (with zeros where
+// a token has another adapter): a value that is infinite or NaN there, as it is or times the factor of W's row (2^35 at most), would be
+// NaN for all of them.  Tiles with such an adapter add it by mu_adapters.
+constexpr float MU_WILD = 0x1p92f;
 __global__ void adapters_b_kernel(AdaptersView v, int slot, int rank, const uint16_t *b) {
     uint16_t *out = reinterpret_cast<uint16_t *>(const_cast<uint8_t *>(v.b)) + (size_t)slot * v.rows * v.r16;
     const size_t n = (size_t)v.rows * v.r16;
     for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
         const int row = (int)(i / v.r16), j = (int)(i - (size_t)row * v.r16);
-        out[i] = j < rank ? b[(size_t)row * rank + j] : (uint16_t)0;
+        const uint16_t w = j < rank ? b[(size_t)row * rank + j] : (uint16_t)0;
+        const float f = v.bf16 ? __uint_as_float((uint32_t)w << 16) : __half2float(__ushort_as_half(w));
+        if (!(fabsf(f) < MU_WILD)) atomicOr(const_cast<int *>(v.wild) + slot, 1);
+        out[i] = w;
     }
 }
 
@@ -175,12 +185,12 @@ __global__ void adapters_clear_kernel(AdaptersView v, int slot) { const_cast<int
 
 cudaError_t launch_adapters_set(const AdaptersView &v, int slot, int rank, int cols, float scale, const void *a, const void *b,
                                 cudaStream_t st) {
-    adapters_b_kernel<<<(unsigned)min((size_t)1024, ((size_t)v.rows * v.r16 + 255) / 256), 256, 0, st>>>(
-        v, slot, rank, reinterpret_cast<const uint16_t *>(b));
     if (v.bf16)
         adapters_a_kernel<<<v.r16, 256, 0, st>>>(v, slot, rank, cols, scale, reinterpret_cast<const __nv_bfloat16 *>(a));
     else
         adapters_a_kernel<<<v.r16, 256, 0, st>>>(v, slot, rank, cols, scale, reinterpret_cast<const __half *>(a));
+    adapters_b_kernel<<<(unsigned)min((size_t)1024, ((size_t)v.rows * v.r16 + 255) / 256), 256, 0, st>>>(
+        v, slot, rank, reinterpret_cast<const uint16_t *>(b));
     return cudaGetLastError();
 }
 
@@ -314,7 +324,8 @@ __global__ void __launch_bounds__(256) mul_prep_kernel(const T *x, long long str
 // Adapters as steps of the product: for every kind of adapter among a tile's tokens, every 16 of its rank and every pair of
 // pieces, 16 columns in A (rows of B_a, bf16) and in the operand (v of the tokens that have it, else 0).  v enters as bf16 pieces,
 // two (2^-17 of the adapter's share of a 16-bit result) or for fp32 three; B_a in fp16 as two pieces, exactly.  The last pieces
-// do not meet.  Four such entries are a step of 64 columns.  A tile with more kinds than MU_EXTRA steps hold has none (nksteps -1).
+// do not meet.  Four such entries are a step of 64 columns.  A tile with more kinds than MU_EXTRA steps hold, or with one whose B holds
+// what is no number (AdaptersView::wild), has none (nksteps -1).
 struct MuKinds {
     int kind[256], start[256], total;  // of a tile's tokens: adapter, the first entry of the kind where this token is its first
     int entry_kind[4 * MU_EXTRA], entry_pair[4 * MU_EXTRA], entry_col[4 * MU_EXTRA];
@@ -335,7 +346,7 @@ ER_DEV void mu_kinds(MuKinds &K, const int32_t *ids, const AdaptersView &ad, int
     if (!r) id = -1;
     K.kind[t] = id;
     for (int i = t; i < 4 * MU_EXTRA; i += 256) K.entry_kind[i] = -1, K.entry_pair[i] = K.entry_col[i] = 0;
-    __syncthreads();
+    const int wild = __syncthreads_or(id >= 0 && ad.wild[id]);
     bool first = id >= 0;
     for (int i = 0; i < t && first; ++i) first = K.kind[i] != id;
     const int mine = first ? r / 16 * per : 0;
@@ -353,7 +364,7 @@ ER_DEV void mu_kinds(MuKinds &K, const int32_t *ids, const AdaptersView &ad, int
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) K.start[8 * t + i] = v[i] + incl - s;
-        if (t == 31) K.total = incl > 4 * MU_EXTRA ? -1 : incl;
+        if (t == 31) K.total = wild || incl > 4 * MU_EXTRA ? -1 : incl;
     }
     __syncthreads();
     if (first && K.total >= 0)
@@ -1084,7 +1095,7 @@ __global__ void __launch_bounds__(mu_threads<TOK>(), 1) mul_main_kernel(const __
             const int ci = sh.n > 1 ? (int)blockIdx.x - sh.first : 0, lo = tok0 + ci * ntok / sh.n, hi = tok0 + (ci + 1) * ntok / sh.n;
             float4 *mine = reinterpret_cast<float4 *>(a.part) + (sh.n > 1 ? sh.slot(a, blockIdx.x) * a.NT * 32 : 0) + thr;
             if constexpr (REG) {
-                const bool many = a.nksteps && __ldcg(a.nksteps + it.tile / a.MT) < 0;  // (too many kinds for steps of their own)
+                const bool many = a.nksteps && __ldcg(a.nksteps + it.tile / a.MT) < 0;  // (no steps of their own)
                 float acc[TOK], td[TOK / 32];
 #pragma unroll
                 for (int h = 0; h < TOK / 32; ++h) td[h] = factor(tok0 + 32 * h, ntok - 32 * h);
@@ -1150,7 +1161,7 @@ __global__ void __launch_bounds__(mu_threads<TOK>(), 1) mul_main_kernel(const __
             } else {
                 if (!(ok = wait(B.dfull + sums.slot, sums.par))) break;
                 tc_fence_after();
-                const bool many = a.nksteps && __ldcg(a.nksteps + it.tile / a.MT) < 0;  // (too many kinds for steps of their own)
+                const bool many = a.nksteps && __ldcg(a.nksteps + it.tile / a.MT) < 0;  // (no steps of their own)
                 for (int h = 0; ok && 32 * h < a.NT; ++h) {
                     const int left = ntok - 32 * h;
                     const bool with = left > 0 && many && adapters(tok0 + 32 * h, left, row, up, lo, hi);

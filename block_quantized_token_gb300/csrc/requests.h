@@ -17,6 +17,7 @@ struct AdaptersView {
     const float *down;  // [slots][r16]: what takes a row's product back, the adapter's scale in it
     const uint8_t *b;   // 16 bits [slots][rows][r16]
     const int *rank;    // [slots], multiples of 16, 0: empty
+    const int *wild;    // [slots], 1: B holds what is no number, or none once a row of W brings it up (MU_WILD)
     int slots, r16, Kp, rows, bf16;
 };
 cudaError_t launch_adapters_set(const AdaptersView &v, int slot, int rank, int cols, float scale, const void *a, const void *b,

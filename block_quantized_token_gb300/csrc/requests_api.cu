@@ -62,7 +62,7 @@ er_status er_adapters_create(const er_adapters_config *c, er_adapters **out) {
     v.rows = c->rows;
     v.bf16 = c->type == ER_BF16;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
-    const size_t nr = up((size_t)v.slots * sizeof(int)), nd = up((size_t)v.slots * v.r16 * sizeof(float));
+    const size_t nr = up((size_t)v.slots * 2 * sizeof(int)), nd = up((size_t)v.slots * v.r16 * sizeof(float));
     const size_t na = (size_t)v.slots * v.r16 * v.Kp * 2, nb = (size_t)v.slots * v.rows * v.r16 * 2;
     ad->bytes = nr + nd + up(na) + up(nb);
     ad->mem = nullptr;
@@ -76,6 +76,7 @@ er_status er_adapters_create(const er_adapters_config *c, er_adapters **out) {
     }
     uint8_t *m = (uint8_t *)ad->mem;
     v.rank = (const int *)m;
+    v.wild = v.rank + v.slots;
     v.down = (const float *)(m + nr);
     v.a = m + nr + nd;
     v.b = m + nr + nd + up(na);

@@ -564,3 +564,59 @@ def test_handles_free_what_they_allocate():
     c.ad.close()
     c.m.close()
     assert er.er_debug_live_allocations() == live
+
+
+# ------------------------------------------------------------------------------------------------------------------
+# adapters that hold infinities and NaN
+# ------------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan, 3e30])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [5, 17, 50, 120, 300])
+def test_an_adapter_s_infinities_stay_with_its_tokens(n, dtype, value):
+    """B of one slot holds a value that is no number (or one so large that it is none once W's row brings it up): tokens of other
+    slots and of none do not see it, those of the slot get what the formula says.  A slot that is filled again is like any other."""
+    rng = np.random.default_rng([n, 3])
+    w = (rng.standard_normal((150, 256)) * 0.05).astype(np.float32)
+    w[40:60] *= 2.0 ** -12
+    c = Case("q8_0", 150, 256, weights=w, ranks=[16, 24, 8])
+    x, ids = c.rows_of(n, dtype), c.rng.integers(-1, 3, n)
+    ids[:4] = [0, 1, 2, -1]
+    clean, plain = c.run(x, dtype, ids), c.run(x, dtype)
+    scale, a, b = c.known[1]
+    bad = b.copy()
+    bad[45, 3], bad[120, 0] = value, value
+    ta, tb = (torch.tensor(z).to(c.at).cuda() for z in (a, bad))
+    c.ad.set(1, ta, tb, scale)
+    out = c.run(x, dtype, ids)
+    assert torch.equal(out[ids == -1], plain[ids == -1])
+    others = ids != 1
+    c.check(x, out, dtype, ids, rows=others)
+    got, v = host(out)[~others], scale * host(x)[~others] @ a.T
+    fine = np.setdiff1d(np.arange(150), [45, 120])
+    np.testing.assert_allclose(got[:, fine], host(clean)[~others][:, fine], rtol=2 * HALF[dtype], atol=2e-4)
+    for row, j in ((45, 3), (120, 0)):
+        with np.errstate(over="ignore", invalid="ignore"):
+            want = v[:, j] * value
+        if math.isnan(value):
+            assert np.isnan(got[:, row]).all()
+        else:
+            assert (np.sign(got[:, row]) == np.sign(want)).all() and (np.abs(got[:, row]) > 1e20).all()
+    c.ad.set(1, ta, torch.tensor(b).to(c.at).cuda(), scale)
+    assert torch.equal(c.run(x, dtype, ids), clean)
+    c.fine()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [5, 17, 50, 120, 300])
+def test_infinities_of_an_adapter_s_a_stay_with_its_tokens(n, dtype):
+    c = Case("q8_0", 150, 256, ranks=[16, 24, 8], adapter_type="f16")
+    x, ids = c.rows_of(n, dtype), c.rng.integers(-1, 3, n)
+    ids[:4] = [0, 1, 2, -1]
+    clean = c.run(x, dtype, ids)
+    scale, a, b = c.known[1]
+    a = a.copy()
+    a[2, 10], a[20, 200] = math.inf, math.nan
+    c.ad.set(1, torch.tensor(a).half().cuda(), torch.tensor(b).half().cuda(), scale)
+    out = c.run(x, dtype, ids)
+    assert torch.equal(out[ids != 1], clean[ids != 1]) and out[ids == 1].isnan().all()
+    c.fine()
