@@ -9,6 +9,7 @@ released.  All compute happens in liber.so.
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Callable, Mapping
 
 import numpy as np
@@ -367,26 +368,38 @@ class PagedCache:
 _ADAPTER_TYPES = {torch.float16: er.ER_F16, torch.bfloat16: er.ER_BF16}
 
 
-# Scratch that calls on a stream share, one after another: (device, stream) -> (address, bytes, tensor).  A call from Python takes
-# 5 us less than with an allocation of its own.
-_scratch: dict[tuple[int, int], tuple[int, int, torch.Tensor]] = {}
-_SCRATCH_KEPT = 1 << 25
+class _Scratch(threading.local):
+    """What a host thread's calls on a stream share, one after another: (device, stream) -> (address, bytes, tensor).
 
-
-def _scratch_of(index: int, stream: int, need: int) -> tuple[int, int, torch.Tensor]:
-    """Scratch for a call on the current stream of device `index`; the caller keeps the tensor until its launch.
-
-    What a graph captures is the graph's alone, as two graphs may run at once; large scratch goes back to the allocator.
+    A call from Python takes 5 us less than with an allocation of its own.  Not shared between threads: a call is up to four
+    launches, and another thread's may come between them.  It goes with its thread; a thread keeps a few streams', the newest.
     """
-    if need > _SCRATCH_KEPT or torch._C._cuda_isCurrentStreamCapturing():
-        t = torch.empty(need, dtype=torch.uint8, device=f"cuda:{index}")
-        return t.data_ptr(), need, t
-    kept = _scratch.get((index, stream))
-    if kept is None or kept[1] < need:
-        size = max(need, 1 << 20)
-        t = torch.empty(size, dtype=torch.uint8, device=f"cuda:{index}")
-        kept = _scratch[(index, stream)] = (t.data_ptr(), size, t)
-    return kept
+
+    KEPT_BYTES, KEPT_STREAMS = 1 << 25, 8
+
+    def __init__(self):
+        self.kept: dict[tuple[int, int], tuple[int, int, torch.Tensor]] = {}
+
+    def get(self, index: int, stream: int, need: int) -> tuple[int, int, torch.Tensor]:
+        """Scratch for a call on the current stream of device `index`; the caller keeps the tensor until its launch.
+
+        What a graph captures is the graph's alone, as two graphs may run at once; large scratch goes back to the allocator.
+        """
+        if need > self.KEPT_BYTES or torch._C._cuda_isCurrentStreamCapturing():
+            t = torch.empty(need, dtype=torch.uint8, device=f"cuda:{index}")
+            return t.data_ptr(), need, t
+        kept = self.kept.get((index, stream))
+        if kept is None or kept[1] < need:
+            self.kept.pop((index, stream), None)
+            if len(self.kept) >= self.KEPT_STREAMS:
+                del self.kept[next(iter(self.kept))]  # (its stream's own allocations take it from here on, in that stream's order)
+            size = max(need, 1 << 20)
+            t = torch.empty(size, dtype=torch.uint8, device=f"cuda:{index}")
+            kept = self.kept[(index, stream)] = (t.data_ptr(), size, t)
+        return kept
+
+
+_scratch = _Scratch()
 
 
 class Adapters:
@@ -460,7 +473,7 @@ class Matrix:
             stream: int | None = None) -> None:
         """out[t] = W x[t], plus adapter ids[t]'s share where that is not negative (er_matrix_mul).
 
-        Scratch is the current stream's: with a `stream` of its own the call takes some from torch's allocator, and the caller
+        Scratch is the thread's for the current stream: with a `stream` of its own the call takes some from torch's allocator, and the caller
         keeps other users of that memory away until the call is done (by making that stream the current one).
         """
         xs, ys = self._row_tensor(x, self.cols, "x"), self._row_tensor(out, self.rows, "out")
@@ -482,7 +495,7 @@ class Matrix:
             raise er.ErError(f"er_matrix_mul: {er.er_last_error()}", er.ER_EINVAL)
         if stream is None:
             stream = torch._C._cuda_getCurrentRawStream(self._index)
-            work = _scratch_of(self._index, stream, need)
+            work = _scratch.get(self._index, stream, need)
         else:
             own = torch.empty(need, dtype=torch.uint8, device=x.device)
             work = own.data_ptr(), need, own

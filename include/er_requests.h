@@ -43,7 +43,8 @@ ER_API er_status er_adapters_clear(er_adapters *ad, int32_t slot, void *stream);
  *   adapters, ids_dev  both or neither: int32 [n_tokens], the slot of each token; a negative number or an empty slot: none.
  *           A number past the slots gets none too and sets flag bit 1 (er_matrix_mul_error).  A shape of the matrix.
  *   work_dev  er_matrix_mul_work_bytes of scratch, 256-byte aligned.  Its contents need no preparation and mean nothing after
- *           the call; calls that may run at the same time take scratch of their own each (those of one stream share it).
+ *           the call; calls that may run at the same time take scratch of their own each.  Those that one host thread queues on
+ *           one stream share it; other threads' calls, on that stream too, do not: a call is up to four launches.
  * Sums are fp32.  W's values (at most 19 bits) and 16-bit rows enter the products exactly, as fp16 pairs and numbers times
  * powers of two of their row, but for values below 2^-31 (fp16 rows: 2^-28) of their row's largest; fp32 rows as fp16 pairs (2^-22).
  * A row of x with an infinity or a NaN, or one whose largest value is below 2^-112, gives a row of NaN or zeros of y; a row of W

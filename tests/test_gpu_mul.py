@@ -620,3 +620,68 @@ def test_infinities_of_an_adapter_s_a_stay_with_its_tokens(n, dtype):
     out = c.run(x, dtype, ids)
     assert torch.equal(out[ids != 1], clean[ids != 1]) and out[ids == 1].isnan().all()
     c.fine()
+
+
+# ------------------------------------------------------------------------------------------------------------------
+# host threads, streams of one's own
+# ------------------------------------------------------------------------------------------------------------------
+def test_two_host_threads_on_one_stream():
+    """A call is several launches, and another thread's may come between them: each works on memory of its own."""
+    import sys
+    import threading
+    cases = [Case("q8_0", 512, 1024, seed=i, ranks=[16]) for i in range(3)]
+    xs = [c.rows_of(n, d) for c, n, d in zip(cases, (70, 40, 12), ("f32", "bf16", "f16"))]
+    ids = [ints(c.rng.integers(-1, 1, len(x))) for c, x in zip(cases, xs)]
+    want, wrong = [], [0, 0, 0]
+    for c, x, i in zip(cases, xs, ids):
+        want.append(torch.empty((len(x), 512), dtype=x.dtype, device="cuda"))
+        c.m.mul(x, want[-1], adapters=c.ad, ids=i)
+    torch.cuda.synchronize()
+    begin = threading.Barrier(3)
+
+    def work(t):
+        outs = [torch.empty_like(want[t]) for _ in range(50)]
+        begin.wait()
+        for _ in range(8):
+            for o in outs:
+                cases[t].m.mul(xs[t], o, adapters=cases[t].ad, ids=ids[t])
+            wrong[t] += sum(not torch.equal(o, want[t]) for o in outs)
+
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=work, args=(t,)) for t in range(3)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(before)
+    assert wrong == [0, 0, 0]
+    for c in cases:
+        c.fine()
+
+
+def test_kept_scratch_is_bounded_and_goes_with_its_thread():
+    import gc
+    import threading
+    c = Case("q8_0", 64, 4096)
+    x, out = c.rows_of(2000, "bf16"), torch.empty((2000, 64), dtype=torch.bfloat16, device="cuda")  # some 16 MB of scratch
+    torch.cuda.synchronize()
+    gc.collect()
+    before = torch.cuda.memory_allocated()
+
+    def use():
+        for s in [torch.cuda.Stream() for _ in range(30)]:
+            with torch.cuda.stream(s):
+                c.m.mul(x, out)
+        torch.cuda.synchronize()
+        peak.append(torch.cuda.memory_allocated())
+
+    peak = []
+    t = threading.Thread(target=use)
+    t.start()
+    t.join()
+    gc.collect()
+    assert peak[0] - before < 200 << 20
+    assert torch.cuda.memory_allocated() == before
