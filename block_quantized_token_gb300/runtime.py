@@ -402,6 +402,11 @@ class _Scratch(threading.local):
 _scratch = _Scratch()
 
 
+def _stream_of(index: int, stream: int) -> torch.cuda.Stream:
+    """The stream of a number (0: the default one)."""
+    return torch.cuda.ExternalStream(stream, device=f"cuda:{index}") if stream else torch.cuda.default_stream(index)
+
+
 class Adapters:
     """Owns an er_adapters handle: low-rank adapters of one matrix shape, one per slot (er_adapters_* in er_requests.h)."""
 
@@ -473,8 +478,8 @@ class Matrix:
             stream: int | None = None) -> None:
         """out[t] = W x[t], plus adapter ids[t]'s share where that is not negative (er_matrix_mul).
 
-        Scratch is the thread's for the current stream: with a `stream` of its own the call takes some from torch's allocator, and the caller
-        keeps other users of that memory away until the call is done (by making that stream the current one).
+        Scratch is the thread's for the stream that the call goes to, the current one or `stream` (a CUDA stream's number).  A graph
+        that captures the call (torch.cuda.graph) owns what it needs.
         """
         xs, ys = self._row_tensor(x, self.cols, "x"), self._row_tensor(out, self.rows, "out")
         n = x.shape[0]
@@ -488,19 +493,18 @@ class Matrix:
         if torch._C._cuda_getDevice() != self._index:
             with torch.cuda.device(self._index):
                 return self.mul(x, out, adapters, ids, stream)
+        current = torch._C._cuda_getCurrentRawStream(self._index)
+        if stream is not None and stream != current:  # (its scratch then comes from that stream's memory and returns there)
+            with torch.cuda.stream(_stream_of(self._index, stream)):
+                return self.mul(x, out, adapters, ids)
         ad = None if adapters is None else adapters.handle
         t = _ROW_TYPES[x.dtype]
         need = er.er_matrix_mul_work_bytes(self.handle, ad, n, t)
         if not need:
             raise er.ErError(f"er_matrix_mul: {er.er_last_error()}", er.ER_EINVAL)
-        if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(self._index)
-            work = _scratch.get(self._index, stream, need)
-        else:
-            own = torch.empty(need, dtype=torch.uint8, device=x.device)
-            work = own.data_ptr(), need, own
+        work = _scratch.get(self._index, current, need)
         er.er_matrix_mul(self.handle, er.er_matrix_mul_args(n, t, x.data_ptr(), out.data_ptr(), xs, ys, ad, _ptr(ids), work[0],
-                                                            work[1]), stream)
+                                                            work[1]), current)
 
     def error(self) -> tuple[int, int]:
         """(status, flags) of the products so far; synchronises (er_matrix_mul_error)."""

@@ -685,3 +685,73 @@ def test_kept_scratch_is_bounded_and_goes_with_its_thread():
     gc.collect()
     assert peak[0] - before < 200 << 20
     assert torch.cuda.memory_allocated() == before
+
+
+def _scratch_seen(monkeypatch):
+    """(address, bytes) of the scratch of every call from here on."""
+    from block_quantized_token_gb300 import er
+    seen, call = [], er.er_matrix_mul
+
+    def spy(mat, args, stream=0):
+        seen.append((args.work, args.work_bytes))
+        call(mat, args, stream)
+
+    monkeypatch.setattr(er, "er_matrix_mul", spy)
+    return seen
+
+
+@pytest.mark.parametrize("n", [20, 20000])
+def test_scratch_of_a_call_on_a_given_stream_is_not_given_away(n, monkeypatch):
+    """mul(..., stream=s): while s still works on it, the current stream's allocations do not get the scratch."""
+    c = Case("q8_0", 300, 1024, ranks=[16])
+    x, ids = c.rows_of(n, "bf16"), ints(c.rng.integers(-1, 1, n))
+    want, out = torch.empty((n, 300), dtype=torch.bfloat16, device="cuda"), torch.zeros((n, 300), dtype=torch.bfloat16, device="cuda")
+    c.m.mul(x, want, adapters=c.ad, ids=ids)
+    torch.cuda.synchronize()
+    seen, s = _scratch_seen(monkeypatch), torch.cuda.Stream()
+    for _ in range(3):
+        done = torch.cuda.Event()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200_000_000)
+        c.m.mul(x, out, adapters=c.ad, ids=ids, stream=s.cuda_stream)
+        done.record(s)
+        at, size = seen[-1]
+        held = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        assert not done.query()  # (else nothing is shown)
+        assert all(t.data_ptr() + size <= at or at + size <= t.data_ptr() for t in held)
+        for t in held:
+            t.fill_(255)
+        s.synchronize()
+        assert torch.equal(out, want)
+        out.zero_()
+        del held, t
+    # the default stream by its number, and the current one by its own
+    for number in (0, torch.cuda.current_stream().cuda_stream):
+        c.m.mul(x, out, adapters=c.ad, ids=ids, stream=number)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        out.zero_()
+    c.fine()
+
+
+def test_a_call_on_a_given_stream_is_captured():
+    """The stream that captures is another than the current one: the graph still owns its scratch."""
+    c = Case("q8_0", 300, 1024, ranks=[16])
+    x, ids = c.rows_of(50, "bf16"), ints(c.rng.integers(-1, 1, 50))
+    want, out = c.run(x, "bf16", ids.cpu().numpy()), torch.zeros((50, 300), dtype=torch.bfloat16, device="cuda")
+    s, g, other = torch.cuda.Stream(), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        other.wait_stream(s)
+        with torch.cuda.stream(other):
+            c.m.mul(x, out, adapters=c.ad, ids=ids, stream=s.cuda_stream)
+        s.wait_stream(other)
+    c.m.mul(c.rows_of(70, "f32"), torch.empty((70, 300), device="cuda"), stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    held = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    del held
+    c.fine()
