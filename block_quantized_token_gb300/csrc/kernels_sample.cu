@@ -789,9 +789,10 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleArgs 
                 fresh = false;
             }
         };
-        // (kk candidates or fewer: their sum; without top-k: all masses'.  Candidates' masses are in the bins, the others' outside)
+        // (fewer than kk candidates: their sum, as what is no candidate then has no mass; as many: X may be the groups' bound, and what
+        // is below it is left out.  Without top-k all masses' sum.  Candidates' masses are in the bins, the others' outside)
         unsigned long long inside = 0;
-        if (has_k && kk < (int)nc) {
+        if (has_k && kk <= (int)nc) {
             inside = sum = search(false, kk);
         } else {
             whole();

@@ -320,3 +320,18 @@ def test_top_k_of_either_integer_type():
         k.fill_(number)
         g.replay()
         assert torch.equal(tokens[:n], run(x, u, top_k=[min(number, 2 ** 31 - 1)] * n)[0])
+
+
+def test_top_k_that_is_all_that_reaches_the_groups_bound():
+    """As many elements reach the bound that groups of elements give as top-k asks for, and more than the sort takes: the others,
+    whose masses are no smaller than anyone's, are still left out."""
+    v = 65536
+    x = torch.zeros((4, v), device="cuda")
+    at = np.concatenate([r * 8704 + 4 * np.arange(257) for r in range(8)])  # 8 CTAs' parts, the first element of a thread's four
+    at = at[at < v]
+    x[:, torch.tensor(at, device="cuda")] = 1.0
+    u = [0.05, 0.35, 0.65, 0.95]
+    for k in (len(at), len(at) - 1, len(at) + 1, 2049):
+        check(x, u, top_k=[k] * 4)
+        check(x, u, top_k=[k] * 4, min_p=[0.3, 0.5, 0.0, 1.0])
+        check(x, u, top_k=[k] * 4, top_p=[1.0, 0.9, 0.99, 0.5])
