@@ -896,8 +896,10 @@ static cudaError_t sm_launch(const SampleArgs &a, cudaStream_t st) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // (more than 48 KB of shared memory: an attribute of the device's kernel, set on every call as devices may differ)
-    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm_smem(a.E));
+    // (more than 48 KB of shared memory: an attribute of the device's kernel, set on every call as devices may differ, and to the
+    // same number by every call: other host threads' vocabularies are larger)
+    static const int most = (int)sm_smem(sm_elements(ER_SAMPLE_MAX_VOCAB));
+    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, sample_kernel<T>, a) : e;
 }
 

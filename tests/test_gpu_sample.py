@@ -335,3 +335,32 @@ def test_top_k_that_is_all_that_reaches_the_groups_bound():
         check(x, u, top_k=[k] * 4)
         check(x, u, top_k=[k] * 4, min_p=[0.3, 0.5, 0.0, 1.0])
         check(x, u, top_k=[k] * 4, top_p=[1.0, 0.9, 0.99, 0.5])
+
+
+def test_two_host_threads_with_other_vocabularies():
+    """The kernel's shared memory is a setting of the device's: one thread's call does not lower it under another's."""
+    import threading
+
+    from block_quantized_token_gb300 import runtime
+    rng = np.random.default_rng(17)
+    xs = [torch.tensor(bulk(rng, 2, v)).float().cuda() for v in (300, 262144)]
+    u, failed, begin = dev([0.3, 0.8]), [], threading.Barrier(2)
+    want = [run(x, [0.3, 0.8], top_k=[40, 0])[0] for x in xs]
+    k = dev([40, 0], torch.int32)
+
+    def work(x, w):
+        t = torch.empty(2, dtype=torch.int32, device="cuda")
+        begin.wait()
+        try:
+            for _ in range(3000):
+                runtime.sample(x, u, t, top_k=k)
+            assert torch.equal(t, w)
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(xs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
