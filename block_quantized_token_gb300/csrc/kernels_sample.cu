@@ -68,7 +68,11 @@ ER_DEV SmScale sm_scale(float T) {
     if (!isfinite(s.cl)) s.cl = 0.f;
     return s;
 }
-// M - x for finite M; of finite numbers at most float32's largest
+// At temperatures above SM_WIDE logits further apart than float32's largest number have a mass.  A row and its temperature then count
+// times 2^-40: differences are numbers, and so is the temperature's reciprocal.  (Only logits below 2^-86 lose bits by it.)
+constexpr float SM_WIDE = 1e30f, SM_WIDE_BY = 0x1p-40f;
+
+// M - x for finite M, at most float32's largest number (where it is cut off, the mass is none)
 ER_DEV float sm_dist(float x, float M) { return fminf(M - x, 3.402823466e38f); }
 
 // (M - x) / (T ln 2) as two floats: the exact difference (Knuth's sum) times 1 / (T ln 2)
@@ -295,6 +299,8 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleArgs 
 
     float temp = a.temperature ? a.temperature[row] : 1.f;
     if (temp > 0.f) temp = fmaxf(temp, 0x1p-120f);  // (1 / (T ln 2) stays a number)
+    const bool wide = temp > SM_WIDE;
+    if (wide) temp *= SM_WIDE_BY;
     const long long k = a.top_k ? a.top_k[row] : a.top_k64 ? a.top_k64[row] : 0;
     const int kk = k <= 0 || k >= a.V ? a.V : (int)k;
     const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f;
@@ -413,9 +419,14 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleArgs 
         __syncthreads();
         M = 0.f;
         bounded = false;
+    } else if (wide) {
+        __syncthreads();
+        for (int i = tid; i < n; i += SM_THREADS) xs[i] *= SM_WIDE_BY;
+        __syncthreads();
+        M *= SM_WIDE_BY;
     }
     sc.M = M;
-    const bool wide = temp > 1e30f;  // (differences may be cut off)
+    // (-infinity may be no octave away from M at an infinite temperature)
     auto mass = [&](float x) { return wide && x == -INFINITY ? 0ull : sm_mass(x, sc, S.table); };
     // the answer: element x, index i, of kept masses' sum W (which is at least the largest element's mass, 1)
     auto answer = [&](float x, int i, unsigned long long W) {
@@ -434,7 +445,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleArgs 
         // ---- what can be kept is at least X: within R, or the groups' bound
         float X = M - R;
         X = fmaxf(X - (fabsf(X) + fabsf(M)) * 0x1p-22f, -3.402823466e38f);  // (rounding, of M - R's terms too)
-        if (has_k && bounded) X = fmaxf(X, sm_value((unsigned long long)group << 32));
+        if (has_k && bounded) X = fmaxf(X, sm_value((unsigned long long)group << 32) * (wide ? SM_WIDE_BY : 1.f));
         auto candidate = [&](float x) { return x >= X; };
         // f(element, its place) for all elements of this CTA, in some order
         auto each = [&](auto f) {

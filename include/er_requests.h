@@ -86,7 +86,7 @@ ER_API er_status er_matrix_mul_inject_wait_shortfall(er_matrix *mat, int32_t ext
  * -infinity): token -1 and -infinity.  Arrays of parameters are [n_rows] or NULL (temperature 1, nothing left out); top_k64_dev is
  * top_k in 64 bits, for callers who have it so: with both ER_EINVAL.
  * The choice is that of the definition in 64 bits, but where a border lies within some 2^-40 of the sum; masses below 2^-45 of
- * the largest count as none, and differences of finite logits past float32's largest number as that.  vocab: at most
+ * the largest count as none, and at temperatures above 1e30 logits below 2^-86 are multiples of 2^-109.  vocab: at most
  * ER_SAMPLE_MAX_VOCAB (else ER_EUNSUPPORTED).  One launch, no scratch. */
 #define ER_SAMPLE_MAX_VOCAB 262144
 typedef struct {

@@ -364,3 +364,17 @@ def test_two_host_threads_with_other_vocabularies():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("temperature", [9e29, 1.1e30, 3e37, 1e38, 3.4e38, math.inf])
+@pytest.mark.parametrize("vocab", [4, 700, 30000])
+def test_differences_past_the_largest_number(vocab, temperature):
+    """Finite logits further apart than float32's largest number, at temperatures where it counts."""
+    rng = np.random.default_rng(vocab)
+    x = rng.uniform(-3.4e38, 3.4e38, (4, vocab))
+    x[0, :4], x[1, :4], x[2, :4] = [3e38, -3e38, 0.0, 1e38], [-3.4e38, 3.4e38, -1e38, 3.4e38], [3.4e38, -3.4e38, -3.3e38, -math.inf]
+    x = torch.tensor(x).float().cuda()
+    for u in ([0.9983, 0.3141, 0.9871, 0.4713], [0.1057, 0.8969, 0.6131, 0.0117]):
+        for kw in ({}, dict(top_k=[3] * 4), dict(top_p=[0.99, 0.9, 0.5, 0.7]), dict(min_p=[1e-4, 0.5, 1e-9, 0.2]),
+                   dict(top_k=[3, 2500, 20, 300], top_p=[0.999] * 4)):
+            check(x, u, temperature=[temperature] * 4, **kw)
