@@ -541,6 +541,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleArgs 
                 ms[j] = i < m ? mass(sm_value(S.list[i])) : 0;
                 incl += ms[j];
             }
+            if (tid == 0) S.keeps = SM_LIST, S.pick = ~0ull;
             const unsigned long long before = sm_scan(incl, S.w64, &total) - incl;
             const int nk = min(kk, m);
             if (has_k && has_p) {  // the sum over the first kk
@@ -554,7 +555,8 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleArgs 
                 sum = S.sum;
             }
             const unsigned long long most = has_p ? sm_times<true>(p, sum) : ~0ull;
-            {  // what is kept is the order's beginning: its end tells its number and its sum
+            {  // what is kept is the order's beginning: its end tells its number and its sum.  (Masses of logits next to each other may
+               // rise by some units, so min-p's may come to an end several times: the first counts, which has the least sum too)
                 unsigned long long b = before, next = 0;
                 bool kept[PL + 1];
                 auto keep = [&](int i, unsigned long long b, unsigned long long m) {
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleArgs 
 #pragma unroll
                 for (int j = 0; j < PL; ++j) {
                     b += ms[j];
-                    if (kept[j] && !kept[j + 1]) S.keeps = PL * tid + j + 1, S.pick = b;
+                    if (kept[j] && !kept[j + 1]) atomicMin(&S.keeps, PL * tid + j + 1), atomicMin(&S.pick, b);
                 }
             }
             __syncthreads();

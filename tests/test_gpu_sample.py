@@ -378,3 +378,28 @@ def test_differences_past_the_largest_number(vocab, temperature):
         for kw in ({}, dict(top_k=[3] * 4), dict(top_p=[0.99, 0.9, 0.5, 0.7]), dict(min_p=[1e-4, 0.5, 1e-9, 0.2]),
                    dict(top_k=[3, 2500, 20, 300], top_p=[0.999] * 4)):
             check(x, u, temperature=[temperature] * 4, **kw)
+
+
+def test_min_p_on_masses_that_are_next_to_each_other():
+    """Logits so close that their masses, whole numbers within 5 of the exact ones, do not all fall with them, with min_p's mass
+    among them: which of these are kept is open, but what is kept is one beginning of the order, and a token is always drawn from it."""
+    rng = np.random.default_rng(16)
+    v, n = 300, 64
+    for _ in range(30):
+        p = np.float32(rng.uniform(2e-5, 9e-5))
+        top = np.float32(-math.log(float(p)))  # logits next to 0 then have masses next to p
+        at = float(top) + math.log(float(p))
+        row = at + (np.arange(v) - v / 2) * 0.08 / (float(p) * 2.0 ** 44)  # 0.08 units of mass apart
+        row = row[rng.permutation(v)].astype(np.float32)
+        row[0] = top
+        x = torch.tensor(np.broadcast_to(row, (n, v)).copy()).cuda()
+        u = 1.0 - np.linspace(1e-5, 0.9 * v * float(p) / 2, n)
+        tokens, lp = run(x, u, min_p=[float(p)] * n, top_k=[v - 1] * n)
+        t, l = tokens.cpu().numpy(), lp.cpu().double().numpy()
+        assert (t >= 0).all()
+        z = row[t].astype(np.float64) - float(top)
+        count = (np.exp(z - l) - 1.0) / float(p)  # elements kept beside the largest, within what the log-probability is exact to
+        tol = 3e-6 / float(p)
+        assert np.ptp(count) < 2 * tol and -tol < count.min() and count.max() < v
+        rank = np.argsort(np.argsort(-row.astype(np.float64), kind="stable"))
+        assert (rank[t] <= count + tol).all()
