@@ -1238,15 +1238,14 @@ static int mu_share(int rem, int UPR, int num_sms) {
     return best;
 }
 
-bool mul_plan(int R, int UPR, int n, int type, int r16, int num_sms, MulPlan *p) {
+// n >= 1, 16 R n <= 2^40 + 2^28: fewer than 2^28 tiles, as NT is 64 at least where there are two tiles of tokens
+void mul_plan(int R, int UPR, int n, int type, int r16, int num_sms, MulPlan *p) {
     const int most = type == ER_F32 ? MU_REG_TOKENS : MU_MAX_TOKENS;
-    if (n < 1) return false;
     p->ntl = (n + most - 1) / most;
     p->NT = ((n + p->ntl - 1) / p->ntl + 15) / 16 * 16;
     p->ntl = (n + p->NT - 1) / p->NT;
     p->MT = (R + 7) / 8;
     const long long tiles = (long long)p->MT * p->ntl;
-    if (tiles > 2147483647ll / 1024) return false;
     // whole tiles for every CTA first; of what is left each tile for a CTA, or for S of them, or all of it spread evenly
     p->waves = (int)(tiles / num_sms);
     p->rem = (int)(tiles % num_sms);
@@ -1265,12 +1264,11 @@ bool mul_plan(int R, int UPR, int n, int type, int r16, int num_sms, MulPlan *p)
         p->waves = p->rem = p->share = 0;
         p->grid = p->slices * max(1, min((R + 1) / 2, num_sms / p->slices));
         p->off_cnt = p->off_k = p->bytes = p->off_part + (p->slices > 1 ? up((size_t)p->slices * n * 16 * R * sizeof(float)) : 0);
-        return true;
+        return;
     }
     p->off_cnt = p->off_part + (p->rem ? up(((size_t)p->grid * 2 * p->NT + 16) * 128 * sizeof(float)) : 0);
     p->off_k = p->off_cnt + up((size_t)p->rem * sizeof(int));
     p->bytes = p->off_k + (p->extra ? up((size_t)p->ntl * (1 + 8 * p->extra) * sizeof(int)) : 0);
-    return true;
 }
 
 template <int QT, bool F32, int TOK>

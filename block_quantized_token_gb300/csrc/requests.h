@@ -34,7 +34,7 @@ struct MulPlan {
     int slices;                // few tokens (kernels_mul_few.cu): slices of the columns; else 0
     size_t off_x, off_up, off_v, off_part, off_cnt, off_k, bytes;
 };
-bool mul_plan(int R, int UPR, int n, int type, int r16, int num_sms, MulPlan *p);
+void mul_plan(int R, int UPR, int n, int type, int r16, int num_sms, MulPlan *p);
 cudaError_t mul_prepare();  // kernel attributes
 int mul_few_slices(int UPR, int n, int planes);
 cudaError_t mul_few_prepare();
