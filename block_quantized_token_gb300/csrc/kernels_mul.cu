@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(256) mul_front_kernel(const T *x, long long st
     if (any) {
         const bool vec = ((uintptr_t)row & 15) == 0;
         const uint4 *a = reinterpret_cast<const uint4 *>(ad.a + (((size_t)id * ad.r16 + j0) * ad.Kp) * 2);
-        // A's rows reach 2^15, so x enters times 2^-15; where a sum overflows all the same (x next to float32's largest), times 2^-60
-        for (float down = 0x1p-15f;; down = 0x1p-60f) {
+        // where a sum overflows (A's rows reach 2^15, x may be next to float32's largest), x enters times 2^-60
+        for (float down = 1.f;; down = 0x1p-60f) {
             float s[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[j] = 0.f;
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(256) mul_front_kernel(const T *x, long long st
             if (tid < 8)
                 for (int w = 0; w < 8; ++w) r += sums[w][tid];
             if (tid < 8) vs[tid] = v[(size_t)t * ad.r16 + j0 + tid] = r * (ad.down[(size_t)id * ad.r16 + j0 + tid] / down);
-            if (!__syncthreads_or(!isfinite(r)) || down < 0x1p-15f) break;
+            if (!__syncthreads_or(!isfinite(r)) || down < 1.f) break;
         }
     }
     if (nksteps) {

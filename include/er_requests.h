@@ -47,9 +47,8 @@ ER_API er_status er_adapters_clear(er_adapters *ad, int32_t slot, void *stream);
  *           one stream share it; other threads' calls, on that stream too, do not: a call is up to four launches.
  * Sums are fp32.  W's values (at most 19 bits) and 16-bit rows enter the products exactly, as fp16 pairs and numbers times
  * powers of two of their row, but for values below 2^-31 (fp16 rows: 2^-28) of their row's largest; fp32 rows as fp16 pairs (2^-22).
- * A row of x with an infinity or a NaN, or one whose largest value is below 2^-112, gives a row of NaN or zeros of y; a row of W
- * with such a scale a column of NaN; infinities and NaN of an adapter stay with the tokens of its slot.  Results do not depend on
- * timing.
+ * A row of x with an infinity or a NaN gives a row of NaN of y, a row of W with such a scale a column of NaN; infinities and NaN
+ * of an adapter stay with the tokens of its slot.  Results do not depend on timing.
  * ER_EINVAL: sizes, strides, alignment, a handle of another device than the current one or of another shape; n_tokens *
  * rows, n_tokens * cols must be below 2^40, n_tokens below 2^24. */
 typedef struct {

@@ -755,3 +755,23 @@ def test_a_call_on_a_given_stream_is_captured():
         assert torch.equal(out, want)
     del held
     c.fine()
+
+
+@pytest.mark.parametrize("n", [5, 40, 100, 300])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_next_to_the_least_number(n, dtype):
+    """Rows whose largest value is below 2^-112 enter times 2^126: exactly (fp32 rows too: their least bit is 2^-149, 2^-23 then).
+    Results are rounded to the type's least numbers, and so are A x's: 2^-150 of each at most, times B."""
+    c = Case("q8_0", 140, 256, ranks=[16, 24])
+    x = c.rng.uniform(0.5, 1.0, (n, 256)) * 2.0 ** c.rng.integers(-140, -105, (n, 1))
+    x = torch.tensor(x).to(DT[dtype]).cuda()
+    least = 2.0 ** -149 if dtype == "f32" else 2.0 ** -133
+    for ids in (None, c.rng.integers(-1, 2, n)):
+        out = c.run(x, dtype, ids)
+        y, (s, t) = orq.product(host(x), c.w, ids, c.known)
+        tol = ((12 * 4 + 100) * 2.0 ** -23 + 2.0 ** -21) * s + HALF[dtype] * np.abs(y) + least
+        if ids is not None:
+            tol += ((256 / 16 + 80 + 24) * 2.0 ** -23 + (2.0 ** -22 if dtype == "f32" else 2.0 ** -16)) * t
+            tol += 2.0 ** -149 * max(np.abs(b).sum(1).max() for _, _, b in c.known.values())
+        assert (np.abs(host(out) - y) <= tol).all(), float((np.abs(host(out) - y) / tol).max())
+    c.fine()
