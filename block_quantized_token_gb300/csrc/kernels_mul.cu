@@ -16,7 +16,9 @@
 // fp32 tokens 172 and 191 us.  Here 64 tokens cost what 16 do (55 us), there twice as much for every 8 more.
 //
 // Weights.  A value d q has up to 19 bits.  Times a power of two of its row (the largest |d| times the largest code to
-// [2^14, 2^15)) it enters as two fp16 numbers: hi = fp16(d q), lo = d q - hi, exactly.
+// [2^14, 2^15)) it enters as two fp16 numbers: hi = fp16(d q), lo = d q - hi, exactly.  (A scale below some 2^-21 of a row's largest
+// is then a subnormal fp16 number; it loses bits, 2^-25 of 2^7 (Q4_0: 2^11) at most, where the largest is 256 (4096) and more, as
+// d has none below 2^-24.)
 //
 // Work.  A tile is 128 rows of W times NT tokens.  Every CTA takes whole tiles first (tile w * grid + cta, so that CTAs that run
 // at the same time share tiles of x and W in L2).  Of the tiles left over each is one CTA's, or S CTAs', or all of them are cut

@@ -45,8 +45,11 @@ ER_API er_status er_adapters_clear(er_adapters *ad, int32_t slot, void *stream);
  *   work_dev  er_matrix_mul_work_bytes of scratch, 256-byte aligned.  Its contents need no preparation and mean nothing after
  *           the call; calls that may run at the same time take scratch of their own each.  Those that one host thread queues on
  *           one stream share it; other threads' calls, on that stream too, do not: a call is up to four launches.
- * Sums are fp32.  W's values (at most 19 bits) and 16-bit rows enter the products exactly, as fp16 pairs and numbers times
- * powers of two of their row, but for values below 2^-31 (fp16 rows: 2^-28) of their row's largest; fp32 rows as fp16 pairs (2^-22).
+ * Sums are fp32; beyond 16 tokens the tensor cores add, which cut a sum off at 2^-23 of it 8 times for 64 columns: in calls of up to
+ * 128 tokens sums of 16 such steps (fp32 rows: of 2, in calls of any size) go on to nearest, in larger ones all columns add up there.
+ * 16-bit rows enter the products exactly, as fp16 numbers times a power of two of their row, but for values below 2^-31 (fp16 rows:
+ * 2^-28) of their row's largest; fp32 rows as fp16 pairs (2^-22).  W's values (at most 19 bits) enter exactly; beyond 16 tokens, where
+ * a row's largest scale is 256 and more (Q4_0: 4096), within 2^-32 (2^-36) of that scale times 128 (8).
  * A row of x with an infinity or a NaN gives a row of NaN of y, a row of W with such a scale a column of NaN; infinities and NaN
  * of an adapter stay with the tokens of its slot.  Results do not depend on timing.
  * ER_EINVAL: sizes, strides, alignment, a handle of another device than the current one or of another shape; n_tokens *

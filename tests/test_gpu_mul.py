@@ -775,3 +775,39 @@ def test_rows_next_to_the_least_number(n, dtype):
             tol += 2.0 ** -149 * max(np.abs(b).sum(1).max() for _, _, b in c.known.values())
         assert (np.abs(host(out) - y) <= tol).all(), float((np.abs(host(out) - y) / tol).max())
     c.fine()
+
+
+@pytest.mark.parametrize("n", [3, 40, 300])
+@pytest.mark.parametrize("w_type", ["q8_0", "q4_0"])
+def test_scales_far_apart_in_a_row(w_type, n):
+    """A row's scales from fp16's largest to its least.  Up to 16 tokens every weight is exact; else d times the row's power of two is
+    rounded to 2^-24 / 2 where the largest scale is 256 (Q4_0: 4096) and more: a value's error is at most 2^-32 (2^-36) of the row's largest
+    scale times 128 (8).  x reads single weights back."""
+    from block_quantized_token_gb300 import runtime
+    rng = np.random.default_rng(12)
+    rows, cols = 64, 128
+    nb = cols // 32
+    d = 2.0 ** rng.uniform(-14, 15.9, (rows, nb)) * rng.choice([-1, 1], (rows, nb))
+    d[:, 0] = 2.0 ** rng.uniform(8, 15.9, rows)
+    d[0], d[1], d[2] = [256.0, 2.0 ** -14 * (1 + 2.0 ** -10), 2.0 ** -20, 2.0 ** -24], [65504.0, 2.0 ** -14, 1.0, 2.0 ** -24], 2.0 ** -24
+    raw = synth.quantize(np.ones((rows, cols), np.float32), w_type).reshape(rows, nb, -1).copy()
+    raw[..., :2] = np.ascontiguousarray(d.astype(np.float16)).view(np.uint8).reshape(rows, nb, 2)
+    raw[..., 2:] = rng.integers(0, 256, raw[..., 2:].shape)
+    raw = raw.reshape(-1)
+    w = oracle.dequant(raw, w_type, rows, cols)
+    m = runtime.Matrix(w_type, rows, cols, torch.from_numpy(raw).cuda())
+    largest = np.abs(d.astype(np.float16).astype(float)).max(1) * (128 if w_type == "q8_0" else 8)
+    least = largest >= (256 * 128 if w_type == "q8_0" else 4096 * 8)
+    for c0 in range(0, cols, n):
+        k = min(n, cols - c0)
+        x = torch.zeros((n, cols), device="cuda")
+        x[torch.arange(k), torch.arange(c0, c0 + k)] = 1.0
+        out = torch.empty((n, rows), device="cuda")
+        m.mul(x, out)
+        got, want = host(out)[:k], w[:, c0:c0 + k].T
+        off = np.abs(got - want) - 2.0 ** -24 * np.abs(want)  # (fp32 holds every weight: the rest is for sums)
+        if n <= 16:
+            assert (off <= 0).all()
+        else:
+            assert (off <= (least * largest * 2.0 ** (-32 if w_type == "q8_0" else -36))).all()
+    assert m.error()[1] == 0
