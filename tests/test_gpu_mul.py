@@ -811,3 +811,62 @@ def test_scales_far_apart_in_a_row(w_type, n):
         else:
             assert (off <= (least * largest * 2.0 ** (-32 if w_type == "q8_0" else -36))).all()
     assert m.error()[1] == 0
+
+
+@pytest.mark.parametrize("w_type", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n", [3, 16, 40, 100, 300])
+def test_the_low_bits_of_weights_count_in_wide_products(n, dtype, w_type):
+    """Columns by turns of 32: scales d and d + 1 unit of fp16, codes q; x is +1 and -1 by turns (of a size by token).  With w = d q,
+    2^10 <= |d| / unit < 2^11, y is half the columns' sum of q unit: at least 2^-11 of it a column, while every partial sum stays
+    below 64 w.  What the sums lose: at most 8 (fp32: 12) additions a step, cut off at 2^-23 of 64 w:
+        |y - exact| <= 12 n_steps 2^-23 64 w + half a step of y
+    (few tokens add blocks of 32 in fewer additions).  At 14336 columns that is 0.021 w + ..., and y = 7168 q unit >= 3.5 w.  The high
+    halves alone step by 2^-11 w and more, as much as a column's share of y: without the low ones y would be another number."""
+    from block_quantized_token_gb300 import runtime
+    rows, cols = 40, 14336
+    rng = np.random.default_rng(11)
+    nb = cols // 32
+    base = (1024 + rng.integers(0, 1022, rows)) * 2.0 ** -18
+    d = np.repeat(base[:, None], nb, 1)
+    d[:, 1::2] += 2.0 ** -18
+    q = rng.integers(65, 127, (rows, 1)) if w_type == "q8_0" else rng.integers(5, 8, (rows, 1))
+    head = np.ascontiguousarray(d.astype(np.float16)).view(np.uint8).reshape(rows, nb, 2)
+    if w_type == "q8_0":
+        body = np.broadcast_to(q[:, :, None], (rows, nb, 32)).astype(np.int8).view(np.uint8)
+    else:
+        body = np.broadcast_to(((q + 8) * 17)[:, :, None], (rows, nb, 16)).astype(np.uint8)
+    raw = np.ascontiguousarray(np.concatenate([head, body], 2)).reshape(-1)
+    w = oracle.dequant(raw, w_type, rows, cols)
+    m = runtime.Matrix(w_type, rows, cols, torch.from_numpy(raw).cuda())
+    sign = np.where(np.arange(cols) // 32 % 2, -1.0, 1.0)
+    size = 2.0 ** rng.integers(-3, 4, (n, 1))
+    x = torch.tensor(sign * size).to(DT[dtype]).cuda()
+    out = torch.empty((n, rows), dtype=DT[dtype], device="cuda")
+    m.mul(x, out)
+    y = host(x) @ w.T
+    top = 64 * np.abs(w).max(1) * size
+    tol = 12 * (cols // 64) * 2.0 ** -23 * top + HALF[dtype] * np.abs(y)
+    assert (np.abs(host(out) - y) <= tol).all(), float((np.abs(host(out) - y) / tol).max())
+    assert (tol < 0.02 * np.abs(y)).all()  # (the tolerance tells the two apart)
+    assert m.error()[1] == 0
+
+
+@pytest.mark.parametrize("n", [5, 16, 17, 100, 300])
+@pytest.mark.parametrize("cols", [4096, 14336])
+def test_fp32_rows_in_norm(cols, n):
+    """The error in norm, where an output's own tolerance is wide.  Random terms: partial sums of k of K terms are sqrt(k / K) of
+    the whole sum's size, so additions that cut off lose at most 2^-23 of 2 / 3 of it each on average.  24 in the tensor cores (by then
+    the partial sum is of two steps: sqrt(2 / n_steps)), the others to nearest and in turn, by chance: n_steps of 2^-24 each
+    at most; halves of x 2^-22, of terms by chance; W exactly:
+        |y - exact| <= (24 sqrt(2 / n_steps) 2^-23 sqrt(n_steps) + n_steps 2^-24 + 2^-21) |exact| < (n_steps 2^-24 + 2^-17.5) |exact|
+    W's low halves (2^-12 of a weight by chance, 2.4e-4) or x's would show."""
+    c = Case("q8_0", 200, cols)
+    x = c.rows_of(n, "f32")
+    y = host(x) @ c.w.T
+    steps = cols // 64
+    bound = steps * 2.0 ** -24 + 2.0 ** -17.5
+    assert bound < 1e-4 / 4
+    err = np.linalg.norm(host(c.run(x, "f32")) - y) / np.linalg.norm(y)
+    assert err <= bound, (err, bound)
+    c.fine()
