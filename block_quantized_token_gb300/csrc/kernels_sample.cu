@@ -127,7 +127,7 @@ struct alignas(16) SmShared {
     unsigned long long top;   // the largest element: (order key, ~index)
     uint32_t group;           // an order key that the largest elements of q groups reach
     float least;              // the least candidate
-    unsigned long long sum, sum_in;  // masses' sums
+    unsigned long long sum;   // masses' sum
     unsigned listed;          // elements for `list`
     uint32_t kmin, kmax;      // of a range that is split again
     unsigned ties;

@@ -870,3 +870,16 @@ def test_fp32_rows_in_norm(cols, n):
     err = np.linalg.norm(host(c.run(x, "f32")) - y) / np.linalg.norm(y)
     assert err <= bound, (err, bound)
     c.fine()
+
+
+@pytest.mark.parametrize("dtype,adapter_type", [("f32", "f16"), ("f16", "bf16"), ("bf16", "bf16")])
+def test_the_largest_ranks_and_the_last_slot(dtype, adapter_type):
+    """Ranks of 129 to 256 beside small ones, in the last of 4096 slots too."""
+    c = Case("q4_0", 100, 288, ranks=[256, 200, 3], adapter_type=adapter_type, slots=4096, max_rank=256)
+    c.put(4095, 129)
+    for n in (2, 16, 17, 64, 65, 130, 300):
+        for pick in ([0], [-1, 0, 1, 2, 4095], [2, 4095]):
+            ids = c.rng.choice(pick, n)
+            x = c.rows_of(n, dtype)
+            c.check(x, c.run(x, dtype, ids), dtype, ids)
+    c.fine()
