@@ -128,6 +128,7 @@ struct alignas(16) SmShared {
     uint32_t group;           // an order key that the largest elements of q groups reach
     float least;              // the least candidate
     unsigned long long sum;   // masses' sum
+    unsigned long long pad;   // (where the fields behind it lie decides spills: 16 bytes with it, 48 without, 128 x 128256 91 and 99 us)
     unsigned listed;          // elements for `list`
     uint32_t kmin, kmax;      // of a range that is split again
     unsigned ties;
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleArgs 
         int where = 0;
         bool any = false;
         auto take = [&](float x, int i) {
-            x = isnan(x) ? -INFINITY : x;  // never chosen
+            x = fmaxf(x, -INFINITY) + 0.f;  // NaN: never chosen; -0 is 0, a tie that goes by index
             if (x > best) best = x, where = i;
             return x;
         };

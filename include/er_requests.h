@@ -78,7 +78,7 @@ ER_API er_status er_matrix_mul_inject_wait_shortfall(er_matrix *mat, int32_t ext
 /* A token of each row of logits, by its request's parameters and a given random number, beside er_decode_step's greedy argmax.
  * Of row i ([vocab] values of `type`, rows `stride` values apart), with T = temperature, in this order:
  *   1. w_j = exp((x_j - max x) / T).  NaN and -infinity have no mass; of +infinities every one has mass 1 and nothing else any.
- *   2. in the order of falling logit, ties by index, the first top_k are kept (top_k <= 0 or >= vocab: all);
+ *   2. in the order of falling logit, ties by index (-0 and 0 tie), the first top_k are kept (top_k <= 0 or >= vocab: all);
  *   3. of these the ones before which the sum of w is below top_p times their sum, the first always (top_p >= 1 or NaN: all);
  *   4. of these the ones with w_j >= min_p, the first always (min_p <= 0 or NaN: all).
  * tokens_dev[i]: the lowest index at which the running sum of the kept w, in the order of the vocabulary, is above uniform_dev[i]

@@ -403,3 +403,22 @@ def test_min_p_on_masses_that_are_next_to_each_other():
         assert np.ptp(count) < 2 * tol and -tol < count.min() and count.max() < v
         rank = np.argsort(np.argsort(-row.astype(np.float64), kind="stable"))
         assert (rank[t] <= count + tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab", [5, 3000, 60000])
+def test_negative_zeros_tie_with_zeros(vocab, dtype):
+    """-0 and 0 are equal logits: the lower index comes first, among the largest as among top-k's and top-p's last."""
+    rng = np.random.default_rng(vocab)
+    x = np.zeros((5, vocab))
+    x[1] = rng.integers(-1, 1, vocab) / 64.0
+    x[2] = rng.integers(0, 2, vocab) / 64.0
+    x[3] = np.where(rng.random(vocab) < 0.5, -math.inf, 0.0)
+    x[4] = rng.integers(-2, 3, vocab)
+    x[(x == 0) & (rng.random(x.shape) < 0.5)] = -0.0
+    x[0, 0] = -0.0
+    x = torch.tensor(x).to(DT[dtype]).cuda()
+    assert bool(torch.signbit(x[0, 0]))
+    for kw in ({}, dict(temperature=[0.0] * 5), dict(top_k=[1] * 5), dict(top_k=[vocab // 3 + 1] * 5), dict(top_p=[0.37] * 5),
+               dict(top_k=[vocab // 2 + 1] * 5, top_p=[0.73] * 5), dict(top_k=[2100] * 5, min_p=[0.99] * 5)):
+        check(x, [0.1357, 0.3511, 0.5713, 0.7331, 0.9177], **kw)
