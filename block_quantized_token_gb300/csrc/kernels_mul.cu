@@ -33,13 +33,18 @@
 //               codes to fp16 hi and lo, to TMEM (A operands)
 //   the last 4  D to y: factors taken back, rows brought together through shared memory.  Tiles of up to 128 tokens take D into
 //               registers every MU_CHUNK steps (fp32 rows: the tensor cores cut sums off, so they add up two steps alone;
-//               four steps take 9 % less time at three times the error), wider ones keep D in TMEM.
+//               four steps take 9 % less time at three times the error), wider ones keep D in TMEM: all columns' products are added
+//               there, and 14336 columns' sums are off by some 2e-5 of their size in norm (fp16 results by 2.089e-4 in place of the
+//               rounding's 2.077e-4, bf16 results by no more than the rounding).
 //
-// What bounds it.  Many tokens: the tensor cores.  8192 bf16 tokens x 4096 x 14336 take 1037 us: the hi and lo products alone,
-// 1.92 PFLOP, run at 1.86 PFLOP/s, 0.98 of what a bf16 library product reaches (tensor pipe active 85 %; with adapters of five
-// requests 1121 us).  fp32 rows: three products, and a chunk's way through registers (500 x 4096 x 4096 78 us with adapters).
+// What bounds it.  Many tokens: the tensor cores.  8192 bf16 tokens x 4096 x 14336 take 1050 us, the hi and lo products alone,
+// 1.92 PFLOP, at 1.83 PFLOP/s, 0.95 of what a bf16 library product reaches (tensor pipe active 85 %); call after call, where the
+// power limit lowers the clock, 1130 us, 0.99 of the library's sustained rate.  With adapters of five requests 1150 and 1185 us.
+// fp32 rows: three products, and a chunk's way through registers (500 x 4096 x 4096 50 us; with adapters 80 us: shrinking
+// and expanding are 12 us each under a profiler, the product then has nine steps more).
 // Few tokens: each tcgen05.mma with A from TMEM costs some 80 clocks whatever its width, 8 (fp32: 12) of them a step: 0.41 us a
-// step of 64 x 128 weights on every SM, 61 fp16 tokens x 32000 x 4096 55 us (2.5 TB/s of W).
+// step of 64 x 128 weights on every SM, 61 fp16 tokens x 32000 x 4096 55 us (2.5 TB/s of W).  An adapters' step costs a tile 1 us, as
+// rows of B come straight from global memory (61 fp16 tokens x 11008 x 4096 Q4_0 27 us, with 2 such steps 34 us, with 14 46 us).
 #include <cuda_bf16.h>
 
 #include "gemv_core.cuh"
@@ -327,7 +332,10 @@ __global__ void __launch_bounds__(256) mul_prep_kernel(const T *x, long long str
 // pieces, 16 columns in A (rows of B_a, bf16) and in the operand (v of the tokens that have it, else 0).  v enters as bf16 pieces,
 // two (2^-17 of the adapter's share of a 16-bit result) or for fp32 three; B_a in fp16 as two pieces, exactly.  The last pieces
 // do not meet.  Four such entries are a step of 64 columns.  A tile with more kinds than MU_EXTRA steps hold, or with one whose B holds
-// what is no number (AdaptersView::wild), has none (nksteps -1).
+// what is no number (AdaptersView::wild), has none (nksteps -1), and its adapters are added row by row (mu_adapters): 15 steps take
+// 61 fp16 tokens x 11008 x 4096 46 us, row by row 59; 36 entries 500 fp32 tokens x 4096 x 4096 80 us and 169 (more than fit: 176
+// to 187).  With room for 32 steps 24 of them would take the first 53 us where 16 adapters of rank 32 now take 60, and calls of few
+// kinds 4 us more (512 bf16 tokens with five of rank 16: 60 to 64 us).
 struct MuKinds {
     int kind[256], start[256], total;  // of a tile's tokens: adapter, the first entry of the kind where this token is its first
     int entry_kind[4 * MU_EXTRA], entry_pair[4 * MU_EXTRA], entry_col[4 * MU_EXTRA];

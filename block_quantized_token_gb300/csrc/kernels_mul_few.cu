@@ -11,13 +11,13 @@
 // item), where warp t sums up token t's 32 rows, adds its adapter's share and writes them.  Columns that do not fit are cut into
 // slices, each with CTAs of its own; sums of slices go to scratch, and a kernel behind this one adds them in their order.
 //
-// What bounds it.  Up to 8 bf16 tokens HBM: 128256 x 4096 Q8_0 92 us, 6.1 TB/s, 0.90 of a copy's rate.  16 tokens (122 us) and
-// fp32 rows (172 us) the warps' own chains: four warps a scheduler, as many as 128 registers allow, issue 36 % of the time, tensor
+// What bounds it.  Up to 8 bf16 tokens HBM: 128256 x 4096 Q8_0 90 us, 6.2 TB/s, 0.92 of a copy's rate.  16 tokens (108 us) and
+// fp32 rows (173 us) the warps' own chains: four warps a scheduler, as many as 128 registers allow, issue 36 % of the time, tensor
 // pipe 20 and 31 %; waiting for loads, for fragments and for products follow one another.  Loads of two steps are on their way; the
 // third costs registers that the products miss (128256 x 4096 with 8 tokens 108 us).  What is further ahead is fetched into L2
 // (32000 x 4096 with 16 bf16 tokens 39 to 32 us).  Two or four pairs of row groups at a time, with half or a quarter of the
 // warps on each, gain nothing (fp32 176 to 183 us), nor do products of both groups of tokens in turn (+ 0 to 3 %).
-// Small matrices: the two kernels' way to each other, 3.3 us for one token x 576 x 576 and 6.7 us for 16 x 4096 x 4096 (2.7 TB/s).
+// Small matrices: the two kernels' way to each other, 3.1 us for one token x 576 x 576 and 6.4 us for 16 x 4096 x 4096 (2.8 TB/s).
 #include <cuda_bf16.h>
 
 #include "gemv_core.cuh"

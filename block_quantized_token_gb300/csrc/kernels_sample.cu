@@ -19,9 +19,9 @@
 //
 // What bounds it.  Rows are read once (512 x 128256 fp32: 263 MB, 39 us at a copy's rate).  Few rows: the cluster's meetings and the
 // first CTA's steps one after another: a row of 128256 with top-k and top-p 13 us, 16 rows with other parameters each 51 us (the
-// slowest, a flat row with top-p, takes the ranges twice), issue 20 %.  Many rows: 512 with top-k 40 and top-p 235 us; two CTAs an
+// slowest, a flat row with top-p, takes the ranges twice), issue 20 %.  Many rows: 512 with top-k and top-p 238 us; two CTAs an
 // SM, each a row's eighth, wait for one another (issue 28 %, barriers first among the stalls).  Temperature alone: masses, some 95
-// instructions each for what is within 2^-24 of the largest (128 x 128256 84 us, issue 61 %); half of them were the terms of a
+// instructions each for what is within 2^-24 of the largest (128 x 128256 91 us, issue 62 %); half of them were the terms of a
 // longer series before the table of 256.
 #include <cooperative_groups.h>
 
