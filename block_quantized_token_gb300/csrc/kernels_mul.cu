@@ -35,7 +35,7 @@
 //               registers every MU_CHUNK steps (fp32 rows: the tensor cores cut sums off, so they add up two steps alone;
 //               four steps take 9 % less time at three times the error), wider ones keep D in TMEM: all columns' products are added
 //               there, and 14336 columns' sums are off by some 2e-5 of their size in norm (fp16 results by 2.089e-4 in place of the
-//               rounding's 2.077e-4, bf16 results by no more than the rounding).
+//               rounding's 2.078e-4, bf16 results by no more than the rounding).
 //
 // What bounds it.  Many tokens: the tensor cores.  8192 bf16 tokens x 4096 x 14336 take 1050 us, the hi and lo products alone,
 // 1.92 PFLOP, at 1.83 PFLOP/s, 0.95 of what a bf16 library product reaches (tensor pipe active 85 %); call after call, where the
